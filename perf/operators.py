@@ -249,7 +249,7 @@ def _plan_plain(s):
     fits = (start[1:] <= T) & (L + new <= p * width)
     need = torch.where(fits & (new > 0), (L + new + p - 1) // p - have, torch.zeros_like(L))
     need_end = torch.cumsum(need, 0)
-    ok = fits & (need_end <= top)
+    ok = fits & ((need == 0) | (need_end <= top))  # who needs no page is never held up
     need = torch.where(ok, need, torch.zeros_like(need))
     count = torch.where(ok, new, torch.zeros_like(new))
     lens = torch.where(d < 0, kept, L + count)
