@@ -11,7 +11,7 @@ import ctypes
 import os
 import re
 import struct
-from ctypes import c_float, c_int32, c_size_t, c_void_p
+from ctypes import c_float, c_int32, c_int64, c_size_t, c_void_p
 
 import torch
 
@@ -20,7 +20,7 @@ from . import build as _build
 DSA_META_MINMAX, DSA_META_MEAN = 0, 1
 DSA_EMA_INIT, DSA_EMA_UPDATE = 0, 1
 DSA_PSA_NLEFT = 1
-DSA_STATUS_BAD_PAGE, DSA_STATUS_OVERFLOW, DSA_STATUS_TIMEOUT = 1, 2, 4
+DSA_STATUS_BAD_PAGE, DSA_STATUS_OVERFLOW, DSA_STATUS_TIMEOUT, DSA_STATUS_NO_PAGES = 1, 2, 4, 8
 RECORD_FLOATS = 132  # partial record: O[128], m, l, 0, 0
 
 HEADER = os.path.join(_build.ROOT, "include", "dsa.h")
@@ -52,6 +52,22 @@ class PrrStepArgs(ctypes.Structure):
         ("count", c_void_p), ("k", c_int32), ("next_idx", c_void_p), ("next_count", c_void_p),
         ("superset", c_int32), ("scale", c_float), ("out", c_void_p), ("m", c_void_p),
         ("l", c_void_p),
+    ]
+
+
+class Chunk(ctypes.Structure):
+    """Mirror of ``dsa_chunk``."""
+    _fields_ = [
+        ("start", c_void_p), ("count", c_void_p), ("row", c_void_p), ("pos", c_void_p),
+        ("slot", c_void_p), ("tokens", c_int32),
+    ]
+
+
+class Rotary(ctypes.Structure):
+    """Mirror of ``dsa_rotary``."""
+    _fields_ = [
+        ("phase", c_void_p), ("axis", c_void_p), ("positions", c_void_p), ("num_axes", c_int32),
+        ("rot_dim", c_int32), ("interleaved", c_int32),
     ]
 
 
@@ -96,6 +112,12 @@ _SIGNATURES = {
     "dsa_prr_step": ([_P, _P, _P, c_size_t, _P], _I),
     "dsa_prr_step_workspace_size": ([_P], c_size_t),
     "dsa_prr_step_counter_bytes": ([_P], c_size_t),
+    "dsa_plan_chunk": ([_P, _P, _P, _P, _I, _P, _P, _P, _P, c_size_t, _P], _I),
+    "dsa_plan_chunk_workspace_size": ([_I], c_size_t),
+    "dsa_append_chunk": ([_P, _P, _P, c_int64, _P, c_int64, _P, _P, c_int64, _P, _I, _I, _P, _P],
+                         _I),
+    "dsa_chunk_attn": ([_P, _P, _P, _I, _I, c_float, _P, _P, _P, _P, c_size_t, _P], _I),
+    "dsa_chunk_attn_workspace_size": ([_P, _I], c_size_t),
 }
 
 _lib = None
@@ -451,3 +473,157 @@ def dsa_prr_step(kv: PagedKV, q, meta, scores, ell, trend, alpha: float, beta: f
     ws_bytes = workspace.numel() * workspace.element_size()
     _check("dsa_prr_step", load().dsa_prr_step(ctypes.byref(kv), ctypes.byref(a), _ptr(workspace),
                                                ws_bytes, _stream(stream)))
+
+
+# ------------------------------------------------------------------------------ chunks of tokens
+
+def _i32(t, shape, what: str, optional: bool = False):
+    """A contiguous int32 CUDA tensor of the given shape (or None), else a ValueError."""
+    if t is None and optional:
+        return None
+    if t.dtype != torch.int32 or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous int32 tensor of shape {tuple(shape)}, got "
+                         f"{t.dtype} {tuple(t.shape)}")
+    return _ptr(t)
+
+
+def page_tables(page_table, seq_lens, page_size: int, num_phys_pages: int, status=None) -> PagedKV:
+    """Descriptor of the page tables alone (no pools), for ``dsa_plan_chunk``."""
+    kv = PagedKV()
+    batch, width = page_table.shape
+    kv.page_table = _i32(page_table, (batch, width), "page_table")
+    kv.seq_lens = _i32(seq_lens, (batch,), "seq_lens")
+    kv.status = _ptr(status)
+    kv.batch, kv.max_pages_per_seq = batch, width
+    kv.num_q_heads = kv.num_kv_heads = 1
+    kv.head_dim, kv.page_size, kv.num_phys_pages = 128, page_size, num_phys_pages
+    kv.tensors = (page_table, seq_lens, status)  # kept alive with the descriptor
+    return kv
+
+
+def chunk(start, count, row=None, pos=None, slot=None, tokens: int | None = None) -> Chunk:
+    """Descriptor of a chunk: ``start`` int32 ``[B + 1]``, ``count`` int32 ``[B]``, ``row``, ``pos``
+    and ``slot`` int32 ``[tokens]`` (``slot`` may be None; ``row`` and ``pos`` too where only the
+    attention reads the chunk, with ``tokens`` given)."""
+    c = Chunk()
+    batch = count.shape[0]
+    n = tokens if tokens is not None else row.shape[0]
+    c.start = _i32(start, (batch + 1,), "start")
+    c.count = _i32(count, (batch,), "count")
+    c.row = _i32(row, (n,), "row", True)
+    c.pos = _i32(pos, (n,), "pos", True)
+    c.slot = _i32(slot, (n,), "slot", True)
+    c.tokens = n
+    c.batch = batch
+    c.tensors = (start, count, row, pos, slot)  # kept alive with the descriptor
+    return c
+
+
+def rotary_phases(inv_freq, device="cuda"):
+    """Frequencies (radians per position, any iterable of floats) as the turns per position in 0.64
+    fixed point that ``dsa_rotary`` takes: an int64 tensor holding the uint64 bit patterns."""
+    from fractions import Fraction
+    # 2 pi to 40 digits: the quotient is rounded once, to 2^-64 of a turn
+    two_pi = Fraction(62831853071795864769252867665590057683943, 10 ** 40)
+    bits = [round(Fraction(float(f)) / two_pi * 2 ** 64) % 2 ** 64 for f in inv_freq]
+    return torch.tensor([b - 2 ** 64 if b >= 2 ** 63 else b for b in bits], dtype=torch.int64,
+                        device=device)
+
+
+def rotary(phase, rot_dim: int, axis=None, positions=None, interleaved: bool = False) -> Rotary:
+    """Descriptor of rotary positions: ``phase`` from ``rotary_phases`` (``rot_dim / 2`` of them),
+    ``axis`` uint8 ``[rot_dim / 2]``, ``positions`` int32 ``[axes][tokens]`` (None: the chunk's)."""
+    if phase.dtype != torch.int64 or tuple(phase.shape) != (rot_dim // 2,):
+        raise ValueError(f"phase must be int64 [{rot_dim // 2}], got {phase.dtype} "
+                         f"{tuple(phase.shape)}")
+    if axis is not None and (axis.dtype != torch.uint8 or tuple(axis.shape) != (rot_dim // 2,)):
+        raise ValueError(f"axis must be uint8 [{rot_dim // 2}]")
+    phase = phase.contiguous()
+    r = Rotary()
+    r.phase, r.axis = _ptr(phase), _ptr(axis)
+    r.tensors = (phase, axis, positions)  # kept alive with the descriptor
+    r.num_axes = 1
+    r.tokens = None
+    if positions is not None:
+        axes, r.tokens = positions.shape
+        r.positions = _i32(positions, (axes, r.tokens), "positions")
+        r.num_axes = axes
+    r.rot_dim, r.interleaved = rot_dim, 1 if interleaved else 0
+    return r
+
+
+def dsa_plan_chunk_workspace_size(batch: int) -> int:
+    return int(load().dsa_plan_chunk_workspace_size(batch))
+
+
+def dsa_plan_chunk(kv: PagedKV, lens_in, delta, free_pages, free_in, free_out, chunk: Chunk,
+                   workspace, stream=None):
+    """Block tables, slot maps and the page stack of a step: writes ``kv``'s page table and lengths,
+    ``free_pages`` / ``free_out`` and the chunk's arrays.  ``lens_in`` may be the lengths' own tensor
+    and ``free_out`` may be ``free_in``."""
+    if chunk.batch != kv.batch:
+        raise ValueError(f"the chunk holds {chunk.batch} requests, the tables {kv.batch}")
+    _check("dsa_plan_chunk", load().dsa_plan_chunk(
+        ctypes.byref(kv), _i32(lens_in, (kv.batch,), "lens_in"),
+        _i32(delta, (kv.batch,), "delta"), _i32(free_pages, (free_pages.numel(),), "free_pages"),
+        free_pages.numel(), _i32(free_in, (1,), "free_in"), _i32(free_out, (1,), "free_out"),
+        ctypes.byref(chunk), _ptr(workspace), workspace.numel() * workspace.element_size(),
+        _stream(stream)))
+
+
+def _token_rows(t, tokens: int, heads: int, what: str) -> int:
+    """Token stride of bf16 ``[tokens][heads][128]`` whose heads are contiguous."""
+    if t.dtype != torch.bfloat16 or tuple(t.shape) != (tokens, heads, 128):
+        raise ValueError(f"{what} must be bf16 [{tokens}][{heads}][128], got {t.dtype} "
+                         f"{tuple(t.shape)}")
+    if tokens and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != 128)):
+        raise ValueError(f"{what}: the heads of a token must be contiguous")
+    return t.stride(0) if tokens > 1 else heads * 128
+
+
+def dsa_append_chunk(kv: PagedKV, chunk: Chunk, k_new, v_new, rotary: Rotary | None = None, q=None,
+                     q_out=None, meta_kind: int = 0, logical_page: int = 0, meta=None, stream=None):
+    """Turns the chunk's keys (and queries, into ``q_out``), writes keys and values into their pages
+    and renews the metadata of every touched page in ``meta`` (if given).  ``k_new``, ``v_new`` and
+    ``q`` are bf16 ``[tokens][heads][128]`` and may be slices of one projection."""
+    n = chunk.tokens
+    if chunk.batch != kv.batch:
+        raise ValueError(f"the chunk holds {chunk.batch} requests, the cache {kv.batch}")
+    if rotary is not None and rotary.tokens is not None and rotary.tokens != n:
+        raise ValueError(f"positions of {rotary.tokens} tokens for a chunk of {n}")
+    qs = 0
+    if q is not None:
+        qs = _token_rows(q, n, kv.num_q_heads, "q")
+        if _token_rows(q_out, n, kv.num_q_heads, "q_out") != kv.num_q_heads * 128:
+            raise ValueError("q_out must be contiguous")
+    _check("dsa_append_chunk", load().dsa_append_chunk(
+        ctypes.byref(kv), ctypes.byref(chunk), _ptr(k_new),
+        _token_rows(k_new, n, kv.num_kv_heads, "k_new"), _ptr(v_new),
+        _token_rows(v_new, n, kv.num_kv_heads, "v_new"),
+        None if rotary is None else ctypes.byref(rotary), _ptr(q), qs, _ptr(q_out), meta_kind,
+        logical_page, _ptr(meta), _stream(stream)))
+
+
+def dsa_chunk_attn_workspace_size(kv: PagedKV, tokens: int) -> int:
+    return int(load().dsa_chunk_attn_workspace_size(ctypes.byref(kv), tokens))
+
+
+def dsa_chunk_attn(kv: PagedKV, chunk: Chunk, q, scale: float, out, m=None, l=None, workspace=None,
+                   sink: int = 0, local: int = 0, stream=None):
+    """Attention of a chunk over the paged cache: causal on dense KV heads, sink + local window on
+    those marked streaming.  ``q`` and ``out`` bf16 ``[tokens][Hq][128]``, ``m`` and ``l`` fp32
+    ``[tokens][Hq]`` or None."""
+    n, hq = chunk.tokens, kv.num_q_heads
+    if chunk.batch != kv.batch:
+        raise ValueError(f"the chunk holds {chunk.batch} requests, the cache {kv.batch}")
+    for t, what in ((q, "q"), (out, "out")):
+        if _token_rows(t, n, hq, what) != hq * 128:
+            raise ValueError(f"{what} must be contiguous")
+    for t, what in ((m, "m"), (l, "l")):
+        if t is not None and (t.dtype != torch.float32 or tuple(t.shape) != (n, hq)
+                              or not t.is_contiguous()):
+            raise ValueError(f"{what} must be contiguous fp32 [{n}][{hq}]")
+    _check("dsa_chunk_attn", load().dsa_chunk_attn(
+        ctypes.byref(kv), ctypes.byref(chunk), _ptr(q), sink, local, scale, _ptr(out), _ptr(m),
+        _ptr(l), _ptr(workspace),
+        0 if workspace is None else workspace.numel() * workspace.element_size(), _stream(stream)))

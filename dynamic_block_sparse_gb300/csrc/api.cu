@@ -2,6 +2,7 @@
 // chooses split counts and launches the kernels on the caller's stream.  Allocates nothing.
 #include <cudaTypedefs.h>
 
+#include <cfloat>
 #include <cstdarg>
 #include <cstdio>
 #include <mutex>
@@ -960,6 +961,183 @@ int dsa_prr_step(const dsa_paged_kv* kv, const dsa_prr_step_args* args, void* wo
   a.l = x.l;
   const cudaError_t e = launch_prr_step(tk, tv, a, workspace, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? ok() : cuda_fail(e, "dsa_prr_step launch");
+}
+
+// ------------------------------------------------------------------------------ chunks of tokens
+
+size_t dsa_plan_chunk_workspace_size(int32_t batch) { return batch > 0 ? 16 : 0; }
+
+int dsa_plan_chunk(const dsa_paged_kv* kv, const int32_t* lens_in, const int32_t* delta,
+                   int32_t* free_pages, int32_t free_capacity, const int32_t* free_in,
+                   int32_t* free_out, const dsa_chunk* chunk, void* workspace,
+                   size_t workspace_bytes, dsa_stream_t stream) {
+  KvView v;
+  int rc = check_kv(kv, 0, &v);
+  if (rc) return rc;
+  if (!chunk) return fail(DSA_ERR_INVALID_ARG, "chunk is NULL");
+  if (chunk->tokens < 0 || free_capacity < 0)
+    return fail(DSA_ERR_INVALID_ARG, "negative tokens or free_capacity");
+  if (!lens_in || !delta || !free_in || !free_out || !chunk->start || !chunk->count ||
+      (free_capacity > 0 && !free_pages) ||
+      (chunk->tokens > 0 && (!chunk->row || !chunk->pos)))
+    return fail(DSA_ERR_INVALID_ARG, "dsa_plan_chunk: NULL pointer");
+  if (v.B > kPlanMaxBatch)
+    return fail(DSA_ERR_UNSUPPORTED, "batch %d > %d", v.B, kPlanMaxBatch);
+  if (static_cast<long long>(v.B) * v.max_pages >= (1LL << 31) ||
+      static_cast<long long>(v.p) * v.max_pages >= (1LL << 31))
+    return fail(DSA_ERR_UNSUPPORTED, "page table of %d x %d entries is too large", v.B, v.max_pages);
+  if (!workspace || workspace_bytes < dsa_plan_chunk_workspace_size(v.B))
+    return fail(DSA_ERR_WORKSPACE, "dsa_plan_chunk: workspace too small");
+  if (!aligned(workspace, 16)) return fail(DSA_ERR_ALIGNMENT, "workspace must be 16-byte aligned");
+  PlanArgs a;
+  a.B = v.B;
+  a.p = v.p;
+  a.max_pages = v.max_pages;
+  a.num_phys = v.num_phys;
+  // the table and the lengths are the caller's, written here
+  a.page_table = const_cast<int32_t*>(kv->page_table);
+  a.lens_in = lens_in;
+  a.lens_out = const_cast<int32_t*>(kv->seq_lens);
+  a.delta = delta;
+  a.free_pages = free_pages;
+  a.free_capacity = free_capacity;
+  a.free_in = free_in;
+  a.free_out = free_out;
+  a.start = chunk->start;
+  a.count = chunk->count;
+  a.row = chunk->row;
+  a.pos = chunk->pos;
+  a.slot = chunk->slot;
+  a.tokens = chunk->tokens;
+  a.ticket = static_cast<int32_t*>(workspace);
+  a.status = v.status;
+  cudaError_t e = launch_plan_chunk(a, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? ok() : cuda_fail(e, "dsa_plan_chunk launch");
+}
+
+int dsa_append_chunk(const dsa_paged_kv* kv, const dsa_chunk* chunk, const void* k_new,
+                     int64_t k_stride, const void* v_new, int64_t v_stride,
+                     const dsa_rotary* rotary, const void* q, int64_t q_stride, void* q_out,
+                     int32_t meta_kind, int32_t logical_page, void* meta, dsa_stream_t stream) {
+  KvView v;
+  int rc = check_kv(kv, 2, &v);
+  if (rc) return rc;
+  if (!chunk) return fail(DSA_ERR_INVALID_ARG, "chunk is NULL");
+  if (chunk->tokens < 0) return fail(DSA_ERR_INVALID_ARG, "negative tokens");
+  if (chunk->tokens == 0) return ok();
+  if (!chunk->start || !chunk->count || !chunk->row || !chunk->pos || !k_new || !v_new)
+    return fail(DSA_ERR_INVALID_ARG, "dsa_append_chunk: NULL pointer");
+  if (!aligned(k_new, 16) || !aligned(v_new, 16))
+    return fail(DSA_ERR_ALIGNMENT, "k_new/v_new must be 16-byte aligned");
+  const int64_t kv_row = static_cast<int64_t>(v.Hkv) * kHeadDim;
+  if (k_stride < kv_row || v_stride < kv_row || k_stride % 8 != 0 || v_stride % 8 != 0)
+    return fail(DSA_ERR_INVALID_ARG, "k/v token strides must be >= Hkv * 128 and multiples of 8");
+  if ((q != nullptr) != (q_out != nullptr))
+    return fail(DSA_ERR_INVALID_ARG, "q and q_out go together");
+  if (q) {
+    const int64_t q_row = static_cast<int64_t>(v.Hq) * kHeadDim;
+    if (!aligned(q, 16) || !aligned(q_out, 16))
+      return fail(DSA_ERR_ALIGNMENT, "q/q_out must be 16-byte aligned");
+    if (q_stride < q_row || q_stride % 8 != 0)
+      return fail(DSA_ERR_INVALID_ARG, "q token stride must be >= Hq * 128 and a multiple of 8");
+    if (q == q_out && q_stride != q_row)
+      return fail(DSA_ERR_INVALID_ARG, "q_out may be q only when q is contiguous");
+  }
+  if (rotary) {
+    if (!rotary->phase) return fail(DSA_ERR_INVALID_ARG, "rotary phase is NULL");
+    if (rotary->rot_dim < 16 || rotary->rot_dim > kHeadDim || rotary->rot_dim % 16 != 0)
+      return fail(DSA_ERR_UNSUPPORTED, "rot_dim %d must be a multiple of 16 in [16, 128]",
+                  rotary->rot_dim);
+    if (rotary->num_axes < 1 || rotary->num_axes > 4)
+      return fail(DSA_ERR_UNSUPPORTED, "num_axes %d must be in [1, 4]", rotary->num_axes);
+    if (rotary->num_axes > 1 && (!rotary->axis || !rotary->positions))
+      return fail(DSA_ERR_INVALID_ARG, "several axes need axis and positions");
+    if (!aligned(rotary->phase, 8)) return fail(DSA_ERR_ALIGNMENT, "phase must be 8-byte aligned");
+  }
+  if (meta) {
+    if (meta_kind != DSA_META_MINMAX && meta_kind != DSA_META_MEAN)
+      return fail(DSA_ERR_INVALID_ARG, "unknown meta_kind %d", meta_kind);
+    if (logical_page <= 0 || v.p % logical_page != 0)
+      return fail(DSA_ERR_INVALID_ARG, "logical_page %d must divide page_size %d", logical_page,
+                  v.p);
+    if (!aligned(meta, 16)) return fail(DSA_ERR_ALIGNMENT, "meta must be 16-byte aligned");
+  }
+  AppendArgs a = {};
+  a.kv = v;
+  a.k_pages = static_cast<__nv_bfloat16*>(const_cast<void*>(kv->k_pages));
+  a.v_pages = static_cast<__nv_bfloat16*>(const_cast<void*>(kv->v_pages));
+  a.start = chunk->start;
+  a.count = chunk->count;
+  a.row = chunk->row;
+  a.pos = chunk->pos;
+  a.tokens = chunk->tokens;
+  a.k = static_cast<const __nv_bfloat16*>(k_new);
+  a.v = static_cast<const __nv_bfloat16*>(v_new);
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.q = static_cast<const __nv_bfloat16*>(q);
+  a.q_stride = q_stride;
+  a.q_out = static_cast<__nv_bfloat16*>(q_out);
+  if (rotary) {
+    a.phase = reinterpret_cast<const unsigned long long*>(rotary->phase);
+    a.axis = rotary->axis;
+    a.positions = rotary->positions;
+    a.num_axes = rotary->num_axes;
+    a.rot_dim = rotary->rot_dim;
+    a.interleaved = rotary->interleaved != 0;
+  }
+  a.lp = meta ? logical_page : v.p;
+  a.meta = meta;
+  cudaError_t e = launch_append_chunk(a, meta_kind, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? ok() : cuda_fail(e, "dsa_append_chunk launch");
+}
+
+size_t dsa_chunk_attn_workspace_size(const dsa_paged_kv* kv, int32_t tokens) {
+  KvView v;
+  if (check_kv(kv, 0, &v) || tokens <= 0) return 0;
+  return 16;
+}
+
+int dsa_chunk_attn(const dsa_paged_kv* kv, const dsa_chunk* chunk, const void* q,
+                   int32_t sink_tokens, int32_t local_tokens, float scale, void* out, float* m,
+                   float* l, void* workspace, size_t workspace_bytes, dsa_stream_t stream) {
+  KvView v;
+  int rc = check_kv(kv, 2, &v);
+  if (rc) return rc;
+  if (!chunk) return fail(DSA_ERR_INVALID_ARG, "chunk is NULL");
+  if (chunk->tokens < 0) return fail(DSA_ERR_INVALID_ARG, "negative tokens");
+  if (chunk->tokens == 0) return ok();
+  if (!chunk->start || !chunk->count || !q || !out)
+    return fail(DSA_ERR_INVALID_ARG, "dsa_chunk_attn: NULL pointer");
+  if (!aligned(q, 16) || !aligned(out, 16))
+    return fail(DSA_ERR_ALIGNMENT, "q and out must be 16-byte aligned");
+  if (sink_tokens < 0 || local_tokens < 0)
+    return fail(DSA_ERR_INVALID_ARG, "negative sink or local tokens");
+  const float sl = scale_log2(scale);
+  if (!(sl >= FLT_MIN && sl <= FLT_MAX))
+    return fail(DSA_ERR_INVALID_ARG, "scale must be positive and finite");
+  if (static_cast<long long>(v.p) * v.max_pages >= (1LL << 31))
+    return fail(DSA_ERR_UNSUPPORTED, "%d pages of %d tokens per request exceed 2^31 tokens",
+                v.max_pages, v.p);
+  if (!workspace || workspace_bytes < dsa_chunk_attn_workspace_size(kv, chunk->tokens))
+    return fail(DSA_ERR_WORKSPACE, "dsa_chunk_attn: workspace too small");
+  if (!aligned(workspace, 16)) return fail(DSA_ERR_ALIGNMENT, "workspace must be 16-byte aligned");
+  ChunkAttnArgs a = {};
+  a.kv = v;
+  a.k_pages = static_cast<const __nv_bfloat16*>(kv->k_pages);
+  a.v_pages = static_cast<const __nv_bfloat16*>(kv->v_pages);
+  a.start = chunk->start;
+  a.count = chunk->count;
+  a.tokens = chunk->tokens;
+  a.q = static_cast<const __nv_bfloat16*>(q);
+  a.sink = sink_tokens;
+  a.local = local_tokens;
+  a.scale_log2 = sl;
+  a.out = static_cast<__nv_bfloat16*>(out);
+  a.m = m;
+  a.l = l;
+  cudaError_t e = launch_chunk_attn(a, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? ok() : cuda_fail(e, "dsa_chunk_attn launch");
 }
 
 }  // extern "C"

@@ -1,0 +1,411 @@
+// A chunk of new tokens enters the paged cache: the page plan (block tables, slot maps, the page
+// stack) and the rotary append (q and k rotated, K and V into their pages, page metadata).
+#include "common.cuh"
+#include "internal.h"
+#include "meta_core.cuh"
+
+namespace dsa {
+namespace {
+
+// ---------------------------------------------------------------------------------------- plan
+// Three prefix sums over the requests decide everything: start (new tokens), gone (pages given
+// back) and need (pages taken).  Every CTA makes them for itself from the 8 bytes per request (B is
+// small against what follows, and no CTA then waits for another), keeps them in shared memory and
+// expands its share of the tokens, of the taken pages and of the returned pages, each with a binary
+// search.  Lengths and stack height may be updated in place, so they are written by the CTA that
+// takes the last ticket, when every other CTA has read them.
+constexpr int kPlanThreads = 512;
+constexpr int kPlanTokens = 2 * kPlanThreads;  // tokens per CTA
+
+struct Sums {
+  long long start, gone, need;
+};
+
+DSA_DEV Sums shfl_up(const Sums& s, int o) {
+  return {__shfl_up_sync(0xffffffffu, s.start, o), __shfl_up_sync(0xffffffffu, s.gone, o),
+          __shfl_up_sync(0xffffffffu, s.need, o)};
+}
+DSA_DEV Sums operator+(const Sums& a, const Sums& b) {
+  return {a.start + b.start, a.gone + b.gone, a.need + b.need};
+}
+
+DSA_DEV int clamp_i32(long long v) {
+  return static_cast<int>(v < 0x7fffffffLL ? v : 0x7fffffffLL);
+}
+
+// First index i with end[i] > v (end non-decreasing); n when there is none.
+DSA_DEV int first_above(const int* end, int n, int v) {
+  int lo = 0, hi = n;
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (end[mid] > v)
+      hi = mid;
+    else
+      lo = mid + 1;
+  }
+  return lo;
+}
+
+struct PlanLen {
+  int len, delta, have, keep;  // clamped length, change, pages held, pages kept (delta < 0)
+};
+
+DSA_DEV PlanLen plan_len(const PlanArgs& a, int b) {
+  PlanLen r;
+  r.len = min(max(a.lens_in[b], 0), a.p * a.max_pages);
+  r.delta = a.delta[b];
+  r.have = (r.len + a.p - 1) / a.p;
+  r.keep = r.have;
+  if (r.delta < 0) {
+    const long long left = static_cast<long long>(r.len) + r.delta;
+    r.keep = left > 0 ? static_cast<int>((left + a.p - 1) / a.p) : 0;
+  }
+  return r;
+}
+
+__global__ void __launch_bounds__(kPlanThreads) plan_chunk_kernel(const PlanArgs a) {
+  launch_dependents();
+  extern __shared__ int sm[];
+  int* s_start = sm;                // [B]: first token of each request
+  int* s_start_end = sm + a.B;      // [B]: one past its last token
+  int* s_gone = sm + 2 * a.B;       // [B]: pages given back by requests 0..b
+  int* s_need = sm + 3 * a.B;       // [B]: pages needed by requests 0..b
+  int* s_count = sm + 4 * a.B;      // [B]: new tokens wanted, 0 when the request cannot hold them
+  __shared__ Sums s_warp[kPlanThreads / 32];
+  __shared__ int s_taken, s_last;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid == 0) s_taken = 0;
+  grid_dependency_wait();
+
+  Sums carry = {0, 0, 0};
+  for (int b0 = 0; b0 < a.B; b0 += kPlanThreads) {
+    const int b = b0 + tid;
+    PlanLen r = {0, 0, 0, 0};
+    if (b < a.B) r = plan_len(a, b);
+    Sums own = {max(r.delta, 0), r.have - r.keep, 0};
+    Sums inc = own;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const Sums up = shfl_up(inc, o);
+      if (lane >= o) inc = inc + up;
+    }
+    if (lane == 31) s_warp[warp] = inc;
+    __syncthreads();
+    Sums base = carry;
+    for (int w = 0; w < warp; ++w) base = base + s_warp[w];
+    for (int w = 0; w < kPlanThreads / 32; ++w) carry = carry + s_warp[w];
+    inc = base + inc;
+    // a request takes part when its tokens lie inside the chunk and its table row can hold them
+    const long long grown = static_cast<long long>(r.len) + own.start;
+    const bool fits = inc.start <= a.tokens && grown <= static_cast<long long>(a.p) * a.max_pages;
+    const int need =
+        fits && own.start > 0 ? static_cast<int>((grown + a.p - 1) / a.p) - r.have : 0;
+    Sums nd = {0, 0, need};
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long up = __shfl_up_sync(0xffffffffu, nd.need, o);
+      if (lane >= o) nd.need += up;
+    }
+    __syncthreads();
+    if (lane == 31) s_warp[warp].need = nd.need;
+    __syncthreads();
+    long long need_base = carry.need, need_total = 0;
+    for (int w = 0; w < kPlanThreads / 32; ++w) {
+      if (w < warp) need_base += s_warp[w].need;
+      need_total += s_warp[w].need;
+    }
+    if (b < a.B) {
+      s_start[b] = clamp_i32(inc.start - own.start);
+      s_start_end[b] = clamp_i32(inc.start);
+      s_gone[b] = clamp_i32(inc.gone);
+      s_need[b] = clamp_i32(need_base + nd.need);
+      s_count[b] = fits ? max(r.delta, 0) : 0;
+    }
+    carry.need += need_total;
+    __syncthreads();
+  }
+
+  const int cap = a.free_capacity;
+  const int held = min(max(a.free_in[0], 0), cap);  // pages on the stack
+  const int gone = s_gone[a.B - 1];
+  const int top = clamp_i32(static_cast<long long>(held) + gone);
+  // Admission: a request that needs pages gets them when those of all requests up to it fit; one
+  // that needs none is always admitted.  s_need never falls, so the pages taken are its last value
+  // that fits.
+  bool refused = false;
+  for (int b = tid; b < a.B; b += kPlanThreads) {
+    const int end = s_need[b], before = b > 0 ? s_need[b - 1] : 0;
+    if (end <= top) atomicMax(&s_taken, end);
+    if (end > before && end > top) s_count[b] = 0;
+    if (s_count[b] == 0 && s_start_end[b] > s_start[b]) refused = true;
+  }
+  if (__syncthreads_or(refused) && tid == 0 && blockIdx.x == 0)
+    raise_status(a.status, DSA_STATUS_NO_PAGES);
+  const int taken = s_taken;
+  int left = top - taken;
+  if (left > cap) {
+    left = cap;
+    if (tid == 0 && blockIdx.x == 0) raise_status(a.status, DSA_STATUS_OVERFLOW);
+  }
+
+  // i-th page given back in this call, in request then position order
+  auto returned = [&](int i) {
+    const int b = first_above(s_gone, a.B, i);
+    const PlanLen r = plan_len(a, b);
+    const int j = r.keep + i - (b > 0 ? s_gone[b - 1] : 0);
+    return a.page_table[static_cast<size_t>(b) * a.max_pages + j];
+  };
+  // k-th page taken in this call: from the top of the stack, returned pages included
+  auto page_taken = [&](int k) {
+    const int s = top - 1 - k;
+    return s < held ? a.free_pages[s] : returned(s - held);
+  };
+
+  const int first = blockIdx.x * kPlanThreads + tid, step = gridDim.x * kPlanThreads;
+  for (int t = first; t < a.tokens; t += step) {
+    const int b = first_above(s_start_end, a.B, t);
+    int row = -1, pos = -1, slot = -1;
+    if (b < a.B && s_count[b] > 0) {
+      const int len = min(max(a.lens_in[b], 0), a.p * a.max_pages);
+      const int have = (len + a.p - 1) / a.p;
+      row = b;
+      pos = len + (t - s_start[b]);
+      const int j = pos / a.p;
+      const int phys = j < have ? a.page_table[static_cast<size_t>(b) * a.max_pages + j]
+                                : page_taken((b > 0 ? s_need[b - 1] : 0) + j - have);
+      if (phys >= 0 && phys < a.num_phys)
+        slot = phys * a.p + pos % a.p;
+      else
+        raise_status(a.status, DSA_STATUS_BAD_PAGE);
+    }
+    a.row[t] = row;
+    a.pos[t] = pos;
+    if (a.slot) a.slot[t] = slot;
+  }
+  for (int k = first; k < taken; k += step) {
+    const int b = first_above(s_need, a.B, k);
+    const PlanLen r = plan_len(a, b);
+    a.page_table[static_cast<size_t>(b) * a.max_pages + r.have + k - (b > 0 ? s_need[b - 1] : 0)] =
+        page_taken(k);
+  }
+  for (int s = held + first; s < left; s += step) a.free_pages[s] = returned(s - held);
+
+  if (gridDim.x > 1) {
+    __syncthreads();
+    if (tid == 0) {
+      __threadfence();
+      s_last = atomicAdd(a.ticket, 1) == static_cast<int>(gridDim.x) - 1;
+    }
+    __syncthreads();
+    if (!s_last) return;
+    if (tid == 0) *a.ticket = 0;
+  } else {
+    __syncthreads();
+  }
+  for (int b = tid; b < a.B; b += kPlanThreads) {
+    const PlanLen r = plan_len(a, b);
+    a.start[b] = s_start[b];
+    a.count[b] = s_count[b];
+    a.lens_out[b] = r.delta < 0 ? static_cast<int>(max(static_cast<long long>(r.len) + r.delta, 0LL))
+                                : r.len + s_count[b];
+  }
+  if (tid == 0) {
+    a.start[a.B] = s_start_end[a.B - 1];
+    a.free_out[0] = left;
+  }
+}
+
+// -------------------------------------------------------------------------------------- append
+// Work is cut at logical-page boundaries so that one CTA writes every new key of the metadata
+// records it makes: a "run" is the new tokens of one request inside one unit of `unit` positions (a
+// multiple of the logical page, at least 16 tokens where the page allows it).  CTA (x, y) takes the
+// runs whose first token lies in [16 x, 16 x + 16) of the chunk, for its group of KV heads and their
+// query heads.  The sines of a token are worked out once per CTA and shared by its heads.
+constexpr int kAppThreads = 256;
+constexpr int kAppTokens = 16;
+
+DSA_DEV void rotate8(const uint4& xa, const uint4& xb, const float2* cs, uint4& ya, uint4& yb) {
+  const __nv_bfloat16* a = reinterpret_cast<const __nv_bfloat16*>(&xa);
+  const __nv_bfloat16* b = reinterpret_cast<const __nv_bfloat16*>(&xb);
+  uint32_t* oa = reinterpret_cast<uint32_t*>(&ya);
+  uint32_t* ob = reinterpret_cast<uint32_t*>(&yb);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float2 c0 = cs[2 * e], c1 = cs[2 * e + 1];
+    const float a0 = __bfloat162float(a[2 * e]), a1 = __bfloat162float(a[2 * e + 1]);
+    const float b0 = __bfloat162float(b[2 * e]), b1 = __bfloat162float(b[2 * e + 1]);
+    oa[e] = pack_bf16(a0 * c0.x - b0 * c0.y, a1 * c1.x - b1 * c1.y);
+    ob[e] = pack_bf16(b0 * c0.x + a0 * c0.y, b1 * c1.x + a1 * c1.y);
+  }
+}
+
+// 8 dims as four neighbouring pairs.
+DSA_DEV uint4 rotate_pairs(const uint4& x, const float2* cs) {
+  const __nv_bfloat16* v = reinterpret_cast<const __nv_bfloat16*>(&x);
+  uint4 y;
+  uint32_t* o = reinterpret_cast<uint32_t*>(&y);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float a = __bfloat162float(v[2 * e]), b = __bfloat162float(v[2 * e + 1]);
+    o[e] = pack_bf16(a * cs[e].x - b * cs[e].y, b * cs[e].x + a * cs[e].y);
+  }
+  return y;
+}
+
+template <int KIND>
+__global__ void __launch_bounds__(kAppThreads) append_chunk_kernel(const AppendArgs a) {
+  launch_dependents();
+  __shared__ float2 s_cs[kAppTokens][kHeadDim / 2];
+  grid_dependency_wait();
+  const KvView& kv = a.kv;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int h0 = blockIdx.y * a.heads_per_cta;
+  const int nh = min(a.heads_per_cta, kv.Hkv - h0);
+  const int G = kv.G, half = a.rot_dim / 2;
+  const int t0 = blockIdx.x * kAppTokens, t1 = min(t0 + kAppTokens, a.tokens);
+
+  for (int lead = t0; lead < t1; ++lead) {
+    // (uniform over the CTA: every thread reads the same words)
+    const int b = a.row[lead];
+    if (b < 0 || b >= kv.B) continue;
+    const int first = a.start[b], n_new = a.count[b];
+    const int pos = a.pos[lead];
+    const bool head_run = lead == first;
+    if (lead < first || lead - first >= n_new || (!head_run && pos % a.unit != 0)) continue;
+    const int n = min(min(a.unit - pos % a.unit, first + n_new - lead), a.tokens - lead);
+    const int L = request_len(kv, b);
+    const int j = pos / kv.p;
+    int phys = -1;
+    if (pos >= 0 && j < kv.max_pages)
+      phys = kv.page_table[static_cast<size_t>(b) * kv.max_pages + j];
+    const bool ok = phys >= 0 && phys < kv.num_phys;
+    if (!ok && tid == 0) raise_status(kv.status, DSA_STATUS_BAD_PAGE);
+
+    for (int c0 = 0; c0 < n; c0 += kAppTokens) {
+      const int nt = min(kAppTokens, n - c0);
+      if (a.phase) {
+        __syncthreads();
+        for (int i = tid; i < nt * half; i += kAppThreads) {
+          const int tt = i / half, pr = i - tt * half;
+          const int t = lead + c0 + tt;
+          const int ax = a.axis ? min(static_cast<int>(a.axis[pr]), a.num_axes - 1) : 0;
+          const long long where =
+              a.positions ? a.positions[static_cast<size_t>(ax) * a.tokens + t] : pos + c0 + tt;
+          // position x phase modulo one turn, exact in 64-bit integers whatever the position; the
+          // top 32 bits are the signed fraction of a turn
+          const unsigned long long turn = static_cast<unsigned long long>(where) * a.phase[pr];
+          const float x = static_cast<float>(static_cast<int>(turn >> 32)) * 4.656612873077393e-10f;
+          float sn, cs;
+          sincospif(x, &sn, &cs);
+          s_cs[tt][pr] = make_float2(cs, sn);
+        }
+        __syncthreads();
+      }
+      // rows of a token: its query heads (with rotation), its keys, its values; 8 threads a row,
+      // two 16-byte pieces each
+      const int nq = a.q ? nh * G : 0;
+      const int rows = nq + 2 * nh;
+      for (int i = tid; i < nt * rows * 8; i += kAppThreads) {
+        const int e = i & 7, rr = (i >> 3) % rows, tt = (i >> 3) / rows;
+        const int t = lead + c0 + tt;
+        const __nv_bfloat16* src;
+        __nv_bfloat16* dst;
+        bool turn = a.phase != nullptr;
+        if (rr < nq) {
+          const int hq = h0 * G + rr;
+          src = a.q + static_cast<size_t>(t) * a.q_stride + hq * kHeadDim;
+          dst = a.q_out + (static_cast<size_t>(t) * kv.Hq + hq) * kHeadDim;
+        } else {
+          const bool is_v = rr - nq >= nh;
+          const int h = h0 + (is_v ? rr - nq - nh : rr - nq);
+          if (!ok) continue;
+          const size_t at = ((static_cast<size_t>(phys) * kv.Hkv + h) * kv.p + (pos + c0 + tt) % kv.p) *
+                            kHeadDim;
+          src = is_v ? a.v + static_cast<size_t>(t) * a.v_stride + h * kHeadDim
+                     : a.k + static_cast<size_t>(t) * a.k_stride + h * kHeadDim;
+          dst = (is_v ? a.v_pages : a.k_pages) + at;
+          if (is_v) turn = false;
+        }
+        const int hp = half / 8;  // 16-byte pieces of half a rotated row
+        int ca, cb;               // this thread's two pieces
+        if (!turn || a.interleaved) {
+          ca = 2 * e;
+          cb = 2 * e + 1;
+        } else if (e < hp) {
+          ca = e;
+          cb = e + hp;
+        } else {
+          ca = 2 * e;  // 2 hp + 2 (e - hp): the pieces behind the rotated ones
+          cb = 2 * e + 1;
+        }
+        uint4 xa = *reinterpret_cast<const uint4*>(src + ca * 8);
+        uint4 xb = *reinterpret_cast<const uint4*>(src + cb * 8);
+        if (turn) {
+          if (a.interleaved) {
+            if (ca < 2 * hp) xa = rotate_pairs(xa, &s_cs[tt][ca * 4]);
+            if (cb < 2 * hp) xb = rotate_pairs(xb, &s_cs[tt][cb * 4]);
+          } else if (e < hp) {
+            uint4 ya, yb;
+            rotate8(xa, xb, &s_cs[tt][ca * 8], ya, yb);
+            xa = ya;
+            xb = yb;
+          }
+        }
+        *reinterpret_cast<uint4*>(dst + ca * 8) = xa;
+        *reinterpret_cast<uint4*>(dst + cb * 8) = xb;
+      }
+    }
+    if (a.meta != nullptr && ok) {
+      // records of the run's unit; the request's first run also renews those before it in its page,
+      // its last run writes those behind it (no valid token: zeros), as the build does
+      const int g = kv.p / a.lp;
+      const int u0 = (pos % kv.p) / a.unit * a.unit;
+      const int sub0 = head_run ? 0 : u0 / a.lp;
+      const bool last_run = lead + n == first + n_new || pos / kv.p != (pos + n) / kv.p;
+      const int sub1 = last_run ? g : (u0 + a.unit) / a.lp;
+      __threadfence_block();
+      __syncthreads();
+      for (int i = warp; i < nh * (sub1 - sub0); i += kAppThreads / 32) {
+        const int h = h0 + i / (sub1 - sub0), sub = sub0 + i % (sub1 - sub0);
+        page_meta<KIND, true>(kv, a.k_pages, a.lp, a.meta, j, h, phys, L, lane, sub, sub + 1);
+      }
+    }
+  }
+}
+
+}  // namespace
+
+size_t plan_smem_bytes(int B) { return static_cast<size_t>(B) * 5 * sizeof(int); }
+
+cudaError_t launch_plan_chunk(const PlanArgs& a, cudaStream_t s) {
+  const size_t bytes = plan_smem_bytes(a.B);
+  cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(plan_chunk_kernel), bytes);
+  if (e != cudaSuccess) return e;
+  int grid = (a.tokens + kPlanTokens - 1) / kPlanTokens;
+  grid = grid < 1 ? 1 : grid > 152 ? 152 : grid;
+  return launch_pdl(plan_chunk_kernel, grid, kPlanThreads, bytes, s, a);
+}
+
+cudaError_t launch_append_chunk(const AppendArgs& in, int kind, cudaStream_t s) {
+  AppendArgs a = in;
+  if (a.tokens <= 0) return cudaSuccess;
+  // the smallest multiple of the logical page that divides the page and holds 16 tokens
+  a.unit = a.kv.p;
+  for (int m = a.lp; m < a.kv.p; m += a.lp)
+    if (m >= kAppTokens && a.kv.p % m == 0) {
+      a.unit = m;
+      break;
+    }
+  const int gx = (a.tokens + kAppTokens - 1) / kAppTokens;
+  // KV heads of one CTA: all of them share the CTA's sines, but a short chunk needs the CTAs
+  int hpc = a.kv.Hkv;
+  while (hpc > 1 && static_cast<long long>(gx) * ((a.kv.Hkv + hpc - 1) / hpc) < 8 * 152)
+    hpc = (hpc + 1) / 2;
+  a.heads_per_cta = hpc;
+  dim3 grid(gx, (a.kv.Hkv + hpc - 1) / hpc);
+  return kind == DSA_META_MINMAX
+             ? launch_pdl(append_chunk_kernel<DSA_META_MINMAX>, grid, kAppThreads, 0, s, a)
+             : launch_pdl(append_chunk_kernel<DSA_META_MEAN>, grid, kAppThreads, 0, s, a);
+}
+
+}  // namespace dsa

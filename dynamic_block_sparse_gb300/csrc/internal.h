@@ -222,6 +222,72 @@ CalibWorkspace calib_workspace(int T, int rows, int n, int k);
 cudaError_t launch_calib(const float* traj, int T, int rows, int n, int stride, int k, int k_pred,
                          float* H, int32_t* best, void* workspace, cudaStream_t s);
 
+// Page plan of a chunk of new tokens (chunk.cu).
+constexpr int kPlanMaxBatch = 8192;  // requests whose prefix sums one CTA keeps in shared memory
+struct PlanArgs {
+  int B, p, max_pages, num_phys;
+  int32_t* page_table;
+  const int32_t* lens_in;
+  int32_t* lens_out;
+  const int32_t* delta;
+  int32_t* free_pages;
+  int free_capacity;
+  const int32_t* free_in;
+  int32_t* free_out;
+  int32_t* start;
+  int32_t* count;
+  int32_t* row;
+  int32_t* pos;
+  int32_t* slot;  // may be null
+  int tokens;
+  int32_t* ticket;  // zero on entry, left zero
+  int32_t* status;
+};
+cudaError_t launch_plan_chunk(const PlanArgs& a, cudaStream_t s);
+
+// Rotary append of a chunk (chunk.cu).
+struct AppendArgs {
+  KvView kv;
+  __nv_bfloat16* k_pages;
+  __nv_bfloat16* v_pages;
+  const int32_t* start;
+  const int32_t* count;
+  const int32_t* row;
+  const int32_t* pos;
+  int tokens;
+  const __nv_bfloat16* k;
+  const __nv_bfloat16* v;
+  long long k_stride, v_stride;  // elements between tokens
+  const __nv_bfloat16* q;        // null: no queries to rotate
+  long long q_stride;
+  __nv_bfloat16* q_out;
+  const unsigned long long* phase;  // null: keys are written as they are
+  const uint8_t* axis;              // null: one axis
+  const int32_t* positions;         // null: chunk positions
+  int num_axes, rot_dim, interleaved;
+  int lp;
+  void* meta;  // may be null
+  int unit, heads_per_cta;  // set by the launch
+};
+cudaError_t launch_append_chunk(const AppendArgs& a, int kind, cudaStream_t s);
+
+// Attention of a chunk over the paged cache (chunk_attn.cu).
+struct ChunkAttnArgs {
+  KvView kv;
+  const __nv_bfloat16* k_pages;
+  const __nv_bfloat16* v_pages;
+  const int32_t* start;
+  const int32_t* count;
+  int tokens;
+  const __nv_bfloat16* q;
+  int sink, local;  // of streaming heads
+  float scale_log2;
+  __nv_bfloat16* out;
+  float* m;  // may be null
+  float* l;  // may be null
+};
+cudaError_t launch_chunk_attn(const ChunkAttnArgs& a, cudaStream_t s);
+
 struct ThresholdArgs {
   KvView kv;
   const __nv_bfloat16* q;

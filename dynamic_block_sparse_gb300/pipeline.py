@@ -3,6 +3,8 @@
 Every buffer a step needs is allocated once, when a decoder is built; a step only enqueues
 library kernels on the current CUDA stream (and, for PRR, on a second stream).
 
+* :class:`Chunk`            — prompts and pieces of prompts: page plan, rotary append and attention
+                              of many new tokens per request (``prefill`` of every decoder).
 * :class:`TopKDecoder`      — kmax/kmin page scores, fixed top-K, sparse attention.
 * :class:`HierDecoder`      — LServe: logical pages scored, max-reduced to physical pages,
                               top-K physical pages reused for ``reuse`` steps; streaming heads
@@ -102,6 +104,67 @@ class Cache:
         return o, m, l
 
 
+class Chunk:
+    """One step's new tokens of a cache, packed request after request on one token axis: the page plan,
+    the rotary append and the attention of prompts, pieces of prompts and single tokens alike.
+
+    The buffers hold up to ``tokens`` new tokens per step and are reused by every step, so a step can
+    be captured into a CUDA graph once and replayed for steps of fewer tokens.  ``free_pages`` (int32)
+    is the stack of the pool's free pages; without it the chunk's arrays are the caller's to fill.
+    """
+
+    def __init__(self, cache: Cache, tokens: int, free_pages=None):
+        c = cache
+        self.cache, self.tokens = c, tokens
+        i32 = dict(dtype=torch.int32, device=c.device)
+        self.start = torch.zeros(c.batch + 1, **i32)
+        self.count = torch.zeros(c.batch, **i32)
+        self.row, self.pos, self.slot = (torch.full((tokens,), -1, **i32) for _ in range(3))
+        self.chunk = B.chunk(self.start, self.count, self.row, self.pos, self.slot)
+        if free_pages is not None:
+            # every page of the pool can come back
+            self.free_pages = torch.full((max(c.num_phys_pages, free_pages.numel()),), -1, **i32)
+            self.free_pages[:free_pages.numel()] = free_pages
+            self.free_count = torch.full((1,), free_pages.numel(), **i32)
+        self.plan_workspace = torch.zeros(B.dsa_plan_chunk_workspace_size(c.batch),
+                                          dtype=torch.uint8, device=c.device)
+        self.q = torch.zeros((tokens, c.num_q_heads, c.head_dim), dtype=torch.bfloat16,
+                             device=c.device)
+        self.out = torch.zeros_like(self.q)
+        self.m, self.l = (torch.zeros((tokens, c.num_q_heads), dtype=torch.float32, device=c.device)
+                          for _ in range(2))
+        self.workspace = torch.zeros(max(16, B.dsa_chunk_attn_workspace_size(c.kv, tokens)),
+                                     dtype=torch.uint8, device=c.device)
+
+    def plan(self, delta, stream=None):
+        """Starts a step: ``delta[b]`` new tokens for request b (or -n: its last n tokens dropped),
+        with pages from the stack.  Advances the cache's lengths and page table and fills the chunk; a
+        request that does not fit gets ``count[b] = 0`` and raises DSA_STATUS_NO_PAGES."""
+        c = self.cache
+        B.dsa_plan_chunk(c.kv, c.seq_lens, delta, self.free_pages, self.free_count, self.free_count,
+                         self.chunk, self.plan_workspace, stream)
+
+    def append(self, k_new, v_new, metas=(), rotary=None, q=None, stream=None):
+        """Writes the chunk's keys and values (``[tokens][Hkv][D]``, turned by ``rotary``) into their
+        pages and renews the touched pages of every ``(kind, logical_page, meta)`` buffer; returns the
+        turned queries, if ``q`` is given."""
+        c = self.cache
+        for i, (kind, lp, meta) in enumerate(tuple(metas) or ((0, 0, None),)):
+            first = q is not None and i == 0
+            B.dsa_append_chunk(c.kv, self.chunk, k_new, v_new, rotary, q if first else None,
+                               self.q if first else None, kind, lp, meta, stream)
+        return self.q if q is not None else None
+
+    def attend(self, q, scale: float | None = None, sink: int = 0, local: int = 0, stream=None):
+        """Causal attention of the chunk's queries over the cache; streaming KV heads see ``sink`` +
+        ``local`` tokens.  Returns (out bf16, m, l), rows in token order."""
+        c = self.cache
+        B.dsa_chunk_attn(c.kv, self.chunk, q, scale if scale is not None else
+                         1.0 / math.sqrt(c.head_dim), self.out, self.m, self.l, self.workspace, sink,
+                         local, stream)
+        return self.out, self.m, self.l
+
+
 class TopKDecoder:
     def __init__(self, cache: Cache, k: int, logical_page: int | None = None,
                  meta_kind: int = B.DSA_META_MINMAX, scale: float | None = None):
@@ -127,6 +190,12 @@ class TopKDecoder:
     def append(self, k_new, v_new, stream=None):
         """Appends one decoded token per request, keeping this decoder's metadata current."""
         self.cache.append(k_new, v_new, [(self.kind, self.lp, self.meta)], stream)
+
+    def prefill(self, chunk: Chunk, q, k_new, v_new, rotary=None, stream=None):
+        """Appends a planned chunk (prompts, or pieces of them), keeping this decoder's metadata
+        current, and attends it over the whole cache: (out bf16, m, l)."""
+        q_t = chunk.append(k_new, v_new, [(self.kind, self.lp, self.meta)], rotary, q, stream)
+        return chunk.attend(q_t, self.scale, stream=stream)
 
     def use_kv8(self, stream=None):
         """Attends over KV8 pages from now on (the pools are quantised once, here); selection is
@@ -202,6 +271,14 @@ class HierDecoder:
         """Appends one decoded token per request, keeping this decoder's metadata current."""
         self.cache.append(k_new, v_new, [(B.DSA_META_MINMAX, self.lp, self.meta)], stream)
 
+    def prefill(self, chunk: Chunk, q, k_new, v_new, rotary=None, stream=None):
+        """Appends a planned chunk (prompts, or pieces of them), keeping this decoder's metadata
+        current, and attends it over the whole cache (streaming heads over their sink + local
+        tokens): (out bf16, m, l)."""
+        q_t = chunk.append(k_new, v_new, [(B.DSA_META_MINMAX, self.lp, self.meta)], rotary, q,
+                           stream)
+        return chunk.attend(q_t, self.scale, self.sink, self.local, stream=stream)
+
     def select(self, q, stream=None):
         c = self.cache
         B.dsa_score_pages(c.kv, q, self.meta, B.DSA_META_MINMAX, self.lp, self.scores, stream)
@@ -252,6 +329,13 @@ class ThresholdDecoder:
         """Appends one decoded token per request, keeping this decoder's metadata current."""
         self.cache.append(k_new, v_new, [(B.DSA_META_MEAN, self.cache.page_size, self.meta)],
                           stream)
+
+    def prefill(self, chunk: Chunk, q, k_new, v_new, rotary=None, stream=None):
+        """Appends a planned chunk (prompts, or pieces of them), keeping this decoder's metadata
+        current, and attends it over the whole cache: (out bf16, m, l)."""
+        q_t = chunk.append(k_new, v_new, [(B.DSA_META_MEAN, self.cache.page_size, self.meta)], rotary, q,
+                           stream)
+        return chunk.attend(q_t, self.scale, stream=stream)
 
     def step(self, q, stream=None):
         c = self.cache
@@ -365,6 +449,13 @@ class PRRDecoder:
         treats it as fresh (level = its score, trend 0)."""
         c = self.cache
         c.append(k_new, v_new, [(B.DSA_META_MINMAX, c.page_size, self.meta)], stream)
+
+    def prefill(self, chunk: Chunk, q, k_new, v_new, rotary=None, stream=None):
+        """Appends a planned chunk (prompts, or pieces of them), keeping this decoder's metadata
+        current, and attends it over the whole cache: (out bf16, m, l)."""
+        q_t = chunk.append(k_new, v_new, [(B.DSA_META_MINMAX, self.cache.page_size, self.meta)], rotary, q,
+                           stream)
+        return chunk.attend(q_t, self.scale, stream=stream)
 
     # ---- stages (one or two library calls each), exposed so a caller can time them one by one
     def stage_score(self, q, stream=None):

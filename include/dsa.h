@@ -49,11 +49,13 @@ enum {
   DSA_ERR_WORKSPACE = -5    /* workspace missing or smaller than the size query returned */
 };
 
-/* Bits a kernel may OR into kv->status (device int32).  Never set by a correct call. */
+/* Bits a kernel may OR into kv->status (device int32).  Never set by a correct call, but for
+ * DSA_STATUS_NO_PAGES, which tells that the pages ran out. */
 enum {
   DSA_STATUS_BAD_PAGE = 1, /* a page-table entry outside [0, num_phys_pages) was skipped */
   DSA_STATUS_OVERFLOW = 2, /* a list exceeded an internal capacity and was truncated */
-  DSA_STATUS_TIMEOUT = 4   /* a bounded on-device wait gave up (the kernel returned early) */
+  DSA_STATUS_TIMEOUT = 4,  /* a bounded on-device wait gave up (the kernel returned early) */
+  DSA_STATUS_NO_PAGES = 8  /* dsa_plan_chunk refused a request (too few pages, or too long) */
 };
 
 enum { DSA_META_MINMAX = 0, DSA_META_MEAN = 1 };
@@ -487,6 +489,126 @@ size_t dsa_prr_step_counter_bytes(const dsa_paged_kv* kv);
  */
 int dsa_merge_partials(const float* partials, int32_t rows, int32_t num_parts, int32_t group,
                        int32_t head_dim, float* out, float* m, float* l, dsa_stream_t stream);
+
+/*
+ * A chunk: the new tokens of one step, packed request after request on one token axis (a prompt, a
+ * piece of a prompt, one decode token, or nothing per request).  Arrays are the caller's device
+ * memory; dsa_plan_chunk fills them, or a caller with its own page manager does.
+ *   start : int32 [B + 1].  Request b's tokens are start[b] .. start[b + 1] - 1; non-decreasing.
+ *   count : int32 [B].  How many of them take part: start[b + 1] - start[b], or 0 (refused).
+ *   row   : int32 [tokens].  Request of every token, -1 where it takes no part.
+ *   pos   : int32 [tokens].  Its position in its request, -1 where it takes no part.
+ *   slot  : int32 [tokens] or NULL.  Its place in the pools, physical page * p + offset, or -1.
+ *   tokens: length of the token axis (a capacity: what lies behind start[B] takes no part, so one
+ *           captured graph serves steps of fewer tokens).
+ * dsa_append_chunk reads start, count, row and pos; dsa_chunk_attn start and count.
+ */
+typedef struct dsa_chunk {
+  int32_t* start;
+  int32_t* count;
+  int32_t* row;
+  int32_t* pos;
+  int32_t* slot;
+  int32_t tokens;
+} dsa_chunk;
+
+/*
+ * Block tables and slot maps of a step, from the requests' lengths: assigns pages to new tokens from
+ * a stack of free pages on the device, takes back the pages of finished or rolled-back requests, and
+ * fills the chunk.  One launch, no host round trip.
+ *   kv         : page_table and seq_lens are WRITTEN; of the rest only the shape fields are read
+ *                (the pools may be NULL).
+ *   lens_in    : int32 [B], lengths L_b before the step; may be kv->seq_lens itself.
+ *   delta      : int32 [B].  n > 0: n new tokens; 0: nothing; n < 0: the last min(-n, L_b) tokens are
+ *                dropped, and every page that then holds no token is given back (any n <= -L_b
+ *                releases the request).
+ *   free_pages : int32 [free_capacity], a stack: entries 0 .. *free_in - 1 are free physical pages.
+ *                Pages given back in this call are pushed first, in request then position order;
+ *                then pages are taken from the top, in request then position order.
+ *   free_in    : int32 [1], pages on the stack before; free_out: int32 [1], after.  They may be the
+ *                same word.  Pages that no longer fit the stack are lost and raise
+ *                DSA_STATUS_OVERFLOW.
+ *   chunk (out): start, count, row, pos and slot, with start the prefix sum of max(delta, 0).
+ * Admission is decided in request order: a request takes part when its tokens end inside
+ * chunk->tokens, its new length fits its table row, and either it needs no new page or the pages that
+ * requests 0 .. b need together are there.  A refused request keeps its length and pages, gets count
+ * 0, its tokens get row = pos = slot = -1, and DSA_STATUS_NO_PAGES is raised.
+ *   kv->seq_lens (out): L_b + count[b], or the shortened length: what the append and the attention
+ *                of this step expect.  Table entries behind a shortened request keep their old ids.
+ *   workspace  : dsa_plan_chunk_workspace_size(B) bytes, ZERO-FILLED before the first use (each
+ *                completed call leaves it zero-filled).
+ * batch <= 8192.
+ */
+int dsa_plan_chunk(const dsa_paged_kv* kv, const int32_t* lens_in, const int32_t* delta,
+                   int32_t* free_pages, int32_t free_capacity, const int32_t* free_in,
+                   int32_t* free_out, const dsa_chunk* chunk, void* workspace,
+                   size_t workspace_bytes, dsa_stream_t stream);
+size_t dsa_plan_chunk_workspace_size(int32_t batch);
+
+/*
+ * Rotary positions with one to four axes (time, height, width, ...).  Pair i of a head's first
+ * rot_dim dims turns by positions[axis[i]][token] * phase[i]:
+ *   (x, y) -> (x cos - y sin, y cos + x sin).
+ *   phase      : uint64 [rot_dim / 2], the turn per position as a fraction of a full turn in 0.64
+ *                fixed point, round(frequency / (2 pi) * 2^64): position times phase modulo 2^64 is
+ *                then exact at any position.  8-byte aligned.
+ *   axis       : uint8 [rot_dim / 2], values < num_axes (larger ones count as the last axis); NULL
+ *                with one axis.
+ *   positions  : int32 [num_axes][tokens]; NULL with one axis: chunk->pos.
+ *   rot_dim    : multiple of 16 in [16, 128]; the dims behind it are not turned.
+ *   interleaved: 0: pair i is dims (i, i + rot_dim / 2); otherwise dims (2 i, 2 i + 1).
+ */
+typedef struct dsa_rotary {
+  const uint64_t* phase;
+  const uint8_t* axis;
+  const int32_t* positions;
+  int32_t num_axes;
+  int32_t rot_dim;
+  int32_t interleaved;
+} dsa_rotary;
+
+/*
+ * Appends a chunk (the several-token form of dsa_append_kv): turns its keys and queries by their
+ * positions, writes keys and values into their pages and renews the metadata of every page that got
+ * a token, exactly as dsa_build_page_meta computes it, bit for bit.  kv->seq_lens ALREADY counts the
+ * chunk and the page table already holds its pages (as dsa_plan_chunk leaves them).
+ *   k_new, v_new : bf16, token t and KV head h at [t * stride + h * D]; strides in elements, at least
+ *                  Hkv * D and a multiple of 8 (slices of one fused projection); 16-byte aligned.
+ *   rotary       : NULL: q and k are taken as they are.
+ *   q, q_out     : NULL, or the queries (same form, Hq heads) and bf16 [tokens][Hq][D] for the turned
+ *                  ones (may be q itself when that is contiguous).
+ *   meta         : as for dsa_append_kv, or NULL.  A caller keeping several metadata buffers calls
+ *                  once per buffer, with q NULL after the first (turning q in place twice would turn
+ *                  it twice; the KV write repeats harmlessly).
+ * Tokens with row -1 and those behind start[B] are neither read nor written.  A token on a bad page
+ * id is skipped (its query is still turned) and raises DSA_STATUS_BAD_PAGE.
+ */
+int dsa_append_chunk(const dsa_paged_kv* kv, const dsa_chunk* chunk, const void* k_new,
+                     int64_t k_stride, const void* v_new, int64_t v_stride,
+                     const dsa_rotary* rotary, const void* q, int64_t q_stride, void* q_out,
+                     int32_t meta_kind, int32_t logical_page, void* meta, dsa_stream_t stream);
+
+/*
+ * Attention of a chunk over the paged cache ([LServe] §3.2: one prefill pass serves dense and
+ * streaming heads): the query at position s of request b attends, on dense KV heads, to tokens
+ * 0 .. s, and on the KV heads marked in kv->head_is_streaming to [0, sink_tokens) ∪
+ * (s - local_tokens, s], both cut at s -- with one token per request the rows of a decode step.
+ * kv->seq_lens counts the chunk and its keys and values are in their pages; the queries of request b
+ * are its last count[b] positions.
+ *   q   : bf16 [tokens][Hq][D], 16-byte aligned.  scale must be positive and finite.
+ *   out : bf16 [tokens][Hq][D], 16-byte aligned; may not overlap q.  m, l: fp32 [tokens][Hq] or NULL
+ *         (m the maximal logit, l the sum of exp(s - m)).  A query that sees no token gets O = 0,
+ *         m = -inf, l = 0.  Rows of tokens that take no part are left as they are.
+ *   workspace : dsa_chunk_attn_workspace_size(kv, tokens) bytes, 16-byte aligned, ZERO-FILLED before
+ *               the first use (each completed call leaves the words it counts with at zero; zero-fill
+ *               it again after DSA_STATUS_TIMEOUT).  Calls that share a workspace must be ordered
+ *               (one stream, or captured graphs that never run at once).
+ * Sums run in fp32; the probabilities are rounded to bf16 for the P.V product.
+ */
+int dsa_chunk_attn(const dsa_paged_kv* kv, const dsa_chunk* chunk, const void* q,
+                   int32_t sink_tokens, int32_t local_tokens, float scale, void* out, float* m,
+                   float* l, void* workspace, size_t workspace_bytes, dsa_stream_t stream);
+size_t dsa_chunk_attn_workspace_size(const dsa_paged_kv* kv, int32_t tokens);
 
 #ifdef __cplusplus
 }

@@ -1,0 +1,210 @@
+"""CPU-only checks of the chunk operators' host side: struct layouts, argument checks that answer
+before any CUDA call, the fixed-point phases, and the reference page plan the GPU tests compare with
+(its own invariants: pages are neither lost nor handed out twice)."""
+
+import ctypes
+import math
+import os
+import random
+import subprocess
+
+import numpy as np
+import pytest
+import torch
+
+from chunk_support import plan_reference
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from dynamic_block_sparse_gb300 import binding, build
+    build.build()
+    return binding.load()
+
+
+def _kv(**kw):
+    from dynamic_block_sparse_gb300 import binding as B
+    kv = B.PagedKV()
+    kv.k_pages = kv.v_pages = kv.page_table = kv.seq_lens = 4096
+    kv.batch, kv.num_q_heads, kv.num_kv_heads = 2, 8, 2
+    kv.head_dim, kv.page_size, kv.max_pages_per_seq, kv.num_phys_pages = 128, 64, 8, 16
+    for k, v in kw.items():
+        setattr(kv, k, v)
+    return kv
+
+
+def _chunk(tokens=16, **kw):
+    from dynamic_block_sparse_gb300 import binding as B
+    c = B.Chunk()
+    c.start = c.count = c.row = c.pos = c.slot = 4096
+    c.tokens = tokens
+    for k, v in kw.items():
+        setattr(c, k, v)
+    return c
+
+
+def test_struct_layouts_match_the_header(tmp_path):
+    from dynamic_block_sparse_gb300 import binding as B
+    lines = ["#include <stdio.h>", "#include <stddef.h>", '#include "dsa.h"', "int main(void) {"]
+    for cname, cls in (("dsa_chunk", B.Chunk), ("dsa_rotary", B.Rotary)):
+        lines.append(f'  printf("{cname} %zu\\n", sizeof({cname}));')
+        for f, _ in cls._fields_:
+            lines.append(f'  printf("{cname}.{f} %zu\\n", offsetof({cname}, {f}));')
+    lines += [f'  printf("no_pages %d\\n", DSA_STATUS_NO_PAGES);', "  return 0;", "}"]
+    src, exe = tmp_path / "layout.c", tmp_path / "layout"
+    src.write_text("\n".join(lines) + "\n")
+    subprocess.run(["gcc", "-I", os.path.join(ROOT, "include"), "-o", str(exe), str(src)],
+                   check=True)
+    got = dict(ln.split() for ln in subprocess.run([str(exe)], capture_output=True, text=True,
+                                                    check=True).stdout.splitlines())
+    assert int(got["no_pages"]) == B.DSA_STATUS_NO_PAGES
+    for cname, cls in (("dsa_chunk", B.Chunk), ("dsa_rotary", B.Rotary)):
+        assert int(got[cname]) == ctypes.sizeof(cls), cname
+        for f, _ in cls._fields_:
+            assert int(got[f"{cname}.{f}"]) == getattr(cls, f).offset, f"{cname}.{f}"
+
+
+def test_plan_chunk_refusals(lib):
+    def call(kv=None, chunk=None, lens=4096, delta=4096, free=4096, cap=16, fin=4096, fout=4096,
+             ws=8192, ws_bytes=16):
+        return lib.dsa_plan_chunk(ctypes.byref(kv or _kv()), lens, delta, free, cap, fin, fout,
+                                  None if chunk == 0 else ctypes.byref(chunk or _chunk()), ws,
+                                  ws_bytes, None)
+    assert call(chunk=0) == -1
+    assert call(chunk=_chunk(tokens=-1)) == -1
+    assert call(cap=-1) == -1
+    for name in ("lens", "delta", "free", "fin", "fout"):
+        assert call(**{name: None}) == -1, name
+    assert call(chunk=_chunk(start=None)) == -1
+    assert call(chunk=_chunk(count=None)) == -1
+    assert call(chunk=_chunk(row=None)) == -1
+    assert call(chunk=_chunk(pos=None)) == -1
+    assert call(kv=_kv(batch=8193)) == -3 and b"8193" in lib.dsa_last_error()
+    assert call(kv=_kv(batch=8192, max_pages_per_seq=1 << 19)) == -3
+    assert call(kv=_kv(page_size=256, max_pages_per_seq=1 << 23, batch=1)) == -3
+    assert call(ws=None) == -5
+    assert call(ws_bytes=8) == -5
+    assert call(ws=8200) == -2
+    assert lib.dsa_plan_chunk_workspace_size(8) == 16
+
+
+def test_append_chunk_refusals(lib):
+    from dynamic_block_sparse_gb300 import binding as B
+
+    def rot(**kw):
+        r = B.Rotary()
+        r.phase, r.num_axes, r.rot_dim = 4096, 1, 128
+        for k, v in kw.items():
+            setattr(r, k, v)
+        return r
+
+    def call(kv=None, chunk=None, k=8192, ks=256, v=8192, vs=256, rotary=None, q=None, qs=1024,
+             qo=None, kind=0, lp=16, meta=16384):
+        return lib.dsa_append_chunk(
+            ctypes.byref(kv or _kv()), None if chunk == 0 else ctypes.byref(chunk or _chunk()), k,
+            ks, v, vs, None if rotary is None else ctypes.byref(rotary), q, qs, qo, kind, lp, meta,
+            None)
+    assert call(chunk=0) == -1
+    assert call(chunk=_chunk(tokens=-1)) == -1
+    assert call(chunk=_chunk(tokens=0), k=None) == 0                 # nothing to do
+    assert call(k=None) == -1 and call(v=None) == -1
+    for f in ("start", "count", "row", "pos"):
+        assert call(chunk=_chunk(**{f: None})) == -1, f
+    assert call(k=8200) == -2 and call(v=8200) == -2
+    assert call(ks=255) == -1 and call(ks=260) == -1 and call(vs=128) == -1
+    assert call(q=4096) == -1 and call(qo=4096) == -1                # only together
+    assert call(q=4100, qo=8192) == -2
+    assert call(q=4096, qo=8192, qs=1023) == -1 and call(q=4096, qo=8192, qs=1028) == -1
+    assert call(q=4096, qo=4096, qs=2048) == -1                      # in place needs contiguity
+    assert call(rotary=rot(phase=None)) == -1
+    assert call(rotary=rot(phase=4100)) == -2
+    for bad in (0, 8, 24, 136, 144):
+        assert call(rotary=rot(rot_dim=bad)) == -3, bad
+    assert call(rotary=rot(num_axes=0)) == -3 and call(rotary=rot(num_axes=5)) == -3
+    assert call(rotary=rot(num_axes=2)) == -1                        # axis and positions missing
+    assert call(rotary=rot(num_axes=2, axis=4096)) == -1
+    assert call(kind=2) == -1 and call(lp=48) == -1 and call(meta=16392) == -2
+
+
+def test_chunk_attn_refusals(lib):
+    def call(kv=None, chunk=None, q=4096, sink=0, local=0, scale=0.1, out=8192, ws=16384,
+             ws_bytes=1 << 40):
+        return lib.dsa_chunk_attn(ctypes.byref(kv or _kv()),
+                                  None if chunk == 0 else ctypes.byref(chunk or _chunk()), q, sink,
+                                  local, scale, out, None, None, ws, ws_bytes, None)
+    assert call(chunk=0) == -1
+    assert call(chunk=_chunk(tokens=-3)) == -1
+    assert call(chunk=_chunk(tokens=0), q=None) == 0                 # nothing to do
+    assert call(q=None) == -1 and call(out=None) == -1
+    assert call(chunk=_chunk(start=None)) == -1 and call(chunk=_chunk(count=None)) == -1
+    assert call(q=4104) == -2 and call(out=8200) == -2
+    assert call(sink=-1) == -1 and call(local=-1) == -1
+    for bad in (0.0, -0.1, math.inf, -math.inf, math.nan, 1e-45, 3e38):
+        assert call(scale=bad) == -1, bad
+    assert call(ws=None) == -5 and call(ws_bytes=0) == -5 and call(ws=16392) == -2
+    assert call(kv=_kv(head_dim=64)) == -3
+    assert call(kv=_kv(page_size=256, max_pages_per_seq=1 << 23, batch=1)) == -3
+
+
+def test_binding_refuses_wrong_tensors(lib):
+    from dynamic_block_sparse_gb300 import binding as B
+    z = lambda *s: torch.zeros(s, dtype=torch.int32)
+    with pytest.raises(ValueError, match="int32"):
+        B.chunk(torch.zeros(3, dtype=torch.int64), z(2), z(4), z(4))
+    with pytest.raises(ValueError, match="shape"):
+        B.chunk(z(4), z(2), z(4), z(4))
+    with pytest.raises(ValueError, match="CUDA"):
+        B.chunk(z(3), z(2), z(4), z(4))
+    with pytest.raises(ValueError, match="phase"):
+        B.rotary(torch.zeros(32, dtype=torch.int64), 128)
+    with pytest.raises(ValueError, match="contiguous"):
+        B._token_rows(torch.zeros(4, 2, 256, dtype=torch.bfloat16)[..., ::2], 4, 2, "k_new")
+    with pytest.raises(ValueError, match="bf16"):
+        B._token_rows(torch.zeros(4, 2, 128), 4, 2, "k_new")
+    assert B._token_rows(torch.zeros(4, 10, 128, dtype=torch.bfloat16)[:, 2:4], 4, 2, "k") == 1280
+
+
+def test_rotary_phases_are_exact_fractions_of_a_turn():
+    """phase * position modulo 2^64 is the turn of position * frequency: checked against a 40-digit
+    value of the angle at positions where float32 has lost it."""
+    from fractions import Fraction
+
+    from dynamic_block_sparse_gb300 import binding as B
+    freqs = [500000.0 ** (-2 * i / 128) for i in range(64)] + [math.pi, 7.0]
+    ph = B.rotary_phases(freqs, "cpu")
+    two_pi = Fraction(62831853071795864769252867665590057683943, 10 ** 40)
+    for f, p in zip(freqs, ph.tolist()):
+        for pos in (0, 1, 131071, (1 << 31) - 1, -5):
+            turns = Fraction(f) * pos / two_pi
+            got = Fraction((p * pos) % 2 ** 64, 2 ** 64)
+            off = abs(got - turns % 1)
+            off = min(off, 1 - off)
+            assert off <= Fraction(abs(pos) + 1, 2 ** 64), (f, pos)
+
+
+@pytest.mark.parametrize("seed", range(20))
+def test_plan_reference_keeps_every_page_once(seed):
+    """Steps of random growth, rollback and release through the reference plan: at any time the pages
+    of the live requests and the stack are a permutation of the pool."""
+    r = random.Random(seed)
+    p, B, width, phys = r.choice([16, 48]), r.randint(1, 9), r.randint(2, 12), r.randint(6, 60)
+    table = np.full((B, width), -7, dtype=np.int64)
+    lens, free = [0] * B, list(r.sample(range(phys), phys))
+    seen = set()
+    for _ in range(30):
+        delta = [r.choice([0, 1, 1, r.randint(1, p * 3), -r.randint(1, 40), -10 ** 6])
+                 for _ in range(B)]
+        got = plan_reference(table, lens, delta, free, p, tokens=200)
+        table, lens, free = got["table"], got["lens"], got["stack"]
+        held = [int(table[b, j]) for b in range(B) for j in range(-(-lens[b] // p))]
+        assert sorted(held + free) == list(range(phys))
+        for t, (b, pos, slot) in enumerate(zip(got["row"], got["pos"], got["slot"])):
+            if b >= 0:
+                assert slot == table[b, pos // p] * p + pos % p and pos < lens[b]
+                assert got["start"][b] <= t < got["start"][b] + got["count"][b]
+            else:
+                assert pos == slot == -1
+        seen.add(got["refused"])
+    assert seen  # both outcomes occur over the seeds; each is asserted page by page above
