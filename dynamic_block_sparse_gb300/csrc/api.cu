@@ -116,6 +116,37 @@ int check_kv(const dsa_paged_kv* kv, int pools, KvView* view) {
   return DSA_OK;
 }
 
+int encode_map(CUtensorMap* map, const void* base, int rank, const cuuint64_t* dims,
+               const cuuint64_t* strides, const cuuint32_t* box) {
+  auto fn = encode_fn();
+  if (!fn) return fail(DSA_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(base), dims,
+                  strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(DSA_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", int(r));
+  return DSA_OK;
+}
+
+// Pool view for key tiles of the chunk attention: (64 dims, token rows, 2 halves), one box a piece of
+// `piece` rows of one half (a piece never crosses a page or a 128-token tile).
+int piece_map(const void* base, const KvView& v, int piece, CUtensorMap* map) {
+  const cuuint64_t dims[3] = {64, static_cast<cuuint64_t>(v.num_phys) * v.Hkv * v.p, 2};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(kHeadDim) * 2, 128};
+  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(piece), 1};
+  return encode_map(map, base, 3, dims, strides, box);
+}
+
+// Query view: (64 dims, query heads, tokens, 2 halves), one box the G heads of 128 / G tokens of one
+// half: rows (token, head) of a query tile.
+int query_map(const void* q, const KvView& v, int tokens, CUtensorMap* map) {
+  const cuuint64_t dims[4] = {64, static_cast<cuuint64_t>(v.Hq), static_cast<cuuint64_t>(tokens), 2};
+  const cuuint64_t row = static_cast<cuuint64_t>(kHeadDim) * 2;
+  const cuuint64_t strides[3] = {row, row * v.Hq, 128};
+  const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(v.G), static_cast<cuuint32_t>(128 / v.G), 1};
+  return encode_map(map, q, 4, dims, strides, box);
+}
+
 int attn_stages(int page, int pages_per_cta) {
   int s = 131072 / (512 * page);
   if (s < 1) s = 1;
@@ -1095,7 +1126,7 @@ int dsa_append_chunk(const dsa_paged_kv* kv, const dsa_chunk* chunk, const void*
 size_t dsa_chunk_attn_workspace_size(const dsa_paged_kv* kv, int32_t tokens) {
   KvView v;
   if (check_kv(kv, 0, &v) || tokens <= 0) return 0;
-  return 16;
+  return chunk_attn_workspace(v.G, tokens).total;
 }
 
 int dsa_chunk_attn(const dsa_paged_kv* kv, const dsa_chunk* chunk, const void* q,
@@ -1116,27 +1147,34 @@ int dsa_chunk_attn(const dsa_paged_kv* kv, const dsa_chunk* chunk, const void* q
   const float sl = scale_log2(scale);
   if (!(sl >= FLT_MIN && sl <= FLT_MAX))
     return fail(DSA_ERR_INVALID_ARG, "scale must be positive and finite");
-  if (static_cast<long long>(v.p) * v.max_pages >= (1LL << 31))
-    return fail(DSA_ERR_UNSUPPORTED, "%d pages of %d tokens per request exceed 2^31 tokens",
+  if (static_cast<long long>(v.p) * v.max_pages > (1LL << 31) - 1024)
+    return fail(DSA_ERR_UNSUPPORTED, "%d pages of %d tokens per request exceed 2^31 - 1024 tokens",
                 v.max_pages, v.p);
-  if (!workspace || workspace_bytes < dsa_chunk_attn_workspace_size(kv, chunk->tokens))
+  if (v.B > kChunkMaxBatch)
+    return fail(DSA_ERR_UNSUPPORTED, "batch %d > %d", v.B, kChunkMaxBatch);
+  const ChunkAttnWorkspace w = chunk_attn_workspace(v.G, chunk->tokens);
+  if (!workspace || workspace_bytes < w.total)
     return fail(DSA_ERR_WORKSPACE, "dsa_chunk_attn: workspace too small");
   if (!aligned(workspace, 16)) return fail(DSA_ERR_ALIGNMENT, "workspace must be 16-byte aligned");
+  CUtensorMap tq, tk, tv;
+  const int piece = v.p % 128 == 0 ? 128 : v.p % 64 == 0 ? 64 : v.p % 32 == 0 ? 32 : 16;
+  if ((rc = query_map(q, v, chunk->tokens, &tq)) || (rc = piece_map(kv->k_pages, v, piece, &tk)) ||
+      (rc = piece_map(kv->v_pages, v, piece, &tv)))
+    return rc;
   ChunkAttnArgs a = {};
   a.kv = v;
-  a.k_pages = static_cast<const __nv_bfloat16*>(kv->k_pages);
-  a.v_pages = static_cast<const __nv_bfloat16*>(kv->v_pages);
   a.start = chunk->start;
   a.count = chunk->count;
-  a.tokens = chunk->tokens;
-  a.q = static_cast<const __nv_bfloat16*>(q);
   a.sink = sink_tokens;
   a.local = local_tokens;
   a.scale_log2 = sl;
   a.out = static_cast<__nv_bfloat16*>(out);
   a.m = m;
   a.l = l;
-  cudaError_t e = launch_chunk_attn(a, static_cast<cudaStream_t>(stream));
+  a.tickets = static_cast<int32_t*>(workspace);
+  a.records = reinterpret_cast<float*>(static_cast<char*>(workspace) + w.records_off);
+  a.rec_rows = w.rows;
+  cudaError_t e = launch_chunk_attn(tq, tk, tv, a, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? ok() : cuda_fail(e, "dsa_chunk_attn launch");
 }
 

@@ -272,21 +272,28 @@ struct AppendArgs {
 cudaError_t launch_append_chunk(const AppendArgs& a, int kind, cudaStream_t s);
 
 // Attention of a chunk over the paged cache (chunk_attn.cu).
+constexpr int kChunkMaxBatch = 8192;  // requests whose prefix sums one CTA keeps in shared memory
+constexpr int kChunkMaxGrid = 512;
 struct ChunkAttnArgs {
   KvView kv;
-  const __nv_bfloat16* k_pages;
-  const __nv_bfloat16* v_pages;
   const int32_t* start;
   const int32_t* count;
-  int tokens;
-  const __nv_bfloat16* q;
   int sink, local;  // of streaming heads
   float scale_log2;
   __nv_bfloat16* out;
   float* m;  // may be null
   float* l;  // may be null
+  int32_t* tickets;  // [grid], zero on entry; left zero
+  float* records;    // [grid][2][rec_rows][kRecordFloats]
+  int rec_rows;
 };
-cudaError_t launch_chunk_attn(const ChunkAttnArgs& a, cudaStream_t s);
+struct ChunkAttnWorkspace {
+  size_t records_off, total;
+  int rows;
+};
+ChunkAttnWorkspace chunk_attn_workspace(int G, int tokens);
+cudaError_t launch_chunk_attn(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtensorMap& tmV,
+                              const ChunkAttnArgs& a, cudaStream_t s);
 
 struct ThresholdArgs {
   KvView kv;
