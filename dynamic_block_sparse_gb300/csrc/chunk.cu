@@ -224,6 +224,72 @@ __global__ void __launch_bounds__(kPlanThreads) plan_chunk_kernel(const PlanArgs
 constexpr int kAppThreads = 256;
 constexpr int kAppTokens = 16;
 
+// ---- cosine and sine of a fraction of a turn (64-bit fixed point), to the last bit of fp32 but for
+// about one value in 10^5: keys that lie next to a rounding border of bf16 then fall on the same side
+// as in an evaluation of wider precision, and with them the page metadata.  The nearest quadrant is
+// taken off exactly; theta = 2 pi r in [-pi/4, pi/4] is a pair of floats (high, low), and the Taylor
+// series of sin and cos are summed with their two largest coefficients and all products by them in
+// such pairs (the terms behind weigh below 2^-11, so plain fp32 leaves 2^-35 there).
+struct Pair {
+  float h, l;
+};
+DSA_DEV Pair pair_sum(float a, float b) {  // |a| >= |b| or a == 0
+  const float s = __fadd_rn(a, b);
+  return {s, __fsub_rn(b, __fsub_rn(s, a))};
+}
+DSA_DEV Pair pair_mul(const Pair& a, const Pair& b) {
+  const float p = __fmul_rn(a.h, b.h);
+  float e = __fmaf_rn(a.h, b.h, -p);
+  e = __fmaf_rn(a.h, b.l, e);
+  return {p, __fmaf_rn(a.l, b.h, e)};
+}
+DSA_DEV Pair pair_add(float ch, float cl, const Pair& p) {  // |ch| >= |p|
+  const Pair s = pair_sum(ch, p.h);
+  return {s.h, __fadd_rn(__fadd_rn(s.l, p.l), cl)};
+}
+
+DSA_DEV float2 cos_sin_turn(unsigned long long turn) {
+  const unsigned q = static_cast<unsigned>((turn + (1ull << 61)) >> 62);  // nearest quarter
+  const long long r = static_cast<long long>(turn - (static_cast<unsigned long long>(q) << 62));
+  // r as the exact sum of 24 + 32 bits (what is dropped is below 2^-56 of a turn)
+  const float rh = static_cast<float>(static_cast<int>(r >> 40)) * 1099511627776.f;
+  const float rl = static_cast<float>(static_cast<unsigned>(r >> 8)) * 256.f;
+  const Pair t = pair_sum(rh, rl);
+  // theta = r * 2 pi / 2^64
+  constexpr float kTurnH = 3.4061217e-19f, kTurnL = -9.4783964e-27f;
+  float th = __fmul_rn(t.h, kTurnH);
+  float tl = __fmaf_rn(t.h, kTurnH, -th);
+  tl = __fmaf_rn(t.h, kTurnL, tl);
+  tl = __fmaf_rn(t.l, kTurnH, tl);
+  const Pair a = pair_sum(th, tl);
+  const Pair z = pair_mul(a, a);
+  // 1 / k!, alternating; the pairs are 1/6, 1/120 and 1/2, 1/24 to 48 bits
+  float ps = __fmaf_rn(z.h, 1.6059044e-10f, -2.5052108e-08f);
+  ps = __fmaf_rn(z.h, ps, 2.7557319e-06f);
+  ps = __fmaf_rn(z.h, ps, -0.0001984127f);
+  Pair s = pair_add(0.008333334f, -4.346172e-10f, pair_mul(z, {ps, 0.f}));
+  s = pair_add(-0.16666667f, 4.967054e-09f, pair_mul(z, s));
+  s = pair_add(a.h, a.l, pair_mul(a, pair_mul(z, s)));
+  float pc = __fmaf_rn(z.h, -1.1470746e-11f, 2.0876756e-09f);
+  pc = __fmaf_rn(z.h, pc, -2.755732e-07f);
+  pc = __fmaf_rn(z.h, pc, 2.4801588e-05f);
+  pc = __fmaf_rn(z.h, pc, -0.0013888889f);
+  Pair c = pair_add(0.041666668f, -1.2417635e-09f, pair_mul(z, {pc, 0.f}));
+  c = pair_add(-0.5f, 0.f, pair_mul(z, c));
+  c = pair_add(1.f, 0.f, pair_mul(z, c));
+  const float sn = __fadd_rn(s.h, s.l), cs = __fadd_rn(c.h, c.l);
+  const float x = q & 1 ? sn : cs, y = q & 1 ? cs : sn;
+  return make_float2(q == 1 || q == 2 ? -x : x, q & 2 ? -y : y);
+}
+
+// (a cos - b sin, b cos + a sin) with every product rounded once, as the formula is written.
+DSA_DEV float turn_x(float a, float b, float2 cs) {
+  return __fsub_rn(__fmul_rn(a, cs.x), __fmul_rn(b, cs.y));
+}
+DSA_DEV float turn_y(float a, float b, float2 cs) {
+  return __fadd_rn(__fmul_rn(b, cs.x), __fmul_rn(a, cs.y));
+}
+
 DSA_DEV void rotate8(const uint4& xa, const uint4& xb, const float2* cs, uint4& ya, uint4& yb) {
   const __nv_bfloat16* a = reinterpret_cast<const __nv_bfloat16*>(&xa);
   const __nv_bfloat16* b = reinterpret_cast<const __nv_bfloat16*>(&xb);
@@ -234,8 +300,8 @@ DSA_DEV void rotate8(const uint4& xa, const uint4& xb, const float2* cs, uint4& 
     const float2 c0 = cs[2 * e], c1 = cs[2 * e + 1];
     const float a0 = __bfloat162float(a[2 * e]), a1 = __bfloat162float(a[2 * e + 1]);
     const float b0 = __bfloat162float(b[2 * e]), b1 = __bfloat162float(b[2 * e + 1]);
-    oa[e] = pack_bf16(a0 * c0.x - b0 * c0.y, a1 * c1.x - b1 * c1.y);
-    ob[e] = pack_bf16(b0 * c0.x + a0 * c0.y, b1 * c1.x + a1 * c1.y);
+    oa[e] = pack_bf16(turn_x(a0, b0, c0), turn_x(a1, b1, c1));
+    ob[e] = pack_bf16(turn_y(a0, b0, c0), turn_y(a1, b1, c1));
   }
 }
 
@@ -247,7 +313,7 @@ DSA_DEV uint4 rotate_pairs(const uint4& x, const float2* cs) {
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
     const float a = __bfloat162float(v[2 * e]), b = __bfloat162float(v[2 * e + 1]);
-    o[e] = pack_bf16(a * cs[e].x - b * cs[e].y, b * cs[e].x + a * cs[e].y);
+    o[e] = pack_bf16(turn_x(a, b, cs[e]), turn_y(a, b, cs[e]));
   }
   return y;
 }
@@ -291,13 +357,8 @@ __global__ void __launch_bounds__(kAppThreads) append_chunk_kernel(const AppendA
           const int ax = a.axis ? min(static_cast<int>(a.axis[pr]), a.num_axes - 1) : 0;
           const long long where =
               a.positions ? a.positions[static_cast<size_t>(ax) * a.tokens + t] : pos + c0 + tt;
-          // position x phase modulo one turn, exact in 64-bit integers whatever the position; the
-          // top 32 bits are the signed fraction of a turn
-          const unsigned long long turn = static_cast<unsigned long long>(where) * a.phase[pr];
-          const float x = static_cast<float>(static_cast<int>(turn >> 32)) * 4.656612873077393e-10f;
-          float sn, cs;
-          sincospif(x, &sn, &cs);
-          s_cs[tt][pr] = make_float2(cs, sn);
+          // position x phase modulo one turn, exact in 64-bit integers whatever the position
+          s_cs[tt][pr] = cos_sin_turn(static_cast<unsigned long long>(where) * a.phase[pr]);
         }
         __syncthreads();
       }
