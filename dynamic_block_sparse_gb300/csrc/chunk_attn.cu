@@ -27,6 +27,8 @@
 #include "common.cuh"
 #include "internal.h"
 
+#include <type_traits>
+
 namespace dsa {
 namespace {
 
@@ -148,10 +150,18 @@ DSA_DEV void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: 
 DSA_DEV void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 DSA_DEV void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
-// Arrives at an mbarrier when every tcgen05 operation this thread issued so far has completed.
-DSA_DEV void tc_commit(uint32_t bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
-               : "memory");
+// The issue warp runs converged on warp-uniform values, so that descriptors and addresses live in
+// uniform registers, and one lane's predicate guards each instruction: issued from inside a one-lane
+// branch, every product first moved its operands there (about 110 cycles a product against the 64 that
+// it takes).
+//
+// Arrives at an mbarrier when every tcgen05 operation the leader issued so far has completed.
+DSA_DEV void tc_commit(uint32_t bar, uint32_t leader) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\tsetp.ne.u32 e, %1, 0;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
+      "r"(leader)
+      : "memory");
 }
 
 // Shared-memory descriptor of a tile of 128-byte swizzled lines.  K-major (Q, K): 8-row groups 1024
@@ -167,19 +177,19 @@ DSA_DEV uint64_t smem_desc(uint32_t addr, uint32_t lbo) {
 constexpr uint32_t kIdesc = (1u << 4) | (1u << 7) | (1u << 10) | ((128u >> 3) << 17) | ((128u >> 4) << 24);
 constexpr uint32_t kIdescV = kIdesc | (1u << 16);
 
-DSA_DEV void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t acc) {
+DSA_DEV void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t acc, uint32_t leader) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(kIdesc), "r"(acc)
+      "{\n\t.reg .pred p, e;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 e, %5, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(kIdesc), "r"(acc), "r"(leader)
       : "memory");
 }
 
-DSA_DEV void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t acc) {
+DSA_DEV void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t acc, uint32_t leader) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(kIdescV), "r"(acc)
+      "{\n\t.reg .pred p, e;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 e, %5, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(kIdescV), "r"(acc), "r"(leader)
       : "memory");
 }
 
@@ -234,6 +244,37 @@ DSA_DEV long long warp_scan_ll(long long v, int lane) {
     if (lane >= o) v += u;
   }
   return v;
+}
+
+// Bits 0 .. x of a word (x below 0: none; above 31: all).
+DSA_DEV uint32_t bits_to(int x) {
+  return x < 0 ? 0u : 0xffffffffu >> (31 - min(x, 31));
+}
+
+DSA_DEV float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
+// Two fp32 lanes in one 64-bit register.
+DSA_DEV uint64_t pair2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+DSA_DEV void unpair2(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+DSA_DEV uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+DSA_DEV uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
 }
 
 // The d-th KV head of a kind (streaming or not), found by the whole warp; -1 when there is none.
@@ -574,16 +615,28 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == kMmaWarp) {
     // ============================================================================== issue warp
-    uint32_t seq = 0, pcnt[2] = {0, 0};
+    uint32_t seq = 0, pcnt0 = 0, pcnt1 = 0;
     bool ok = true;
+    const uint32_t leader = lane == 0;
+    auto uni = [](int v) { return __shfl_sync(0xffffffffu, v, 0); };
+    const uint32_t ut = uni(tmem), ubase = uni(smem_base);
     for (int u = 0; ok; ++u) {
       const int us = u & 1;
       if (!warp_wait(smem_u32(&ctl->ufull[us]), (u >> 1) & 1, abort, kv.status)) break;
-      const Unit un = ctl->unit[us];
+      struct {
+        int kb, ns, w0, len, split, n0;
+      } un;
+      const Unit& in = ctl->unit[us];
+      un.kb = uni(in.kb);
+      un.ns = uni(in.ns);
+      un.w0 = uni(in.w0);
+      un.len = uni(in.len);
+      un.split = uni(in.split);
+      un.n0 = uni(in.n0);
+      const int nk = uni(in.ke) - un.kb, valid = uni(in.valid);
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&ctl->uempty[us]));
-      if (!un.valid) break;
-      const int nk = un.ke - un.kb;
+      if (!valid) break;
       if (!warp_wait(smem_u32(&ctl->qfull), u & 1, abort, kv.status)) break;
       auto stage = [&](uint32_t pos) { return (seq + pos) % kRing; };
       auto wait_full = [&](uint32_t pos) {
@@ -592,36 +645,31 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       auto pos_k = [&](int kk) { return static_cast<uint32_t>(kk == 0 ? 0 : 2 * kk - 1); };
       auto pos_v = [&](int kk) { return static_cast<uint32_t>(kk + 1 < nk ? 2 * kk + 2 : 2 * kk + 1); };
-      auto commit = [&](unsigned long long* bar) {
-        if (lane == 0) tc_commit(smem_u32(bar));
-      };
+      auto commit = [&](unsigned long long* bar) { tc_commit(smem_u32(bar), leader); };
       auto qk = [&](int t, int kk) {  // S_t = Q K^T
-        if (lane == 0) {
-          const uint32_t q = smem_base + (un.split ? 0 : t) * kTileBytes;
-          const uint32_t kt = smem_base + kOffRing + stage(pos_k(kk)) * kTileBytes;
+        const uint32_t q = ubase + (un.split ? 0 : t) * kTileBytes;
+        const uint32_t kt = ubase + kOffRing + stage(pos_k(kk)) * kTileBytes;
+        const uint64_t dq = smem_desc(q, 16), dk = smem_desc(kt, 16);
 #pragma unroll
-          for (int ks = 0; ks < 8; ++ks) {
-            const uint32_t off = (ks >> 2) * kHalfBytes + (ks & 3) * 32;
-            mma_ss(tmem + kS0 + 128 * t, smem_desc(q + off, 16), smem_desc(kt + off, 16), ks > 0);
-          }
-          tc_commit(smem_u32(&ctl->sfull[t]));
+        for (int ks = 0; ks < 8; ++ks) {
+          constexpr uint32_t kHalf16 = kHalfBytes >> 4;
+          const uint32_t off = (ks >> 2) * kHalf16 + (ks & 3) * 2;
+          mma_ss(ut + kS0 + 128 * t, dq + off, dk + off, ks > 0, leader);
         }
-        __syncwarp();
+        commit(&ctl->sfull[t]);
       };
       auto pv = [&](int t, int kk, bool first) {  // O_t += P V
-        if (lane == 0) {
-          const uint32_t vt = smem_base + kOffRing + stage(pos_v(kk)) * kTileBytes;
+        const uint32_t vt = ubase + kOffRing + stage(pos_v(kk)) * kTileBytes;
+        const uint64_t dv = smem_desc(vt, kHalfBytes);
 #pragma unroll
-          for (int ks = 0; ks < 8; ++ks)
-            mma_ts(tmem + kO0 + 128 * t, tmem + kS0 + 128 * t + 8 * ks,
-                   smem_desc(vt + ks * 2048, kHalfBytes), ks > 0 || !first);
-          tc_commit(smem_u32(&ctl->odone[t]));
-        }
-        __syncwarp();
+        for (int ks = 0; ks < 8; ++ks)
+          mma_ts(ut + kO0 + 128 * t, ut + kS0 + 128 * t + 8 * ks, dv + ks * (2048 >> 4),
+                 ks > 0 || !first, leader);
+        commit(&ctl->odone[t]);
       };
       auto wait_p = [&](int t) {
-        const bool r = warp_wait(smem_u32(&ctl->pready[t]), pcnt[t] & 1, abort, kv.status);
-        ++pcnt[t];
+        const uint32_t ph = t ? pcnt1++ : pcnt0++;
+        const bool r = warp_wait(smem_u32(&ctl->pready[t]), ph & 1, abort, kv.status);
         tc_fence_after();
         return r;
       };
@@ -747,24 +795,27 @@ __global__ void __launch_bounds__(kThreads, 1)
           const bool cut = t0 + 127 > pos_lo || kmask != 0xffu ||
                            (un.win && t0 + 128 > a.sink && t0 <= pos_hi - a.local);
           if (cut) {
-            // columns a .. seen: up to the row's own position, and in the sink or the window
+            // the row's visible columns as bits: up to its own position, in the sink or the window
             const int hi = pos - t0, lo = un.win ? max(pos - a.local, -1) - t0 : -1;
-            const int sk = un.win ? a.sink - t0 : 0;
+            const int sk = un.win ? a.sink - t0 - 1 : -1;
 #pragma unroll
-            for (int e = 0; e < 128; ++e) {
-              const bool seen = e <= hi && (e > lo || e < sk) && (kmask >> (e >> 4) & 1);
-              if (!seen) s[e] = -INFINITY;
+            for (int w = 0; w < 4; ++w) {
+              const uint32_t groups = ((kmask >> (2 * w) & 1) ? 0x0000ffffu : 0u) |
+                                      ((kmask >> (2 * w + 1) & 1) ? 0xffff0000u : 0u);
+              const uint32_t seen = bits_to(hi - 32 * w) &
+                                    (~bits_to(lo - 32 * w) | bits_to(sk - 32 * w)) & groups;
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (!(seen >> e & 1)) s[32 * w + e] = -INFINITY;
             }
           }
-          float m0 = -INFINITY, m1 = -INFINITY, m2 = -INFINITY, m3 = -INFINITY;
+          float m0 = s[0], m1 = s[1];
 #pragma unroll
-          for (int e = 0; e < 128; e += 4) {
-            m0 = fmaxf(m0, s[e]);
-            m1 = fmaxf(m1, s[e + 1]);
-            m2 = fmaxf(m2, s[e + 2]);
-            m3 = fmaxf(m3, s[e + 3]);
+          for (int e = 2; e < 126; e += 4) {
+            m0 = max3(m0, s[e], s[e + 1]);
+            m1 = max3(m1, s[e + 2], s[e + 3]);
           }
-          mtrue = fmaxf(mtrue, fmaxf(fmaxf(m0, m1), fmaxf(m2, m3)));
+          mtrue = max3(mtrue, max3(m0, s[126], s[127]), m1);
           const bool up = mtrue * sc > mref * sc + kLazyLog2;
           if (__any_sync(0xffffffffu, up)) {
             const float f = up ? fast_exp2((mref - mtrue) * sc) : 1.f;
@@ -785,26 +836,30 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           const float mm = mref > -INFINITY ? mref * sc : 0.f;
-          float l0 = 0.f, l1 = 0.f, l2 = 0.f, l3 = 0.f;
+          const uint64_t sc2 = pair2(sc, sc), mm2 = pair2(-mm, -mm);
+          uint64_t la = 0, lb = 0;  // (two zeros each)
 #pragma unroll
           for (int c0 = 0; c0 < 128; c0 += 64) {
             uint32_t p[32];
 #pragma unroll
             for (int e = 0; e < 64; e += 4) {
-              const float p0 = fast_exp2(fmaf(s[c0 + e], sc, -mm));
-              const float p1 = fast_exp2(fmaf(s[c0 + e + 1], sc, -mm));
-              const float p2 = fast_exp2(fmaf(s[c0 + e + 2], sc, -mm));
-              const float p3 = fast_exp2(fmaf(s[c0 + e + 3], sc, -mm));
-              l0 += p0;
-              l1 += p1;
-              l2 += p2;
-              l3 += p3;
-              p[e / 2] = pack_bf16(p0, p1);
-              p[e / 2 + 1] = pack_bf16(p2, p3);
+              float x0, x1, x2, x3;
+              unpair2(fma2(pair2(s[c0 + e], s[c0 + e + 1]), sc2, mm2), x0, x1);
+              unpair2(fma2(pair2(s[c0 + e + 2], s[c0 + e + 3]), sc2, mm2), x2, x3);
+              x0 = fast_exp2(x0);
+              x1 = fast_exp2(x1);
+              x2 = fast_exp2(x2);
+              x3 = fast_exp2(x3);
+              la = add2(la, pair2(x0, x1));
+              lb = add2(lb, pair2(x2, x3));
+              p[e / 2] = pack_bf16(x0, x1);
+              p[e / 2 + 1] = pack_bf16(x2, x3);
             }
             tmem_st_32(tS + c0 / 2, p);
           }
-          l += (l0 + l1) + (l2 + l3);
+          float l0, l1;
+          unpair2(add2(la, lb), l0, l1);
+          l += l0 + l1;
           tmem_wait_st();
         }
         tc_fence_before();
@@ -912,38 +967,66 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (!(ok = meet())) break;
         if (*const_cast<volatile int*>(&ctl->last)) {
-          // merge in CTA order: every thread takes (row, 4 dims) pairs, rows fastest
+          // merge in CTA order: `per` threads a row, each with every per-th float4 of it
           const int rows = un.ntok * G;
-          for (int e = tid; e < rows * 32; e += 256) {
-            const int mr = e % rows, c4 = e / rows;
-            float M = -INFINITY, Mt = -INFINITY;
+          int per = 1;
+          while (per < 32 && 2 * per * rows <= 256) per *= 2;
+          for (int r0 = 0; r0 < rows; r0 += 256 / per) {
+            const int mr = r0 + tid % (256 / per), sub = tid / (256 / per);
+            if (mr >= rows) continue;
+            auto record = [&](int q) {
+              return a.records + static_cast<size_t>(2 * (un.cta0 + q) + (q == 0)) * R * kRecordFloats;
+            };
+            float M = -INFINITY, Mt = -INFINITY, ls = 0.f;
+#pragma unroll 4
             for (int q = 0; q < parts; ++q) {
-              const float* rq = a.records + static_cast<size_t>(2 * (un.cta0 + q) + (q == 0)) * R *
-                                                kRecordFloats;
-              M = fmaxf(M, __ldcg(rq + 128 * R + mr));
-              Mt = fmaxf(Mt, __ldcg(rq + 130 * R + mr));
+              M = fmaxf(M, __ldcg(record(q) + 128 * R + mr));
+              Mt = fmaxf(Mt, __ldcg(record(q) + 130 * R + mr));
             }
             const float Mz = M > -INFINITY ? M : 0.f;
-            float ls = 0.f;
-            float4 os = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int q = 0; q < parts; ++q) {
-              const float* rq = a.records + static_cast<size_t>(2 * (un.cta0 + q) + (q == 0)) * R *
-                                                kRecordFloats;
-              const float wq = fast_exp2((__ldcg(rq + 128 * R + mr) - Mz) * sc);
-              ls += __ldcg(rq + 129 * R + mr) * wq;
-              const float4 v = __ldcg(reinterpret_cast<const float4*>(rq) + static_cast<size_t>(c4) * R + mr);
-              os.x = fmaf(v.x, wq, os.x);
-              os.y = fmaf(v.y, wq, os.y);
-              os.z = fmaf(v.z, wq, os.z);
-              os.w = fmaf(v.w, wq, os.w);
-            }
+#pragma unroll 4
+            for (int q = 0; q < parts; ++q)
+              ls += __ldcg(record(q) + 129 * R + mr) *
+                    fast_exp2((__ldcg(record(q) + 128 * R + mr) - Mz) * sc);
             const float iv = ls == 0.f ? 0.f : 1.f / ls;
             const size_t at = static_cast<size_t>(un.tok0 + mr / G) * kv.Hq + un.h * G + mr % G;
-            uint2 v;
-            v.x = pack_bf16(os.x * iv, os.y * iv);
-            v.y = pack_bf16(os.z * iv, os.w * iv);
-            *reinterpret_cast<uint2*>(a.out + at * kHeadDim + 4 * c4) = v;
-            if (c4 == 0) {
+            auto sum = [&](auto width, int c_first) {  // `width` float4s, per apart
+              constexpr int N = decltype(width)::value;
+              float4 o[N];
+#pragma unroll
+              for (int e = 0; e < N; ++e) o[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll (N >= 8 ? 1 : 8 / N)
+              for (int q = 0; q < parts; ++q) {
+                const float* rq = record(q);
+                float4 v[N];
+#pragma unroll
+                for (int e = 0; e < N; ++e)
+                  v[e] = __ldcg(reinterpret_cast<const float4*>(rq) +
+                                static_cast<size_t>(c_first + e * per) * R + mr);
+                const float wq = fast_exp2((__ldcg(rq + 128 * R + mr) - Mz) * sc);
+#pragma unroll
+                for (int e = 0; e < N; ++e) {
+                  o[e].x = fmaf(v[e].x, wq, o[e].x);
+                  o[e].y = fmaf(v[e].y, wq, o[e].y);
+                  o[e].z = fmaf(v[e].z, wq, o[e].z);
+                  o[e].w = fmaf(v[e].w, wq, o[e].w);
+                }
+              }
+#pragma unroll
+              for (int e = 0; e < N; ++e) {
+                uint2 v;
+                v.x = pack_bf16(o[e].x * iv, o[e].y * iv);
+                v.y = pack_bf16(o[e].z * iv, o[e].w * iv);
+                *reinterpret_cast<uint2*>(a.out + at * kHeadDim + 4 * (c_first + e * per)) = v;
+              }
+            };
+            if (per <= 2)
+              for (int c = sub; c < 32; c += 16 * per) sum(std::integral_constant<int, 16>(), c);
+            else if (per <= 8)
+              for (int c = sub; c < 32; c += 4 * per) sum(std::integral_constant<int, 4>(), c);
+            else
+              for (int c = sub; c < 32; c += per) sum(std::integral_constant<int, 1>(), c);
+            if (sub == 0) {
               if (a.m) a.m[at] = Mt * sc * kLn2;
               if (a.l) a.l[at] = Mt > -INFINITY ? ls * fast_exp2((M - Mt) * sc) : ls;
             }
