@@ -40,8 +40,8 @@ constexpr uint32_t kTileBytes = 2 * kHalfBytes;
 constexpr float kLazyLog2 = 8.f;  // P stays below 2^8 times its weight at the true maximum
 
 // Registers per thread: a softmax thread holds a row of 128 logits.  The launch has 168 x 384 = 64512,
-// and 200 x 256 + 104 x 128 is exactly that.
-constexpr int kSoftmaxRegs = 200, kOtherRegs = 104;
+// and 208 x 256 + 88 x 128 is exactly that.
+constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
 static_assert(kSoftmaxRegs * 256 + kOtherRegs * 128 <= 168 * kThreads, "registers of the launch");
 template <int N>
 DSA_DEV void regs_inc() {
@@ -68,7 +68,7 @@ constexpr uint32_t kOffRing = 2 * kTileBytes;
 constexpr uint32_t kOffCtl = kOffRing + kRing * kTileBytes;
 struct Ctl {
   unsigned long long full[kRing], empty[kRing];
-  unsigned long long qfull, qempty, sfull[2], pready[2], odone[2], ufull[2], uempty[2], both;
+  unsigned long long qfull, qempty, sfull[2], pready[2][2], odone[2], ufull[2], uempty[2], both;
   uint32_t tmem;
   int abort, last, pad;
   Unit unit[2];
@@ -133,6 +133,16 @@ DSA_DEV void tmem_ld_128(uint32_t addr, uint32_t (&r)[128]) {
       : "r"(addr));
 }
 
+DSA_DEV void tmem_st_16(uint32_t addr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+      "%11, %12, %13, %14, %15, %16};"
+      :: "r"(addr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]),
+        "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]),
+        "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+
 DSA_DEV void tmem_st_32(uint32_t addr, const uint32_t (&r)[32]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
@@ -150,18 +160,18 @@ DSA_DEV void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: 
 DSA_DEV void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 DSA_DEV void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
-// The issue warp runs converged on warp-uniform values, so that descriptors and addresses live in
-// uniform registers, and one lane's predicate guards each instruction: issued from inside a one-lane
-// branch, every product first moved its operands there (about 110 cycles a product against the 64 that
-// it takes).
-//
-// Arrives at an mbarrier when every tcgen05 operation the leader issued so far has completed.
-DSA_DEV void tc_commit(uint32_t bar, uint32_t leader) {
-  asm volatile(
-      "{\n\t.reg .pred e;\n\tsetp.ne.u32 e, %1, 0;\n\t"
-      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
-      "r"(leader)
-      : "memory");
+// One lane of the converged warp.
+DSA_DEV bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\tselp.u32 %0, 1, 0, e;\n\t}"
+               : "=r"(r));
+  return r != 0;
+}
+
+// Arrives at an mbarrier when every tcgen05 operation this thread issued so far has completed.
+DSA_DEV void tc_commit(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
+               : "memory");
 }
 
 // Shared-memory descriptor of a tile of 128-byte swizzled lines.  K-major (Q, K): 8-row groups 1024
@@ -177,19 +187,19 @@ DSA_DEV uint64_t smem_desc(uint32_t addr, uint32_t lbo) {
 constexpr uint32_t kIdesc = (1u << 4) | (1u << 7) | (1u << 10) | ((128u >> 3) << 17) | ((128u >> 4) << 24);
 constexpr uint32_t kIdescV = kIdesc | (1u << 16);
 
-DSA_DEV void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t acc, uint32_t leader) {
+DSA_DEV void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t acc) {
   asm volatile(
-      "{\n\t.reg .pred p, e;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 e, %5, 0;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(kIdesc), "r"(acc), "r"(leader)
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(kIdesc), "r"(acc)
       : "memory");
 }
 
-DSA_DEV void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t acc, uint32_t leader) {
+DSA_DEV void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t acc) {
   asm volatile(
-      "{\n\t.reg .pred p, e;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 e, %5, 0;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(kIdescV), "r"(acc), "r"(leader)
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(kIdescV), "r"(acc)
       : "memory");
 }
 
@@ -319,7 +329,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(smem_u32(&ctl->qempty), 1);
     for (int t = 0; t < 2; ++t) {
       mbar_init(smem_u32(&ctl->sfull[t]), 1);
-      mbar_init(smem_u32(&ctl->pready[t]), 4);   // one arrival per softmax warp
+      mbar_init(smem_u32(&ctl->pready[t][0]), 4);  // one arrival per softmax warp
+      mbar_init(smem_u32(&ctl->pready[t][1]), 4);
       mbar_init(smem_u32(&ctl->odone[t]), 1);
       mbar_init(smem_u32(&ctl->ufull[t]), 1);
       mbar_init(smem_u32(&ctl->uempty[t]), 9);   // eight softmax warps and the issue warp
@@ -617,7 +628,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ============================================================================== issue warp
     uint32_t seq = 0, pcnt0 = 0, pcnt1 = 0;
     bool ok = true;
-    const uint32_t leader = lane == 0;
     auto uni = [](int v) { return __shfl_sync(0xffffffffu, v, 0); };
     const uint32_t ut = uni(tmem), ubase = uni(smem_base);
     for (int u = 0; ok; ++u) {
@@ -645,33 +655,45 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       auto pos_k = [&](int kk) { return static_cast<uint32_t>(kk == 0 ? 0 : 2 * kk - 1); };
       auto pos_v = [&](int kk) { return static_cast<uint32_t>(kk + 1 < nk ? 2 * kk + 2 : 2 * kk + 1); };
-      auto commit = [&](unsigned long long* bar) { tc_commit(smem_u32(bar), leader); };
+      // (elect_one picks the same lane every time, so a commit covers all products issued before it)
+      auto commit = [&](unsigned long long* bar) {
+        if (elect_one()) tc_commit(smem_u32(bar));
+        __syncwarp();
+      };
       auto qk = [&](int t, int kk) {  // S_t = Q K^T
         const uint32_t q = ubase + (un.split ? 0 : t) * kTileBytes;
         const uint32_t kt = ubase + kOffRing + stage(pos_k(kk)) * kTileBytes;
         const uint64_t dq = smem_desc(q, 16), dk = smem_desc(kt, 16);
+        if (elect_one()) {
 #pragma unroll
-        for (int ks = 0; ks < 8; ++ks) {
-          constexpr uint32_t kHalf16 = kHalfBytes >> 4;
-          const uint32_t off = (ks >> 2) * kHalf16 + (ks & 3) * 2;
-          mma_ss(ut + kS0 + 128 * t, dq + off, dk + off, ks > 0, leader);
+          for (int ks = 0; ks < 8; ++ks) {
+            constexpr uint32_t kHalf16 = kHalfBytes >> 4;
+            const uint32_t off = (ks >> 2) * kHalf16 + (ks & 3) * 2;
+            mma_ss(ut + kS0 + 128 * t, dq + off, dk + off, ks > 0);
+          }
+          tc_commit(smem_u32(&ctl->sfull[t]));
         }
-        commit(&ctl->sfull[t]);
+        __syncwarp();
       };
-      auto pv = [&](int t, int kk, bool first) {  // O_t += P V
+      // O_t += P V, in two halves of 64 keys as the softmax delivers them
+      auto pv = [&](int t, int kk, bool first) {
         const uint32_t vt = ubase + kOffRing + stage(pos_v(kk)) * kTileBytes;
         const uint64_t dv = smem_desc(vt, kHalfBytes);
-#pragma unroll
-        for (int ks = 0; ks < 8; ++ks)
-          mma_ts(ut + kO0 + 128 * t, ut + kS0 + 128 * t + 8 * ks, dv + ks * (2048 >> 4),
-                 ks > 0 || !first, leader);
-        commit(&ctl->odone[t]);
-      };
-      auto wait_p = [&](int t) {
         const uint32_t ph = t ? pcnt1++ : pcnt0++;
-        const bool r = warp_wait(smem_u32(&ctl->pready[t]), ph & 1, abort, kv.status);
-        tc_fence_after();
-        return r;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          if (!warp_wait(smem_u32(&ctl->pready[t][half]), ph & 1, abort, kv.status)) return false;
+          tc_fence_after();
+          if (elect_one()) {
+#pragma unroll
+            for (int ks = 4 * half; ks < 4 * half + 4; ++ks)
+              mma_ts(ut + kO0 + 128 * t, ut + kS0 + 128 * t + 8 * ks, dv + ks * (2048 >> 4),
+                     ks > 0 || !first);
+            if (half == 1) tc_commit(smem_u32(&ctl->odone[t]));
+          }
+          __syncwarp();
+        }
+        return true;
       };
       // V rows behind the request's last token share its page: whatever they hold must not reach the
       // product, where it would meet P = 0
@@ -702,15 +724,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = wait_v(kk);
           if (!ok) break;
           if (kk < un.n0) {
-            if (!(ok = wait_p(0))) break;
-            pv(0, kk, kk == 0);
+            if (!(ok = pv(0, kk, kk == 0))) break;
           }
           if (kk + 1 < nk) {
             if (!(ok = wait_full(pos_k(kk + 1)))) break;
             if (kk + 1 < un.n0) qk(0, kk + 1);
           }
-          if (!(ok = wait_p(1))) break;
-          pv(1, kk, kk == 0);
+          if (!(ok = pv(1, kk, kk == 0))) break;
           commit(&ctl->empty[stage(pos_v(kk))]);
           if (kk + 1 < nk) {
             qk(1, kk + 1);
@@ -730,8 +750,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int kk = 0; kk < nk && ok; ++kk) {
           const int t = kk & 1;
           if (!(ok = wait_v(kk))) break;
-          if (!(ok = wait_p(t))) break;
-          pv(t, kk, kk < 2);
+          if (!(ok = pv(t, kk, kk < 2))) break;
           commit(&ctl->empty[stage(pos_v(kk))]);
           if (kk + 2 < nk) {
             if (!(ok = wait_full(pos_k(kk + 2)))) break;
@@ -794,7 +813,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t kmask = *const_cast<volatile uint32_t*>(&ctl->kmask[(tiles + kk) & 7]);
           const bool cut = t0 + 127 > pos_lo || kmask != 0xffu ||
                            (un.win && t0 + 128 > a.sink && t0 <= pos_hi - a.local);
-          if (cut) {
+          if (__any_sync(0xffffffffu, cut)) {
             // the row's visible columns as bits: up to its own position, in the sink or the window
             const int hi = pos - t0, lo = un.win ? max(pos - a.local, -1) - t0 : -1;
             const int sk = un.win ? a.sink - t0 - 1 : -1;
@@ -809,13 +828,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!(seen >> e & 1)) s[32 * w + e] = -INFINITY;
             }
           }
-          float m0 = s[0], m1 = s[1];
+          float m0 = fmaxf(s[0], s[1]), m1 = fmaxf(s[2], s[3]), m2 = fmaxf(s[4], s[5]),
+                m3 = fmaxf(s[6], s[7]);
 #pragma unroll
-          for (int e = 2; e < 126; e += 4) {
+          for (int e = 8; e < 128; e += 8) {
             m0 = max3(m0, s[e], s[e + 1]);
             m1 = max3(m1, s[e + 2], s[e + 3]);
+            m2 = max3(m2, s[e + 4], s[e + 5]);
+            m3 = max3(m3, s[e + 6], s[e + 7]);
           }
-          mtrue = max3(mtrue, max3(m0, s[126], s[127]), m1);
+          mtrue = max3(mtrue, max3(m0, m1, m2), m3);
           const bool up = mtrue * sc > mref * sc + kLazyLog2;
           if (__any_sync(0xffffffffu, up)) {
             const float f = up ? fast_exp2((mref - mtrue) * sc) : 1.f;
@@ -839,10 +861,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint64_t sc2 = pair2(sc, sc), mm2 = pair2(-mm, -mm);
           uint64_t la = 0, lb = 0;  // (two zeros each)
 #pragma unroll
-          for (int c0 = 0; c0 < 128; c0 += 64) {
-            uint32_t p[32];
+          for (int c0 = 0; c0 < 128; c0 += 32) {
+            uint32_t p[16];
 #pragma unroll
-            for (int e = 0; e < 64; e += 4) {
+            for (int e = 0; e < 32; e += 4) {
               float x0, x1, x2, x3;
               unpair2(fma2(pair2(s[c0 + e], s[c0 + e + 1]), sc2, mm2), x0, x1);
               unpair2(fma2(pair2(s[c0 + e + 2], s[c0 + e + 3]), sc2, mm2), x2, x3);
@@ -855,16 +877,21 @@ __global__ void __launch_bounds__(kThreads, 1)
               p[e / 2] = pack_bf16(x0, x1);
               p[e / 2 + 1] = pack_bf16(x2, x3);
             }
-            tmem_st_32(tS + c0 / 2, p);
+            tmem_st_16(tS + c0 / 2, p);
+            if (c0 % 64 == 32) {  // this half of P is complete
+              tmem_wait_st();
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(smem_u32(&ctl->pready[t][c0 / 64]));
+            }
           }
           float l0, l1;
           unpair2(add2(la, lb), l0, l1);
           l += l0 + l1;
-          tmem_wait_st();
+        } else if (lane == 0) {  // no live row in this warp: what P holds for it does not matter
+          mbar_arrive(smem_u32(&ctl->pready[t][0]));
+          mbar_arrive(smem_u32(&ctl->pready[t][1]));
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&ctl->pready[t]));
       }
       if (!ok) break;
       // ---- the unit's end: this stream's last product
