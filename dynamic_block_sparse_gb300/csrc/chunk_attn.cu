@@ -95,18 +95,14 @@ DSA_DEV void tmem_ld_32(uint32_t addr, uint32_t (&r)[32]) {
       : "r"(addr));
 }
 
-// 128 columns of this thread's TMEM lane.
-DSA_DEV void tmem_ld_128(uint32_t addr, uint32_t (&r)[128]) {
+// 64 columns of this thread's TMEM lane.
+DSA_DEV void tmem_ld_64(uint32_t addr, uint32_t (&r)[64]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x128.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+      "tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
       "%11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, "
       "%28, %29, %30, %31, %32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, "
       "%45, %46, %47, %48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, "
-      "%62, %63, %64, %65, %66, %67, %68, %69, %70, %71, %72, %73, %74, %75, %76, %77, %78, "
-      "%79, %80, %81, %82, %83, %84, %85, %86, %87, %88, %89, %90, %91, %92, %93, %94, %95, "
-      "%96, %97, %98, %99, %100, %101, %102, %103, %104, %105, %106, %107, %108, %109, %110, "
-      "%111, %112, %113, %114, %115, %116, %117, %118, %119, %120, %121, %122, %123, %124, "
-      "%125, %126, %127}, [%128];\n\t"
+      "%62, %63}, [%64];\n\t"
       "tcgen05.wait::ld.sync.aligned;"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
         "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
@@ -118,18 +114,7 @@ DSA_DEV void tmem_ld_128(uint32_t addr, uint32_t (&r)[128]) {
         "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]), "=r"(r[48]),
         "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]),
         "=r"(r[55]), "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]),
-        "=r"(r[61]), "=r"(r[62]), "=r"(r[63]), "=r"(r[64]), "=r"(r[65]), "=r"(r[66]),
-        "=r"(r[67]), "=r"(r[68]), "=r"(r[69]), "=r"(r[70]), "=r"(r[71]), "=r"(r[72]),
-        "=r"(r[73]), "=r"(r[74]), "=r"(r[75]), "=r"(r[76]), "=r"(r[77]), "=r"(r[78]),
-        "=r"(r[79]), "=r"(r[80]), "=r"(r[81]), "=r"(r[82]), "=r"(r[83]), "=r"(r[84]),
-        "=r"(r[85]), "=r"(r[86]), "=r"(r[87]), "=r"(r[88]), "=r"(r[89]), "=r"(r[90]),
-        "=r"(r[91]), "=r"(r[92]), "=r"(r[93]), "=r"(r[94]), "=r"(r[95]), "=r"(r[96]),
-        "=r"(r[97]), "=r"(r[98]), "=r"(r[99]), "=r"(r[100]), "=r"(r[101]), "=r"(r[102]),
-        "=r"(r[103]), "=r"(r[104]), "=r"(r[105]), "=r"(r[106]), "=r"(r[107]), "=r"(r[108]),
-        "=r"(r[109]), "=r"(r[110]), "=r"(r[111]), "=r"(r[112]), "=r"(r[113]), "=r"(r[114]),
-        "=r"(r[115]), "=r"(r[116]), "=r"(r[117]), "=r"(r[118]), "=r"(r[119]), "=r"(r[120]),
-        "=r"(r[121]), "=r"(r[122]), "=r"(r[123]), "=r"(r[124]), "=r"(r[125]), "=r"(r[126]),
-        "=r"(r[127])
+        "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
       : "r"(addr));
 }
 
@@ -285,6 +270,44 @@ DSA_DEV uint64_t add2(uint64_t a, uint64_t b) {
   uint64_t d;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
+}
+
+// The largest of 64 logits (as their bits) and m.
+DSA_DEV float row_max(const uint32_t (&r)[64], float m) {
+  float m0 = m, m1 = __uint_as_float(r[0]), m2 = __uint_as_float(r[1]), m3 = __uint_as_float(r[2]);
+  m0 = max3(m0, __uint_as_float(r[3]), __uint_as_float(r[4]));
+  m1 = max3(m1, __uint_as_float(r[5]), __uint_as_float(r[6]));
+  m2 = max3(m2, __uint_as_float(r[7]), __uint_as_float(r[8]));
+#pragma unroll
+  for (int e = 9; e < 57; e += 8) {
+    m3 = max3(m3, __uint_as_float(r[e]), __uint_as_float(r[e + 1]));
+    m0 = max3(m0, __uint_as_float(r[e + 2]), __uint_as_float(r[e + 3]));
+    m1 = max3(m1, __uint_as_float(r[e + 4]), __uint_as_float(r[e + 5]));
+    m2 = max3(m2, __uint_as_float(r[e + 6]), __uint_as_float(r[e + 7]));
+  }
+  m3 = max3(m3, __uint_as_float(r[57]), __uint_as_float(r[58]));
+  m0 = max3(m0, __uint_as_float(r[59]), __uint_as_float(r[60]));
+  m1 = max3(m1, __uint_as_float(r[61]), __uint_as_float(r[62]));
+  return max3(max3(m0, m1, m2), m3, __uint_as_float(r[63]));
+}
+
+// p = bf16 pairs of 2^(s sc - mm) for 32 logits, their sum into (la, lb).
+DSA_DEV void expo(const uint32_t* r, uint64_t sc2, uint64_t mm2, uint64_t& la, uint64_t& lb,
+                  uint32_t (&p)[16]) {
+#pragma unroll
+  for (int e = 0; e < 32; e += 4) {
+    float x0, x1, x2, x3;
+    unpair2(fma2(pair2(__uint_as_float(r[e]), __uint_as_float(r[e + 1])), sc2, mm2), x0, x1);
+    unpair2(fma2(pair2(__uint_as_float(r[e + 2]), __uint_as_float(r[e + 3])), sc2, mm2), x2, x3);
+    x0 = fast_exp2(x0);
+    x1 = fast_exp2(x1);
+    x2 = fast_exp2(x2);
+    x3 = fast_exp2(x3);
+    la = add2(la, pair2(x0, x1));
+    lb = add2(lb, pair2(x2, x3));
+    p[e / 2] = pack_bf16(x0, x1);
+    p[e / 2 + 1] = pack_bf16(x2, x3);
+  }
 }
 
 // The d-th KV head of a kind (streaming or not), found by the whole warp; -1 when there is none.
@@ -784,18 +807,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int u = 0; ok; ++u) {
       const int us = u & 1;
       if (!warp_wait(smem_u32(&ctl->ufull[us]), (u >> 1) & 1, abort, kv.status)) break;
-      const Unit un = ctl->unit[us];
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&ctl->uempty[us]));
+      // (read from shared memory where it is used: the loop below needs the registers for the row)
+      const volatile Unit& un = ctl->unit[us];
       if (!un.valid) break;
       const int nk = un.ke - un.kb;
       const int nt = un.split ? (nk + 1 - t) / 2 : t == 0 ? un.n0 : nk;
       const int my_tok = (un.split ? 0 : t * TQ) + r_tok;  // token of the unit
       const bool live = r_tok < TQ && my_tok < un.ntok;
       const bool any = __any_sync(0xffffffffu, live);
-      const int pos = un.pos0 + min(my_tok, un.ntok - 1);
       const int pos_lo = un.pos0 + (un.split ? 0 : t * TQ);
-      const int pos_hi = un.pos0 + min(un.ntok, (un.split ? 1 : t + 1) * TQ) - 1;
       float mref = -INFINITY, mtrue = -INFINITY, l = 0.f;
       for (int j = 0; j < nt; ++j) {
         if (!(ok = warp_wait(smem_u32(&ctl->sfull[t]), scnt & 1, abort, kv.status))) break;
@@ -805,39 +825,43 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int kk = un.split ? 2 * j + t : j;
           const int list = un.kb + kk;
           const int t0 = (list < un.ns ? list : un.w0 + list - un.ns) * 128;
-          uint32_t raw[128];
-          tmem_ld_128(tS, raw);
-          float s[128];
-#pragma unroll
-          for (int e = 0; e < 128; ++e) s[e] = __uint_as_float(raw[e]);
           const uint32_t kmask = *const_cast<volatile uint32_t*>(&ctl->kmask[(tiles + kk) & 7]);
-          const bool cut = t0 + 127 > pos_lo || kmask != 0xffu ||
-                           (un.win && t0 + 128 > a.sink && t0 <= pos_hi - a.local);
+          const bool win = un.win;
+          bool cut = t0 + 127 > pos_lo || kmask != 0xffu;
+          if (win)  // (the stream's last row sees least of the window's far end)
+            cut |= t0 + 128 > a.sink &&
+                   t0 <= un.pos0 + min(un.ntok, (un.split ? 1 : t + 1) * TQ) - 1 - a.local;
           if (__any_sync(0xffffffffu, cut)) {
-            // the row's visible columns as bits: up to its own position, in the sink or the window
-            const int hi = pos - t0, lo = un.win ? max(pos - a.local, -1) - t0 : -1;
-            const int sk = un.win ? a.sink - t0 - 1 : -1;
-#pragma unroll
+            const int pos = un.pos0 + min(my_tok, un.ntok - 1);
+            // Tiles at an edge of the mask are masked in TMEM first, so that the common path below
+            // holds its row in the registers the load wrote.  The row's visible columns as bits: up to
+            // its own position, in the sink or the window, on good pages.
+            const int hi = pos - t0, lo = win ? max(pos - a.local, -1) - t0 : -1;
+            const int sk = win ? a.sink - t0 - 1 : -1;
+#pragma unroll 1
             for (int w = 0; w < 4; ++w) {
               const uint32_t groups = ((kmask >> (2 * w) & 1) ? 0x0000ffffu : 0u) |
                                       ((kmask >> (2 * w + 1) & 1) ? 0xffff0000u : 0u);
               const uint32_t seen = bits_to(hi - 32 * w) &
                                     (~bits_to(lo - 32 * w) | bits_to(sk - 32 * w)) & groups;
+              if (__all_sync(0xffffffffu, seen == 0xffffffffu)) continue;
+              uint32_t r[32];
+              tmem_ld_32(tS + 32 * w, r);
 #pragma unroll
               for (int e = 0; e < 32; ++e)
-                if (!(seen >> e & 1)) s[32 * w + e] = -INFINITY;
+                if (!(seen >> e & 1)) r[e] = 0xff800000u;  // -inf
+              tmem_st_32(tS + 32 * w, r);
             }
+            tmem_wait_st();
           }
-          float m0 = fmaxf(s[0], s[1]), m1 = fmaxf(s[2], s[3]), m2 = fmaxf(s[4], s[5]),
-                m3 = fmaxf(s[6], s[7]);
-#pragma unroll
-          for (int e = 8; e < 128; e += 8) {
-            m0 = max3(m0, s[e], s[e + 1]);
-            m1 = max3(m1, s[e + 2], s[e + 3]);
-            m2 = max3(m2, s[e + 4], s[e + 5]);
-            m3 = max3(m3, s[e + 6], s[e + 7]);
-          }
-          mtrue = max3(mtrue, max3(m0, m1, m2), m3);
+          // The maximum needs all 128 columns, the exponentials take them 32 at a time: the second
+          // half is read twice, so that a thread holds 64 of them at most.
+          uint32_t ra[64];
+          tmem_ld_64(tS + 64, ra);
+          float m0 = row_max(ra, mtrue);
+          tmem_ld_64(tS, ra);
+          m0 = row_max(ra, m0);
+          mtrue = m0;
           const bool up = mtrue * sc > mref * sc + kLazyLog2;
           if (__any_sync(0xffffffffu, up)) {
             const float f = up ? fast_exp2((mref - mtrue) * sc) : 1.f;
@@ -860,31 +884,24 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float mm = mref > -INFINITY ? mref * sc : 0.f;
           const uint64_t sc2 = pair2(sc, sc), mm2 = pair2(-mm, -mm);
           uint64_t la = 0, lb = 0;  // (two zeros each)
-#pragma unroll
-          for (int c0 = 0; c0 < 128; c0 += 32) {
-            uint32_t p[16];
-#pragma unroll
-            for (int e = 0; e < 32; e += 4) {
-              float x0, x1, x2, x3;
-              unpair2(fma2(pair2(s[c0 + e], s[c0 + e + 1]), sc2, mm2), x0, x1);
-              unpair2(fma2(pair2(s[c0 + e + 2], s[c0 + e + 3]), sc2, mm2), x2, x3);
-              x0 = fast_exp2(x0);
-              x1 = fast_exp2(x1);
-              x2 = fast_exp2(x2);
-              x3 = fast_exp2(x3);
-              la = add2(la, pair2(x0, x1));
-              lb = add2(lb, pair2(x2, x3));
-              p[e / 2] = pack_bf16(x0, x1);
-              p[e / 2 + 1] = pack_bf16(x2, x3);
-            }
-            tmem_st_16(tS + c0 / 2, p);
-            if (c0 % 64 == 32) {  // this half of P is complete
-              tmem_wait_st();
-              tc_fence_before();
-              __syncwarp();
-              if (lane == 0) mbar_arrive(smem_u32(&ctl->pready[t][c0 / 64]));
-            }
-          }
+          auto deliver = [&](int half) {
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&ctl->pready[t][half]));
+          };
+          uint32_t p[16];
+          expo(ra, sc2, mm2, la, lb, p);
+          tmem_st_16(tS, p);
+          expo(ra + 32, sc2, mm2, la, lb, p);
+          tmem_st_16(tS + 16, p);
+          deliver(0);
+          tmem_ld_64(tS + 64, ra);
+          expo(ra, sc2, mm2, la, lb, p);
+          tmem_st_16(tS + 32, p);
+          expo(ra + 32, sc2, mm2, la, lb, p);
+          tmem_st_16(tS + 48, p);
+          deliver(1);
           float l0, l1;
           unpair2(add2(la, lb), l0, l1);
           l += l0 + l1;
@@ -1060,6 +1077,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&ctl->uempty[us]));
     }
   }
   __syncthreads();
