@@ -241,6 +241,19 @@ DSA_DEV long long warp_scan_ll(long long v, int lane) {
   return v;
 }
 
+// 32 bytes in one store; 16 where the rows of the caller's tensor are not 32-byte aligned.
+DSA_DEV void store32(void* dst, const uint32_t (&v)[8]) {
+  if ((reinterpret_cast<uintptr_t>(dst) & 31) == 0) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(v[0]),
+                 "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+  } else {
+    uint4* d = static_cast<uint4*>(dst);
+    d[0] = make_uint4(v[0], v[1], v[2], v[3]);
+    d[1] = make_uint4(v[4], v[5], v[6], v[7]);
+  }
+}
+
 // Bits 0 .. x of a word (x below 0: none; above 31: all).
 DSA_DEV uint32_t bits_to(int x) {
   return x < 0 ? 0u : 0xffffffffu >> (31 - min(x, 31));
@@ -542,20 +555,33 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       __syncwarp();
 
-      // key rows of a tile for this lane's piece; bit s of *bad: piece s lies on a bad page
-      auto piece_row = [&](int kk, uint32_t* bad) {
-        const int tile = kk < un.ns ? kk : un.w0 + kk - un.ns;
-        const int s = tile * 128 + my_seg * seg;
-        int row = oob;
-        bool is_bad = false;
-        if (loads && s < len) {
-          const int j = s / kv.p;
-          const int phys = kv.page_table[static_cast<size_t>(b) * kv.max_pages + j];
-          is_bad = phys < 0 || phys >= kv.num_phys;
-          if (!is_bad) row = (phys * kv.Hkv + h) * kv.p + (s - j * kv.p);
+      // This lane's piece of a key tile: its page-table entry (-2: behind the request's tokens), read
+      // two tiles ahead of its use, and the pool row that it gives.
+      auto piece_token = [&](int kk) {
+        const int list = un.kb + kk;
+        return (list < un.ns ? list : un.w0 + list - un.ns) * 128 + my_seg * seg;
+      };
+      auto piece_page = [&](int kk) {
+        const int s = piece_token(kk);
+        if (!loads || s >= len) return -2;
+        return max(kv.page_table[static_cast<size_t>(b) * kv.max_pages + s / kv.p], -1);
+      };
+      // the row (oob where there is nothing to load), and the tile's valid 16-token groups for the
+      // softmax
+      auto piece_row = [&](int kk, int phys) {
+        const bool good = phys >= 0 && phys < kv.num_phys;
+        const uint32_t bad =
+            __ballot_sync(0xffffffffu, phys != -2 && !good) & ((1u << nseg) - 1u);
+        if (lane == 0) {
+          uint32_t m = 0xffu;
+          if (bad) {
+            for (int s = 0; s < nseg; ++s)
+              if (bad >> s & 1) m &= ~(((1u << (seg / 16)) - 1u) << (s * (seg / 16)));
+            raise_status(kv.status, DSA_STATUS_BAD_PAGE);
+          }
+          ctl->kmask[(tiles + kk) & 7] = m;
         }
-        *bad = __ballot_sync(0xffffffffu, is_bad) & ((1u << nseg) - 1u);
-        return row;
+        return good ? (phys * kv.Hkv + h) * kv.p + piece_token(kk) % kv.p : oob;
       };
       auto load_tile = [&](uint32_t pos, const CUtensorMap* map, int row) {
         const uint32_t xx = seq + pos, st = xx % kRing, ph = xx / kRing;
@@ -568,19 +594,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                       map, row, my_half, bar);
         return true;
       };
-      auto note_mask = [&](int kk, uint32_t bad) {
-        if (lane == 0) {
-          uint32_t m = 0xffu;
-          for (int s = 0; s < nseg; ++s)
-            if (bad >> s & 1) m &= ~(((1u << (seg / 16)) - 1u) << (s * (seg / 16)));
-          ctl->kmask[(tiles + kk) & 7] = m;
-          if (bad) raise_status(kv.status, DSA_STATUS_BAD_PAGE);
-        }
-      };
-
-      uint32_t bad, bad_next = 0;
-      int row = piece_row(un.kb, &bad), row_next = oob;
-      if (nk > 1) row_next = piece_row(un.kb + 1, &bad_next);
+      const int page0 = piece_page(0);
+      int page_next = nk > 1 ? piece_page(1) : -2;
       if (u > 0 && !warp_wait(smem_u32(&ctl->qempty), (u - 1) & 1, abort, kv.status)) break;
       if (lane == 0) {
         const uint32_t bar = smem_u32(&ctl->qfull), bytes = static_cast<uint32_t>(G * TQ) * 128;
@@ -591,21 +606,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                        bar);
       }
       __syncwarp();
-      note_mask(0, bad);
+      int row = piece_row(0, page0);
       ok = load_tile(0, &tmK, row);
       for (int kk = 0; kk < nk && ok; ++kk) {
-        int row_after = oob;
-        uint32_t bad_after = 0;
-        if (kk + 2 < nk) row_after = piece_row(un.kb + kk + 2, &bad_after);
+        const int page_after = kk + 2 < nk ? piece_page(kk + 2) : -2;
         if (kk + 1 < nk) {
-          note_mask(kk + 1, bad_next);
+          const int row_next = piece_row(kk + 1, page_next);
           ok = load_tile(2 * kk + 1, &tmK, row_next) && load_tile(2 * kk + 2, &tmV, row);
+          row = row_next;
         } else {
           ok = load_tile(2 * kk + 1, &tmV, row);
         }
-        row = row_next;
-        row_next = row_after;
-        bad_next = bad_after;
+        page_next = page_after;
       }
       seq += 2 * nk;
       tiles += nk;
@@ -818,24 +830,29 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int pos_lo = un.pos0 + (un.split ? 0 : t * TQ);
       float mref = -INFINITY, mtrue = -INFINITY, l = 0.f;
       for (int j = 0; j < nt; ++j) {
+        // what needs no S is worked out before S is there
+        const int kk = un.split ? 2 * j + t : j;
+        const int list = un.kb + kk;
+        const int t0 = (list < un.ns ? list : un.w0 + list - un.ns) * 128;
+        const bool win = un.win;
+        bool cut = t0 + 127 > pos_lo;
+        if (win)  // (the stream's last row sees least of the window's far end)
+          cut |= t0 + 128 > a.sink &&
+                 t0 <= un.pos0 + min(un.ntok, (un.split ? 1 : t + 1) * TQ) - 1 - a.local;
         if (!(ok = warp_wait(smem_u32(&ctl->sfull[t]), scnt & 1, abort, kv.status))) break;
         ++scnt;
         tc_fence_after();
         if (any) {
-          const int kk = un.split ? 2 * j + t : j;
-          const int list = un.kb + kk;
-          const int t0 = (list < un.ns ? list : un.w0 + list - un.ns) * 128;
           const uint32_t kmask = *const_cast<volatile uint32_t*>(&ctl->kmask[(tiles + kk) & 7]);
-          const bool win = un.win;
-          bool cut = t0 + 127 > pos_lo || kmask != 0xffu;
-          if (win)  // (the stream's last row sees least of the window's far end)
-            cut |= t0 + 128 > a.sink &&
-                   t0 <= un.pos0 + min(un.ntok, (un.split ? 1 : t + 1) * TQ) - 1 - a.local;
-          if (__any_sync(0xffffffffu, cut)) {
+          // The maximum needs all 128 columns, the exponentials take them 32 at a time: the second
+          // half is read twice, so that a thread holds 64 of them at most.
+          uint32_t ra[64];
+          tmem_ld_64(tS + 64, ra);
+          if (__any_sync(0xffffffffu, cut || kmask != 0xffu)) {
+            // Tiles at an edge of the mask are masked in TMEM first, so that the common path holds its
+            // row in the registers the load wrote.  The row's visible columns as bits: up to its own
+            // position, in the sink or the window, on good pages.
             const int pos = un.pos0 + min(my_tok, un.ntok - 1);
-            // Tiles at an edge of the mask are masked in TMEM first, so that the common path below
-            // holds its row in the registers the load wrote.  The row's visible columns as bits: up to
-            // its own position, in the sink or the window, on good pages.
             const int hi = pos - t0, lo = win ? max(pos - a.local, -1) - t0 : -1;
             const int sk = win ? a.sink - t0 - 1 : -1;
 #pragma unroll 1
@@ -853,11 +870,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               tmem_st_32(tS + 32 * w, r);
             }
             tmem_wait_st();
+            tmem_ld_64(tS + 64, ra);
           }
-          // The maximum needs all 128 columns, the exponentials take them 32 at a time: the second
-          // half is read twice, so that a thread holds 64 of them at most.
-          uint32_t ra[64];
-          tmem_ld_64(tS + 64, ra);
           float m0 = row_max(ra, mtrue);
           tmem_ld_64(tS, ra);
           m0 = row_max(ra, m0);
@@ -964,13 +978,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (live) {
             if (un.whole) {
 #pragma unroll
-              for (int e = 0; e < 32; e += 8) {
-                uint4 v;
-                v.x = pack_bf16(o[e] * inv, o[e + 1] * inv);
-                v.y = pack_bf16(o[e + 2] * inv, o[e + 3] * inv);
-                v.z = pack_bf16(o[e + 4] * inv, o[e + 5] * inv);
-                v.w = pack_bf16(o[e + 6] * inv, o[e + 7] * inv);
-                *reinterpret_cast<uint4*>(dst + c0 + e) = v;
+              for (int e = 0; e < 32; e += 16) {  // whole 32-byte sectors
+                uint32_t v[8];
+#pragma unroll
+                for (int x = 0; x < 8; ++x)
+                  v[x] = pack_bf16(o[e + 2 * x] * inv, o[e + 2 * x + 1] * inv);
+                store32(dst + c0 + e, v);
               }
             } else {
 #pragma unroll
