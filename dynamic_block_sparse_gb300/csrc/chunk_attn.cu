@@ -22,8 +22,9 @@
 //
 // Inside a CTA: warps 0-3 and 4-7 are the streams' softmax warpgroups (a thread owns a row: S from
 // TMEM in one load, P back to TMEM over S as bf16), warp 8 loads (TMA: Q tiles, and K and V tiles of
-// 128 tokens assembled from page pieces into a ring of five 32 KB stages), warp 9 issues the tcgen05
-// products (S = Q K^T from shared memory, O += P V with P from TMEM).
+// 128 tokens assembled from page pieces into a ring of five 32 KB stages, K and V in turn), one thread
+// of warp 9 issues the tcgen05 products (S = Q K^T from shared memory, O += P V with P from TMEM), and
+// warp 10 clears the rows behind a request's last token in the V tile that holds it.
 #include "common.cuh"
 #include "internal.h"
 
@@ -33,7 +34,7 @@ namespace dsa {
 namespace {
 
 constexpr int kThreads = 384;
-constexpr int kLoadWarp = 8, kMmaWarp = 9;
+constexpr int kLoadWarp = 8, kMmaWarp = 9, kTailWarp = 10;
 constexpr int kRing = 5;
 constexpr uint32_t kHalfBytes = 128 * 128;  // 64 dims of 128 rows, 128-byte swizzled lines
 constexpr uint32_t kTileBytes = 2 * kHalfBytes;
@@ -68,10 +69,12 @@ constexpr uint32_t kOffRing = 2 * kTileBytes;
 constexpr uint32_t kOffCtl = kOffRing + kRing * kTileBytes;
 struct Ctl {
   unsigned long long full[kRing], empty[kRing];
-  unsigned long long qfull, qempty, sfull[2], pready[2][2], odone[2], ufull[2], uempty[2], both;
+  unsigned long long qfull, qempty, sfull[2], pready[2][2], odone[2], ufull[2], uempty[2], both,
+      tail[4];
   uint32_t tmem;
   int abort, last, pad;
   Unit unit[2];
+  int tail_stage[4], tail_row[4];  // V tiles with rows to clear: ring stage (-1: the end), first row
   uint32_t kmask[8];      // valid 16-token groups of a key tile
   float xm[2][128], xl[2][128], xtrue[128];
 };
@@ -372,6 +375,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(smem_u32(&ctl->uempty[t]), 9);   // eight softmax warps and the issue warp
     }
     mbar_init(smem_u32(&ctl->both), 8);          // the eight softmax warps
+    for (int s = 0; s < 4; ++s) mbar_init(smem_u32(&ctl->tail[s]), 1);
     ctl->abort = 0;
     fence_mbar_init();
   }
@@ -518,6 +522,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int oob = kv.num_phys * kv.Hkv * kv.p;  // first row behind the pools: loads zeros
     const long long x_begin = x;
     uint32_t seq = 0, tiles = 0;  // ring positions and key tiles before this unit
+    uint32_t tails = 0;           // V tiles handed to the tail warp
     int u = 0;
     bool ok = true;
     for (; x < x1 && ok; ++u) {
@@ -583,10 +588,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         return good ? (phys * kv.Hkv + h) * kv.p + piece_token(kk) % kv.p : oob;
       };
-      auto load_tile = [&](uint32_t pos, const CUtensorMap* map, int row) {
+      // Ring position seq + pos.  A V tile with rows to clear (from row `clear` of it) completes on a
+      // tail barrier, and the tail warp fills the stage's own barrier when they are cleared.
+      auto load_tile = [&](uint32_t pos, const CUtensorMap* map, int row, int clear) {
         const uint32_t xx = seq + pos, st = xx % kRing, ph = xx / kRing;
         if (ph > 0 && !warp_wait(smem_u32(&ctl->empty[st]), (ph - 1) & 1, abort, kv.status)) return false;
-        const uint32_t bar = smem_u32(&ctl->full[st]);
+        uint32_t bar = smem_u32(&ctl->full[st]);
+        if (clear >= 0) {
+          bar = smem_u32(&ctl->tail[tails & 3]);
+          if (lane == 0) {
+            ctl->tail_stage[tails & 3] = st;
+            ctl->tail_row[tails & 3] = clear;
+          }
+          ++tails;
+        }
         if (lane == 0) mbar_arrive_expect_tx(bar, kTileBytes);
         __syncwarp();
         if (loads)
@@ -607,16 +622,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       __syncwarp();
       int row = piece_row(0, page0);
-      ok = load_tile(0, &tmK, row);
       for (int kk = 0; kk < nk && ok; ++kk) {
         const int page_after = kk + 2 < nk ? piece_page(kk + 2) : -2;
-        if (kk + 1 < nk) {
-          const int row_next = piece_row(kk + 1, page_next);
-          ok = load_tile(2 * kk + 1, &tmK, row_next) && load_tile(2 * kk + 2, &tmV, row);
-          row = row_next;
-        } else {
-          ok = load_tile(2 * kk + 1, &tmV, row);
-        }
+        // V rows behind the request's last token share its page: whatever they hold must not reach
+        // the product, where it would meet P = 0 (pieces wholly behind it are loaded as zeros)
+        const int left = len - (piece_token(kk) - my_seg * seg);
+        ok = load_tile(2 * kk, &tmK, row, -1) &&
+             load_tile(2 * kk + 1, &tmV, row, left < 128 && left % seg != 0 ? left : -1);
+        if (kk + 1 < nk) row = piece_row(kk + 1, page_next);
         page_next = page_after;
       }
       seq += 2 * nk;
@@ -648,157 +661,146 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) {
           ctl->unit[us].valid = 0;
           mbar_arrive(smem_u32(&ctl->ufull[us]));
+          ctl->tail_stage[tails & 3] = -1;
+          mbar_arrive(smem_u32(&ctl->tail[tails & 3]));
         }
       }
     }
     if (*abort && lane == 0) {
-      // loads that were issued and not consumed land before the CTA leaves (bounded)
-      for (int s = 0; s < kRing; ++s)
-        for (int t = 0; t < 2000 && !mbar_try_wait(smem_u32(&ctl->full[s]), 0) &&
-                        !mbar_try_wait(smem_u32(&ctl->full[s]), 1);
-             ++t) {
-        }
+      // loads in flight land before the CTA leaves
+      for (int t = 0; t < 64; ++t) __nanosleep(1000);
     }
   } else if (warp == kMmaWarp) {
     // ============================================================================== issue warp
-    uint32_t seq = 0, pcnt0 = 0, pcnt1 = 0;
-    bool ok = true;
-    auto uni = [](int v) { return __shfl_sync(0xffffffffu, v, 0); };
-    const uint32_t ut = uni(tmem), ubase = uni(smem_base);
-    for (int u = 0; ok; ++u) {
-      const int us = u & 1;
-      if (!warp_wait(smem_u32(&ctl->ufull[us]), (u >> 1) & 1, abort, kv.status)) break;
-      struct {
-        int kb, ns, w0, len, split, n0;
-      } un;
-      const Unit& in = ctl->unit[us];
-      un.kb = uni(in.kb);
-      un.ns = uni(in.ns);
-      un.w0 = uni(in.w0);
-      un.len = uni(in.len);
-      un.split = uni(in.split);
-      un.n0 = uni(in.n0);
-      const int nk = uni(in.ke) - un.kb, valid = uni(in.valid);
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&ctl->uempty[us]));
-      if (!valid) break;
-      if (!warp_wait(smem_u32(&ctl->qfull), u & 1, abort, kv.status)) break;
-      auto stage = [&](uint32_t pos) { return (seq + pos) % kRing; };
-      auto wait_full = [&](uint32_t pos) {
-        const uint32_t xx = seq + pos;
-        return warp_wait(smem_u32(&ctl->full[xx % kRing]), (xx / kRing) & 1, abort, kv.status);
+    // One thread.  The tensor core takes about four products ahead of the one it works on, 256 cycles,
+    // so what lies between two groups of products has to stay below that: ring places are counted
+    // along instead of divided out, and descriptors are sums with constants.
+    if (elect_one()) {
+      auto wait = [&](const unsigned long long* bar, uint32_t parity) {
+        return mbar_wait(smem_u32(bar), parity, abort, kv.status);
       };
-      auto pos_k = [&](int kk) { return static_cast<uint32_t>(kk == 0 ? 0 : 2 * kk - 1); };
-      auto pos_v = [&](int kk) { return static_cast<uint32_t>(kk + 1 < nk ? 2 * kk + 2 : 2 * kk + 1); };
-      // (elect_one picks the same lane every time, so a commit covers all products issued before it)
-      auto commit = [&](unsigned long long* bar) {
-        if (elect_one()) tc_commit(smem_u32(bar));
-        __syncwarp();
-      };
-      auto qk = [&](int t, int kk) {  // S_t = Q K^T
-        const uint32_t q = ubase + (un.split ? 0 : t) * kTileBytes;
-        const uint32_t kt = ubase + kOffRing + stage(pos_k(kk)) * kTileBytes;
-        const uint64_t dq = smem_desc(q, 16), dk = smem_desc(kt, 16);
-        if (elect_one()) {
-#pragma unroll
-          for (int ks = 0; ks < 8; ++ks) {
-            constexpr uint32_t kHalf16 = kHalfBytes >> 4;
-            const uint32_t off = (ks >> 2) * kHalf16 + (ks & 3) * 2;
-            mma_ss(ut + kS0 + 128 * t, dq + off, dk + off, ks > 0);
+      struct Place {  // of a ring position: stage, phase
+        uint32_t st, ph;
+        DSA_DEV void next2() {
+          st += 2;
+          if (st >= kRing) {
+            st -= kRing;
+            ph ^= 1;
           }
-          tc_commit(smem_u32(&ctl->sfull[t]));
         }
-        __syncwarp();
       };
-      // O_t += P V, in two halves of 64 keys as the softmax delivers them
-      auto pv = [&](int t, int kk, bool first) {
-        const uint32_t vt = ubase + kOffRing + stage(pos_v(kk)) * kTileBytes;
-        const uint64_t dv = smem_desc(vt, kHalfBytes);
-        const uint32_t ph = t ? pcnt1++ : pcnt0++;
+      Place pk = {0, 0}, pv = {1, 0};  // of the next K and V tile (positions alternate: K V K V ...)
+      const uint64_t dq = smem_desc(smem_base, 16), dk0 = smem_desc(smem_base + kOffRing, 16);
+      const uint64_t dv0 = smem_desc(smem_base + kOffRing, kHalfBytes);
+      constexpr uint32_t kTile16 = kTileBytes >> 4, kHalf16 = kHalfBytes >> 4;
+      uint32_t pph[2] = {0, 0};  // phases of P
+      bool ok = true;
+      auto qk = [&](int t, uint32_t st, uint32_t q) {  // S_t = Q K^T
+        const uint64_t da = dq + q * kTile16, db = dk0 + st * kTile16;
+#pragma unroll
+        for (int ks = 0; ks < 8; ++ks) {
+          const uint32_t off = (ks >> 2) * kHalf16 + (ks & 3) * 2;
+          mma_ss(tmem + kS0 + 128 * t, da + off, db + off, ks > 0);
+        }
+        tc_commit(smem_u32(&ctl->sfull[t]));
+      };
+      auto product = [&](int t, uint32_t st, uint32_t acc) {  // O_t += P V, as P's halves arrive
+        const uint64_t db = dv0 + st * kTile16;
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-          if (!warp_wait(smem_u32(&ctl->pready[t][half]), ph & 1, abort, kv.status)) return false;
+          if (!wait(&ctl->pready[t][half], pph[t])) return false;
           tc_fence_after();
-          if (elect_one()) {
 #pragma unroll
-            for (int ks = 4 * half; ks < 4 * half + 4; ++ks)
-              mma_ts(ut + kO0 + 128 * t, ut + kS0 + 128 * t + 8 * ks, dv + ks * (2048 >> 4),
-                     ks > 0 || !first);
-            if (half == 1) tc_commit(smem_u32(&ctl->odone[t]));
-          }
-          __syncwarp();
+          for (int ks = 4 * half; ks < 4 * half + 4; ++ks)
+            mma_ts(tmem + kO0 + 128 * t, tmem + kS0 + 128 * t + 8 * ks, db + ks * (2048 >> 4),
+                   ks > 0 ? 1 : acc);
         }
+        pph[t] ^= 1;
+        tc_commit(smem_u32(&ctl->odone[t]));
         return true;
       };
-      // V rows behind the request's last token share its page: whatever they hold must not reach the
-      // product, where it would meet P = 0
-      auto wait_v = [&](int kk) {
-        if (!wait_full(pos_v(kk))) return false;
-        const int list = un.kb + kk;
-        const int t0 = (list < un.ns ? list : un.w0 + list - un.ns) * 128;
-        const int r0 = un.len - t0;
-        if (r0 < 128 && r0 % seg != 0) {  // (pieces wholly behind it were loaded as zeros)
-          const uint32_t off = kOffRing + stage(pos_v(kk)) * kTileBytes;
-          const int rows = seg - r0 % seg;
-          for (int e = lane; e < rows * 16; e += 32)
-            *reinterpret_cast<uint4*>(smem + off + ((e >> 3) & 1) * kHalfBytes + (r0 + (e >> 4)) * 128 +
-                                      (e & 7) * 16) = make_uint4(0, 0, 0, 0);
-          fence_proxy_async_smem();
-          __syncwarp();
-        }
-        return true;
-      };
-      ok = wait_full(0);
-      if (!ok) break;
-      if (!un.split) {
-        if (un.n0 > 0) qk(0, 0);
-        qk(1, 0);
-        commit(&ctl->empty[stage(0)]);
-        if (nk == 1) commit(&ctl->qempty);
-        for (int kk = 0; kk < nk && ok; ++kk) {
-          ok = wait_v(kk);
-          if (!ok) break;
-          if (kk < un.n0) {
-            if (!(ok = pv(0, kk, kk == 0))) break;
+      for (int u = 0; ok; ++u) {
+        const int us = u & 1;
+        if (!wait(&ctl->ufull[us], (u >> 1) & 1)) break;
+        const Unit& un = ctl->unit[us];
+        const int nk = un.ke - un.kb, n0 = un.n0, split = un.split, valid = un.valid;
+        mbar_arrive(smem_u32(&ctl->uempty[us]));
+        if (!valid) break;
+        if (!wait(&ctl->qfull, u & 1)) break;
+        if (!(ok = wait(&ctl->full[pk.st], pk.ph))) break;
+        if (!split) {
+          if (n0 > 0) qk(0, pk.st, 0);
+          qk(1, pk.st, 1);
+          tc_commit(smem_u32(&ctl->empty[pk.st]));
+          if (nk == 1) tc_commit(smem_u32(&ctl->qempty));
+          pk.next2();
+          for (int kk = 0; kk < nk; ++kk) {
+            const bool more = kk + 1 < nk;
+            if (!(ok = wait(&ctl->full[pv.st], pv.ph))) break;
+            if (kk < n0 && !(ok = product(0, pv.st, kk > 0))) break;
+            if (more) {
+              if (!(ok = wait(&ctl->full[pk.st], pk.ph))) break;
+              if (kk + 1 < n0) qk(0, pk.st, 0);
+            }
+            if (!(ok = product(1, pv.st, kk > 0))) break;
+            tc_commit(smem_u32(&ctl->empty[pv.st]));
+            pv.next2();
+            if (more) {
+              qk(1, pk.st, 1);
+              tc_commit(smem_u32(&ctl->empty[pk.st]));
+              if (kk + 2 == nk) tc_commit(smem_u32(&ctl->qempty));
+              pk.next2();
+            }
           }
-          if (kk + 1 < nk) {
-            if (!(ok = wait_full(pos_k(kk + 1)))) break;
-            if (kk + 1 < un.n0) qk(0, kk + 1);
+        } else {
+          qk(0, pk.st, 0);
+          tc_commit(smem_u32(&ctl->empty[pk.st]));
+          pk.next2();
+          if (nk > 1) {
+            if (!(ok = wait(&ctl->full[pk.st], pk.ph))) break;
+            qk(1, pk.st, 0);
+            tc_commit(smem_u32(&ctl->empty[pk.st]));
+            pk.next2();
           }
-          if (!(ok = pv(1, kk, kk == 0))) break;
-          commit(&ctl->empty[stage(pos_v(kk))]);
-          if (kk + 1 < nk) {
-            qk(1, kk + 1);
-            commit(&ctl->empty[stage(pos_k(kk + 1))]);
-            if (kk + 2 == nk) commit(&ctl->qempty);
-          }
-        }
-      } else {
-        qk(0, 0);
-        commit(&ctl->empty[stage(0)]);
-        if (nk > 1) {
-          if (!(ok = wait_full(pos_k(1)))) break;
-          qk(1, 1);
-          commit(&ctl->empty[stage(pos_k(1))]);
-        }
-        if (nk <= 2) commit(&ctl->qempty);
-        for (int kk = 0; kk < nk && ok; ++kk) {
-          const int t = kk & 1;
-          if (!(ok = wait_v(kk))) break;
-          if (!(ok = pv(t, kk, kk < 2))) break;
-          commit(&ctl->empty[stage(pos_v(kk))]);
-          if (kk + 2 < nk) {
-            if (!(ok = wait_full(pos_k(kk + 2)))) break;
-            qk(t, kk + 2);
-            commit(&ctl->empty[stage(pos_k(kk + 2))]);
-            if (kk + 3 == nk) commit(&ctl->qempty);
+          if (nk <= 2) tc_commit(smem_u32(&ctl->qempty));
+          for (int kk = 0; kk < nk; kk += 2) {
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+              if (kk + t >= nk) break;
+              if (!(ok = wait(&ctl->full[pv.st], pv.ph))) break;
+              if (!(ok = product(t, pv.st, kk > 0))) break;
+              tc_commit(smem_u32(&ctl->empty[pv.st]));
+              pv.next2();
+              if (kk + t + 2 < nk) {
+                if (!(ok = wait(&ctl->full[pk.st], pk.ph))) break;
+                qk(t, pk.st, 0);
+                tc_commit(smem_u32(&ctl->empty[pk.st]));
+                if (kk + t + 3 == nk) tc_commit(smem_u32(&ctl->qempty));
+                pk.next2();
+              }
+            }
+            if (!ok) break;
           }
         }
       }
-      seq += 2 * nk;
+      if (*abort)  // products in flight end before TMEM is freed
+        for (int t = 0; t < 64; ++t) __nanosleep(1000);
     }
-    if (*abort) {  // products in flight end before TMEM is freed
-      for (int t = 0; t < 64; ++t) __nanosleep(1000);
+    __syncwarp();
+  } else if (warp == kTailWarp) {
+    // =============================================================================== tail warp
+    for (uint32_t x = 0;; ++x) {
+      if (!warp_wait(smem_u32(&ctl->tail[x & 3]), (x >> 2) & 1, abort, kv.status)) break;
+      const int st = ctl->tail_stage[x & 3], r0 = ctl->tail_row[x & 3];
+      if (st < 0) break;
+      uint8_t* tile = smem + kOffRing + st * kTileBytes;
+      const int rows = seg - r0 % seg;
+      for (int e = lane; e < rows * 16; e += 32)
+        *reinterpret_cast<uint4*>(tile + ((e >> 3) & 1) * kHalfBytes + (r0 + (e >> 4)) * 128 +
+                                  (e & 7) * 16) = make_uint4(0, 0, 0, 0);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&ctl->full[st]));
     }
   }
   } else {
