@@ -21,9 +21,10 @@
 // No CTA waits for another.
 //
 // Inside a CTA: warps 0-3 and 4-7 are the streams' softmax warpgroups (a thread owns a row: S from
-// TMEM in one load, P back to TMEM over S as bf16), warp 8 loads (TMA: Q tiles, and K and V tiles of
-// 128 tokens assembled from page pieces into a ring of five 32 KB stages, K and V in turn), one thread
-// of warp 9 issues the tcgen05 products (S = Q K^T from shared memory, O += P V with P from TMEM), and
+// TMEM in one load, P back to TMEM over S as bf16), warps 8 and 11 load (TMA: Q and K tiles; V
+// tiles; of 128 tokens, assembled from page pieces, into a ring of five 32 KB stages, K and V in turn:
+// with pages of 16 tokens one warp issues the 32 pieces of a K and a V tile in more time than the
+// products take), one thread of warp 9 issues the tcgen05 products (S = Q K^T from shared memory, O += P V with P from TMEM), and
 // warp 10 clears the rows behind a request's last token in the V tile that holds it.
 #include "common.cuh"
 #include "internal.h"
@@ -34,7 +35,7 @@ namespace dsa {
 namespace {
 
 constexpr int kThreads = 384;
-constexpr int kLoadWarp = 8, kMmaWarp = 9, kTailWarp = 10;
+constexpr int kLoadWarp = 8, kMmaWarp = 9, kTailWarp = 10, kValueWarp = 11;
 constexpr int kRing = 5;
 constexpr uint32_t kHalfBytes = 128 * 128;  // 64 dims of 128 rows, 128-byte swizzled lines
 constexpr uint32_t kTileBytes = 2 * kHalfBytes;
@@ -372,7 +373,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(smem_u32(&ctl->pready[t][1]), 4);
       mbar_init(smem_u32(&ctl->odone[t]), 1);
       mbar_init(smem_u32(&ctl->ufull[t]), 1);
-      mbar_init(smem_u32(&ctl->uempty[t]), 9);   // eight softmax warps and the issue warp
+      mbar_init(smem_u32(&ctl->uempty[t]), 10);  // eight softmax warps, issue warp, value warp
     }
     mbar_init(smem_u32(&ctl->both), 8);          // the eight softmax warps
     for (int s = 0; s < 4; ++s) mbar_init(smem_u32(&ctl->tail[s]), 1);
@@ -461,6 +462,45 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp >= 8) {
   regs_dec<kOtherRegs>();
+  const int lseg = 31 - __clz(seg), nseg = 128 >> lseg, my_seg = lane & (nseg - 1), my_half = lane / nseg;
+  const bool loads = my_half < 2;  // a lane loads one half (of the dims) of one piece of a tile
+  const uint32_t per_page = kv.p >> lseg, magic = 0xffffffffu / per_page + 1;  // pieces of a page
+  const int oob = kv.num_phys * kv.Hkv * kv.p;  // first row behind the pools: loads zeros
+  // first token of a lane's piece of list entry `list`
+  auto piece_token = [&](int list, int ns, int w0) {
+    return (list < ns ? list : w0 + list - ns) * 128 + (my_seg << lseg);
+  };
+  // its page-table entry (-2: behind the request's tokens)
+  auto piece_page = [&](int s, int b, int len) {
+    if (!loads || s >= len) return -2;
+    const uint32_t x = s >> lseg;  // below 2^27, so the product below is the exact quotient
+    const uint32_t j = per_page == 1 ? x : __umulhi(x, magic);
+    return max(kv.page_table[static_cast<size_t>(b) * kv.max_pages + j], -1);
+  };
+  // the pool row it gives (oob where there is nothing to load)
+  auto piece_row = [&](int s, int phys, int h) {
+    if (phys < 0 || phys >= kv.num_phys) return oob;
+    const uint32_t x = s >> lseg;
+    const uint32_t in_page = per_page == 1 ? 0 : x - __umulhi(x, magic) * per_page;
+    return (phys * kv.Hkv + h) * kv.p + static_cast<int>(in_page << lseg);
+  };
+  struct Place {  // of a ring position: stage, phase; K and V positions alternate
+    uint32_t st, ph;
+    DSA_DEV void next2() {
+      st += 2;
+      if (st >= kRing) {
+        st -= kRing;
+        ph ^= 1;
+      }
+    }
+  };
+  auto load_pieces = [&](uint32_t st, const CUtensorMap* map, int row, uint32_t bar) {
+    if (lane == 0) mbar_arrive_expect_tx(bar, kTileBytes);
+    __syncwarp();
+    if (loads)
+      tma_load_kv(smem_base + kOffRing + st * kTileBytes + my_half * kHalfBytes + ((my_seg * 128) << lseg),
+                  map, row, my_half, bar);
+  };
   if (warp == kLoadWarp) {
     // =============================================================================== load warp
 
@@ -517,12 +557,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
     fence_proxy_async_smem();  // the prefix sums are read; the ring takes their place
 
-    const int nseg = 128 / seg, my_seg = lane % nseg, my_half = lane / nseg;
-    const bool loads = my_half < 2;
-    const int oob = kv.num_phys * kv.Hkv * kv.p;  // first row behind the pools: loads zeros
     const long long x_begin = x;
-    uint32_t seq = 0, tiles = 0;  // ring positions and key tiles before this unit
-    uint32_t tails = 0;           // V tiles handed to the tail warp
+    uint32_t tiles = 0;      // key tiles before this unit
+    Place pk = {0, 1};       // of the next K tile (a fresh barrier passes a wait for phase 1)
     int u = 0;
     bool ok = true;
     for (; x < x1 && ok; ++u) {
@@ -560,57 +597,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       __syncwarp();
 
-      // This lane's piece of a key tile: its page-table entry (-2: behind the request's tokens), read
-      // two tiles ahead of its use, and the pool row that it gives.
-      auto piece_token = [&](int kk) {
-        const int list = un.kb + kk;
-        return (list < un.ns ? list : un.w0 + list - un.ns) * 128 + my_seg * seg;
-      };
-      auto piece_page = [&](int kk) {
-        const int s = piece_token(kk);
-        if (!loads || s >= len) return -2;
-        return max(kv.page_table[static_cast<size_t>(b) * kv.max_pages + s / kv.p], -1);
-      };
-      // the row (oob where there is nothing to load), and the tile's valid 16-token groups for the
-      // softmax
-      auto piece_row = [&](int kk, int phys) {
-        const bool good = phys >= 0 && phys < kv.num_phys;
-        const uint32_t bad =
-            __ballot_sync(0xffffffffu, phys != -2 && !good) & ((1u << nseg) - 1u);
-        if (lane == 0) {
-          uint32_t m = 0xffu;
-          if (bad) {
-            for (int s = 0; s < nseg; ++s)
-              if (bad >> s & 1) m &= ~(((1u << (seg / 16)) - 1u) << (s * (seg / 16)));
-            raise_status(kv.status, DSA_STATUS_BAD_PAGE);
-          }
-          ctl->kmask[(tiles + kk) & 7] = m;
-        }
-        return good ? (phys * kv.Hkv + h) * kv.p + piece_token(kk) % kv.p : oob;
-      };
-      // Ring position seq + pos.  A V tile with rows to clear (from row `clear` of it) completes on a
-      // tail barrier, and the tail warp fills the stage's own barrier when they are cleared.
-      auto load_tile = [&](uint32_t pos, const CUtensorMap* map, int row, int clear) {
-        const uint32_t xx = seq + pos, st = xx % kRing, ph = xx / kRing;
-        if (ph > 0 && !warp_wait(smem_u32(&ctl->empty[st]), (ph - 1) & 1, abort, kv.status)) return false;
-        uint32_t bar = smem_u32(&ctl->full[st]);
-        if (clear >= 0) {
-          bar = smem_u32(&ctl->tail[tails & 3]);
-          if (lane == 0) {
-            ctl->tail_stage[tails & 3] = st;
-            ctl->tail_row[tails & 3] = clear;
-          }
-          ++tails;
-        }
-        if (lane == 0) mbar_arrive_expect_tx(bar, kTileBytes);
-        __syncwarp();
-        if (loads)
-          tma_load_kv(smem_base + kOffRing + st * kTileBytes + my_half * kHalfBytes + my_seg * seg * 128,
-                      map, row, my_half, bar);
-        return true;
-      };
-      const int page0 = piece_page(0);
-      int page_next = nk > 1 ? piece_page(1) : -2;
+      int page = piece_page(piece_token(un.kb, un.ns, un.w0), b, len);
+      int page_next = nk > 1 ? piece_page(piece_token(un.kb + 1, un.ns, un.w0), b, len) : -2;
       if (u > 0 && !warp_wait(smem_u32(&ctl->qempty), (u - 1) & 1, abort, kv.status)) break;
       if (lane == 0) {
         const uint32_t bar = smem_u32(&ctl->qfull), bytes = static_cast<uint32_t>(G * TQ) * 128;
@@ -621,18 +609,26 @@ __global__ void __launch_bounds__(kThreads, 1)
                        bar);
       }
       __syncwarp();
-      int row = piece_row(0, page0);
-      for (int kk = 0; kk < nk && ok; ++kk) {
-        const int page_after = kk + 2 < nk ? piece_page(kk + 2) : -2;
-        // V rows behind the request's last token share its page: whatever they hold must not reach
-        // the product, where it would meet P = 0 (pieces wholly behind it are loaded as zeros)
-        const int left = len - (piece_token(kk) - my_seg * seg);
-        ok = load_tile(2 * kk, &tmK, row, -1) &&
-             load_tile(2 * kk + 1, &tmV, row, left < 128 && left % seg != 0 ? left : -1);
-        if (kk + 1 < nk) row = piece_row(kk + 1, page_next);
+      for (int kk = 0; kk < nk; ++kk) {
+        // page ids are read two tiles ahead of their use
+        const int page_after =
+            kk + 2 < nk ? piece_page(piece_token(un.kb + kk + 2, un.ns, un.w0), b, len) : -2;
+        const int row = piece_row(piece_token(un.kb + kk, un.ns, un.w0), page, h);
+        // the tile's valid 16-token groups, for the softmax
+        uint32_t good = 0xffu;
+        const uint32_t bad = __ballot_sync(0xffffffffu, page != -2 && row == oob) & ((1u << nseg) - 1u);
+        if (bad) {
+          for (int x = 0; x < nseg; ++x)
+            if (bad >> x & 1) good &= ~(((1u << (seg / 16)) - 1u) << (x * (seg / 16)));
+          if (lane == 0) raise_status(kv.status, DSA_STATUS_BAD_PAGE);
+        }
+        if (lane == 0) ctl->kmask[(tiles + kk) & 7] = good;
+        if (!(ok = warp_wait(smem_u32(&ctl->empty[pk.st]), pk.ph, abort, kv.status))) break;
+        load_pieces(pk.st, &tmK, row, smem_u32(&ctl->full[pk.st]));
+        pk.next2();
+        page = page_next;
         page_next = page_after;
       }
-      seq += 2 * nk;
       tiles += nk;
       // the next unit starts at the next item
       x += nk;
@@ -661,13 +657,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) {
           ctl->unit[us].valid = 0;
           mbar_arrive(smem_u32(&ctl->ufull[us]));
-          ctl->tail_stage[tails & 3] = -1;
-          mbar_arrive(smem_u32(&ctl->tail[tails & 3]));
         }
       }
     }
-    if (*abort && lane == 0) {
-      // loads in flight land before the CTA leaves
+    if (*abort) {  // loads in flight land before the CTA leaves
       for (int t = 0; t < 64; ++t) __nanosleep(1000);
     }
   } else if (warp == kMmaWarp) {
@@ -678,16 +671,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (elect_one()) {
       auto wait = [&](const unsigned long long* bar, uint32_t parity) {
         return mbar_wait(smem_u32(bar), parity, abort, kv.status);
-      };
-      struct Place {  // of a ring position: stage, phase
-        uint32_t st, ph;
-        DSA_DEV void next2() {
-          st += 2;
-          if (st >= kRing) {
-            st -= kRing;
-            ph ^= 1;
-          }
-        }
       };
       Place pk = {0, 0}, pv = {1, 0};  // of the next K and V tile (positions alternate: K V K V ...)
       const uint64_t dq = smem_desc(smem_base, 16), dk0 = smem_desc(smem_base + kOffRing, 16);
@@ -787,6 +770,54 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int t = 0; t < 64; ++t) __nanosleep(1000);
     }
     __syncwarp();
+  } else if (warp == kValueWarp) {
+    // ============================================================================== value warp
+    Place pv = {1, 1};
+    uint32_t tails = 0;  // tiles handed to the tail warp
+    bool ok = true;
+    for (int u = 0; ok; ++u) {
+      const int us = u & 1;
+      if (!warp_wait(smem_u32(&ctl->ufull[us]), (u >> 1) & 1, abort, kv.status)) break;
+      const Unit& in = ctl->unit[us];
+      const int valid = in.valid, b = in.b, h = in.h, len = in.len, kb = in.kb, ke = in.ke, ns = in.ns,
+                w0 = in.w0;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&ctl->uempty[us]));
+      if (!valid) {
+        if (lane == 0) {
+          ctl->tail_stage[tails & 3] = -1;
+          mbar_arrive(smem_u32(&ctl->tail[tails & 3]));
+        }
+        break;
+      }
+      int page = piece_page(piece_token(kb, ns, w0), b, len);
+      int page_next = kb + 1 < ke ? piece_page(piece_token(kb + 1, ns, w0), b, len) : -2;
+      for (int k = kb; k < ke; ++k) {
+        const int page_after = k + 2 < ke ? piece_page(piece_token(k + 2, ns, w0), b, len) : -2;
+        const int s = piece_token(k, ns, w0), row = piece_row(s, page, h);
+        if (!(ok = warp_wait(smem_u32(&ctl->empty[pv.st]), pv.ph, abort, kv.status))) break;
+        // Rows behind the request's last token share its page: whatever they hold must not reach the
+        // product, where it would meet P = 0 (pieces wholly behind it are loaded as zeros).  Such a
+        // tile completes on a tail barrier, and the tail warp fills the stage's own barrier when
+        // they are cleared.
+        const int left = len - (s - (my_seg << lseg));
+        uint32_t bar = smem_u32(&ctl->full[pv.st]);
+        if (left < 128 && (left & (seg - 1)) != 0) {
+          bar = smem_u32(&ctl->tail[tails & 3]);
+          if (lane == 0) {
+            ctl->tail_stage[tails & 3] = pv.st;
+            ctl->tail_row[tails & 3] = left;
+          }
+          ++tails;
+        }
+        load_pieces(pv.st, &tmV, row, bar);
+        pv.next2();
+        page = page_next;
+        page_next = page_after;
+      }
+    }
+    if (*abort)  // loads in flight land before the CTA leaves
+      for (int t = 0; t < 64; ++t) __nanosleep(1000);
   } else if (warp == kTailWarp) {
     // =============================================================================== tail warp
     for (uint32_t x = 0;; ++x) {
