@@ -223,6 +223,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_chunk_kernel(const PlanArgs
 // query heads.  The sines of a token are worked out once per CTA and shared by its heads.
 constexpr int kAppThreads = 256;
 constexpr int kAppTokens = 16;
+constexpr int kAppBatch = 4;
+constexpr int kAppCtas = 4 * 152;  // CTAs wanted before heads are shared
 
 // ---- cosine and sine of a fraction of a turn (64-bit fixed point), to the last bit of fp32 but for
 // about one value in 10^5: keys that lie next to a rounding border of bf16 then fall on the same side
@@ -297,7 +299,7 @@ DSA_DEV void rotate8(const uint4& xa, const uint4& xb, const float2* cs, uint4& 
   uint32_t* ob = reinterpret_cast<uint32_t*>(&yb);
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
-    const float2 c0 = cs[2 * e], c1 = cs[2 * e + 1];
+    const float2 c0 = cs[8 * (2 * e)], c1 = cs[8 * (2 * e + 1)];
     const float a0 = __bfloat162float(a[2 * e]), a1 = __bfloat162float(a[2 * e + 1]);
     const float b0 = __bfloat162float(b[2 * e]), b1 = __bfloat162float(b[2 * e + 1]);
     oa[e] = pack_bf16(turn_x(a0, b0, c0), turn_x(a1, b1, c1));
@@ -305,7 +307,7 @@ DSA_DEV void rotate8(const uint4& xa, const uint4& xb, const float2* cs, uint4& 
   }
 }
 
-// 8 dims as four neighbouring pairs.
+// 8 dims as four neighbouring pairs (their sines 8 words apart).
 DSA_DEV uint4 rotate_pairs(const uint4& x, const float2* cs) {
   const __nv_bfloat16* v = reinterpret_cast<const __nv_bfloat16*>(&x);
   uint4 y;
@@ -313,7 +315,7 @@ DSA_DEV uint4 rotate_pairs(const uint4& x, const float2* cs) {
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
     const float a = __bfloat162float(v[2 * e]), b = __bfloat162float(v[2 * e + 1]);
-    o[e] = pack_bf16(turn_x(a, b, cs[e]), turn_y(a, b, cs[e]));
+    o[e] = pack_bf16(turn_x(a, b, cs[8 * e]), turn_y(a, b, cs[8 * e]));
   }
   return y;
 }
@@ -321,7 +323,8 @@ DSA_DEV uint4 rotate_pairs(const uint4& x, const float2* cs) {
 template <int KIND>
 __global__ void __launch_bounds__(kAppThreads) append_chunk_kernel(const AppendArgs a) {
   launch_dependents();
-  __shared__ float2 s_cs[kAppTokens][kHeadDim / 2];
+  // sines of pair 8 e + k at [k][e]: the 8 threads of a row read neighbouring words
+  __shared__ float2 s_cs[kAppTokens][8][8];
   grid_dependency_wait();
   const KvView& kv = a.kv;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -329,23 +332,55 @@ __global__ void __launch_bounds__(kAppThreads) append_chunk_kernel(const AppendA
   const int nh = min(a.heads_per_cta, kv.Hkv - h0);
   const int G = kv.G, half = a.rot_dim / 2;
   const int t0 = blockIdx.x * kAppTokens, t1 = min(t0 + kAppTokens, a.tokens);
+  // this thread's two pieces of a turned row: the same dims of both halves, neighbours where pairs are
+  // neighbours, and behind the turned dims (piece 2 hp + 2 (e - hp) = 2 e)
+  const int e = tid & 7, hp = half / 8;
+  const int turn_a = !a.interleaved && e < hp ? e : 2 * e;
+  const int turn_b = !a.interleaved && e < hp ? e + hp : 2 * e + 1;
 
-  for (int lead = t0; lead < t1; ++lead) {
-    // (uniform over the CTA: every thread reads the same words)
-    const int b = a.row[lead];
-    if (b < 0 || b >= kv.B) continue;
-    const int first = a.start[b], n_new = a.count[b];
-    const int pos = a.pos[lead];
-    const bool head_run = lead == first;
-    if (lead < first || lead - first >= n_new || (!head_run && pos % a.unit != 0)) continue;
-    const int n = min(min(a.unit - pos % a.unit, first + n_new - lead), a.tokens - lead);
-    const int L = request_len(kv, b);
-    const int j = pos / kv.p;
-    int phys = -1;
-    if (pos >= 0 && j < kv.max_pages)
-      phys = kv.page_table[static_cast<size_t>(b) * kv.max_pages + j];
-    const bool ok = phys >= 0 && phys < kv.num_phys;
-    if (!ok && tid == 0) raise_status(kv.status, DSA_STATUS_BAD_PAGE);
+  // The runs that begin here, found by one warp: a token each, their dependent reads side by side.
+  struct Run {
+    int n, pos, len, phys, first_run, last_run;
+  };
+  __shared__ Run s_run[kAppTokens];
+  __shared__ uint32_t s_leads;
+  if (warp == 0) {
+    const int t = t0 + lane;
+    bool leads = false;
+    if (lane < kAppTokens && t < t1) {
+      const int b = a.row[t], pos = a.pos[t];
+      if (b >= 0 && b < kv.B && pos >= 0) {
+        const int first = a.start[b], n_new = a.count[b];
+        leads = t >= first && t - first < n_new && (t == first || pos % a.unit == 0);
+        if (leads) {
+          Run r;
+          r.n = min(min(a.unit - pos % a.unit, first + n_new - t), a.tokens - t);
+          r.pos = pos;
+          r.len = request_len(kv, b);
+          const int j = pos / kv.p;
+          r.phys = -1;
+          if (j < kv.max_pages) r.phys = kv.page_table[static_cast<size_t>(b) * kv.max_pages + j];
+          if (r.phys < 0 || r.phys >= kv.num_phys) {
+            r.phys = -1;
+            raise_status(kv.status, DSA_STATUS_BAD_PAGE);
+          }
+          r.first_run = t == first;
+          r.last_run = t + r.n == first + n_new || j != (pos + r.n) / kv.p;
+          s_run[lane] = r;
+        }
+      }
+    }
+    const uint32_t m = __ballot_sync(0xffffffffu, leads);
+    if (lane == 0) s_leads = m;
+  }
+  __syncthreads();
+
+  for (uint32_t todo = s_leads; todo != 0; todo &= todo - 1) {
+    const int at = __ffs(todo) - 1, lead = t0 + at;
+    const Run run = s_run[at];
+    const int n = run.n, pos = run.pos, phys = run.phys, j = pos / kv.p;
+    const bool ok = phys >= 0;
+    const int slot0 = pos - j * kv.p;
 
     for (int c0 = 0; c0 < n; c0 += kAppTokens) {
       const int nt = min(kAppTokens, n - c0);
@@ -358,62 +393,82 @@ __global__ void __launch_bounds__(kAppThreads) append_chunk_kernel(const AppendA
           const long long where =
               a.positions ? a.positions[static_cast<size_t>(ax) * a.tokens + t] : pos + c0 + tt;
           // position x phase modulo one turn, exact in 64-bit integers whatever the position
-          s_cs[tt][pr] = cos_sin_turn(static_cast<unsigned long long>(where) * a.phase[pr]);
+          s_cs[tt][pr & 7][pr >> 3] = cos_sin_turn(static_cast<unsigned long long>(where) * a.phase[pr]);
         }
         __syncthreads();
       }
-      // rows of a token: its query heads (with rotation), its keys, its values; 8 threads a row,
-      // two 16-byte pieces each
+      // Rows of a token: its query heads, its keys, its values; 8 threads a row, two 16-byte pieces
+      // each.  A thread walks the (token, row) pairs 32 apart, kAppBatch of them at a time with all
+      // their loads in flight.
       const int nq = a.q ? nh * G : 0;
       const int rows = nq + 2 * nh;
-      for (int i = tid; i < nt * rows * 8; i += kAppThreads) {
-        const int e = i & 7, rr = (i >> 3) % rows, tt = (i >> 3) / rows;
-        const int t = lead + c0 + tt;
-        const __nv_bfloat16* src;
-        __nv_bfloat16* dst;
-        bool turn = a.phase != nullptr;
-        if (rr < nq) {
-          const int hq = h0 * G + rr;
-          src = a.q + static_cast<size_t>(t) * a.q_stride + hq * kHeadDim;
-          dst = a.q_out + (static_cast<size_t>(t) * kv.Hq + hq) * kHeadDim;
-        } else {
-          const bool is_v = rr - nq >= nh;
-          const int h = h0 + (is_v ? rr - nq - nh : rr - nq);
-          if (!ok) continue;
-          const size_t at = ((static_cast<size_t>(phys) * kv.Hkv + h) * kv.p + (pos + c0 + tt) % kv.p) *
-                            kHeadDim;
-          src = is_v ? a.v + static_cast<size_t>(t) * a.v_stride + h * kHeadDim
-                     : a.k + static_cast<size_t>(t) * a.k_stride + h * kHeadDim;
-          dst = (is_v ? a.v_pages : a.k_pages) + at;
-          if (is_v) turn = false;
-        }
-        const int hp = half / 8;  // 16-byte pieces of half a rotated row
-        int ca, cb;               // this thread's two pieces
-        if (!turn || a.interleaved) {
-          ca = 2 * e;
-          cb = 2 * e + 1;
-        } else if (e < hp) {
-          ca = e;
-          cb = e + hp;
-        } else {
-          ca = 2 * e;  // 2 hp + 2 (e - hp): the pieces behind the rotated ones
-          cb = 2 * e + 1;
-        }
-        uint4 xa = *reinterpret_cast<const uint4*>(src + ca * 8);
-        uint4 xb = *reinterpret_cast<const uint4*>(src + cb * 8);
-        if (turn) {
-          if (a.interleaved) {
-            if (ca < 2 * hp) xa = rotate_pairs(xa, &s_cs[tt][ca * 4]);
-            if (cb < 2 * hp) xb = rotate_pairs(xb, &s_cs[tt][cb * 4]);
-          } else if (e < hp) {
-            uint4 ya, yb;
-            rotate8(xa, xb, &s_cs[tt][ca * 8], ya, yb);
-            xa = ya;
-            xb = yb;
+      int tt = 0, rr = tid >> 3;
+      const int step_t = 32 / rows, step_r = 32 - step_t * rows;
+      while (rr >= rows) {
+        rr -= rows;
+        ++tt;
+      }
+      while (tt < nt) {
+        uint4 xa[kAppBatch], xb[kAppBatch];
+        __nv_bfloat16* dst[kAppBatch];
+        int cs_of[kAppBatch];  // token whose sines turn the row, -1: none
+#pragma unroll
+        for (int u = 0; u < kAppBatch; ++u) {
+          dst[u] = nullptr;
+          cs_of[u] = -1;
+          if (tt < nt) {
+            const int t = lead + c0 + tt;
+            const __nv_bfloat16* src;
+            if (rr < nq) {
+              const int hq = h0 * G + rr;
+              src = a.q + static_cast<size_t>(t) * a.q_stride + hq * kHeadDim;
+              dst[u] = a.q_out + (static_cast<size_t>(t) * kv.Hq + hq) * kHeadDim;
+              if (a.phase) cs_of[u] = tt;
+            } else {
+              const bool is_v = rr - nq >= nh;
+              const int h = h0 + rr - nq - (is_v ? nh : 0);
+              src = is_v ? a.v + static_cast<size_t>(t) * a.v_stride + h * kHeadDim
+                         : a.k + static_cast<size_t>(t) * a.k_stride + h * kHeadDim;
+              if (ok)
+                dst[u] = (is_v ? a.v_pages : a.k_pages) +
+                         ((static_cast<size_t>(phys) * kv.Hkv + h) * kv.p + slot0 + c0 + tt) * kHeadDim;
+              if (a.phase && !is_v) cs_of[u] = tt;
+            }
+            if (dst[u] != nullptr) {
+              const int ca = cs_of[u] >= 0 ? turn_a : 2 * e, cb = cs_of[u] >= 0 ? turn_b : 2 * e + 1;
+              xa[u] = *reinterpret_cast<const uint4*>(src + ca * 8);
+              xb[u] = *reinterpret_cast<const uint4*>(src + cb * 8);
+            }
+          }
+          tt += step_t;
+          rr += step_r;
+          if (rr >= rows) {
+            rr -= rows;
+            ++tt;
           }
         }
-        *reinterpret_cast<uint4*>(dst + ca * 8) = xa;
-        *reinterpret_cast<uint4*>(dst + cb * 8) = xb;
+#pragma unroll
+        for (int u = 0; u < kAppBatch; ++u) {
+          if (dst[u] == nullptr) continue;
+          const bool turn = cs_of[u] >= 0;
+          const int ca = turn ? turn_a : 2 * e, cb = turn ? turn_b : 2 * e + 1;
+          if (turn) {
+            const float2* cs = &s_cs[cs_of[u]][0][e];
+            if (e < hp) {
+              if (a.interleaved) {
+                xa[u] = rotate_pairs(xa[u], cs);
+                xb[u] = rotate_pairs(xb[u], cs + 4 * 8);
+              } else {
+                uint4 ya, yb;
+                rotate8(xa[u], xb[u], cs, ya, yb);
+                xa[u] = ya;
+                xb[u] = yb;
+              }
+            }
+          }
+          *reinterpret_cast<uint4*>(dst[u] + ca * 8) = xa[u];
+          *reinterpret_cast<uint4*>(dst[u] + cb * 8) = xb[u];
+        }
       }
     }
     if (a.meta != nullptr && ok) {
@@ -421,14 +476,13 @@ __global__ void __launch_bounds__(kAppThreads) append_chunk_kernel(const AppendA
       // its last run writes those behind it (no valid token: zeros), as the build does
       const int g = kv.p / a.lp;
       const int u0 = (pos % kv.p) / a.unit * a.unit;
-      const int sub0 = head_run ? 0 : u0 / a.lp;
-      const bool last_run = lead + n == first + n_new || pos / kv.p != (pos + n) / kv.p;
-      const int sub1 = last_run ? g : (u0 + a.unit) / a.lp;
+      const int sub0 = run.first_run ? 0 : u0 / a.lp;
+      const int sub1 = run.last_run ? g : (u0 + a.unit) / a.lp;
       __threadfence_block();
       __syncthreads();
       for (int i = warp; i < nh * (sub1 - sub0); i += kAppThreads / 32) {
         const int h = h0 + i / (sub1 - sub0), sub = sub0 + i % (sub1 - sub0);
-        page_meta<KIND, true>(kv, a.k_pages, a.lp, a.meta, j, h, phys, L, lane, sub, sub + 1);
+        page_meta<KIND, true>(kv, a.k_pages, a.lp, a.meta, j, h, phys, run.len, lane, sub, sub + 1);
       }
     }
   }
@@ -460,7 +514,7 @@ cudaError_t launch_append_chunk(const AppendArgs& in, int kind, cudaStream_t s) 
   const int gx = (a.tokens + kAppTokens - 1) / kAppTokens;
   // KV heads of one CTA: all of them share the CTA's sines, but a short chunk needs the CTAs
   int hpc = a.kv.Hkv;
-  while (hpc > 1 && static_cast<long long>(gx) * ((a.kv.Hkv + hpc - 1) / hpc) < 8 * 152)
+  while (hpc > 1 && static_cast<long long>(gx) * ((a.kv.Hkv + hpc - 1) / hpc) < kAppCtas)
     hpc = (hpc + 1) / 2;
   a.heads_per_cta = hpc;
   dim3 grid(gx, (a.kv.Hkv + hpc - 1) / hpc);
