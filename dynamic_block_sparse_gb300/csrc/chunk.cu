@@ -220,10 +220,12 @@ __global__ void __launch_bounds__(kPlanThreads) plan_chunk_kernel(const PlanArgs
 // records it makes: a "run" is the new tokens of one request inside one unit of `unit` positions (a
 // multiple of the logical page, at least 16 tokens where the page allows it).  CTA (x, y) takes the
 // runs whose first token lies in [16 x, 16 x + 16) of the chunk, for its group of KV heads and their
-// query heads.  The sines of a token are worked out once per CTA and shared by its heads.
+// query heads.  A warp takes a token: its 32 lanes hold 4 of the 128 dims each, with their cosines and
+// sines in registers for all heads of the group, and the rows of 256 bytes stream through kAppRows at
+// a time.
 constexpr int kAppThreads = 256;
 constexpr int kAppTokens = 16;
-constexpr int kAppBatch = 4;
+constexpr int kAppRows = 8;
 constexpr int kAppCtas = 4 * 152;  // CTAs wanted before heads are shared
 
 // ---- cosine and sine of a fraction of a turn (64-bit fixed point), to the last bit of fp32 but for
@@ -284,207 +286,197 @@ DSA_DEV float2 cos_sin_turn(unsigned long long turn) {
   return make_float2(q == 1 || q == 2 ? -x : x, q & 2 ? -y : y);
 }
 
-// (a cos - b sin, b cos + a sin) with every product rounded once, as the formula is written.
-DSA_DEV float turn_x(float a, float b, float2 cs) {
-  return __fsub_rn(__fmul_rn(a, cs.x), __fmul_rn(b, cs.y));
-}
-DSA_DEV float turn_y(float a, float b, float2 cs) {
-  return __fadd_rn(__fmul_rn(b, cs.x), __fmul_rn(a, cs.y));
+// What a lane multiplies its four dims with: out = own * c + partner * s, each product rounded once, as
+// the formulas x cos - y sin and y cos + x sin are written.
+struct Turn {
+  float c[4], s[4];
+  int from;     // lane that holds the partner dims (half-split pairs)
+  bool on;      // this lane's dims are turned
+  bool inside;  // neighbouring pairs: the partner is the lane's own neighbour dim
+};
+
+DSA_DEV uint2 turn_row(const uint2& x, const Turn& r) {
+  float own[4], other[4];
+  own[0] = __uint_as_float(x.x << 16);
+  own[1] = __uint_as_float(x.x & 0xffff0000u);
+  own[2] = __uint_as_float(x.y << 16);
+  own[3] = __uint_as_float(x.y & 0xffff0000u);
+  if (r.inside) {
+    other[0] = own[1];
+    other[1] = own[0];
+    other[2] = own[3];
+    other[3] = own[2];
+  } else {
+    const uint32_t a = __shfl_sync(0xffffffffu, x.x, r.from), b = __shfl_sync(0xffffffffu, x.y, r.from);
+    other[0] = __uint_as_float(a << 16);
+    other[1] = __uint_as_float(a & 0xffff0000u);
+    other[2] = __uint_as_float(b << 16);
+    other[3] = __uint_as_float(b & 0xffff0000u);
+  }
+  float o[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    o[i] = __fadd_rn(__fmul_rn(own[i], r.c[i]), __fmul_rn(other[i], r.s[i]));
+  uint2 y;
+  y.x = pack_bf16(o[0], o[1]);
+  y.y = pack_bf16(o[2], o[3]);
+  return r.on ? y : x;
 }
 
-DSA_DEV void rotate8(const uint4& xa, const uint4& xb, const float2* cs, uint4& ya, uint4& yb) {
-  const __nv_bfloat16* a = reinterpret_cast<const __nv_bfloat16*>(&xa);
-  const __nv_bfloat16* b = reinterpret_cast<const __nv_bfloat16*>(&xb);
-  uint32_t* oa = reinterpret_cast<uint32_t*>(&ya);
-  uint32_t* ob = reinterpret_cast<uint32_t*>(&yb);
+// The lane's Turn for token t at chunk position pos: lane l works out pairs l and l + 32 and the warp
+// shares them.
+DSA_DEV Turn make_turn(const AppendArgs& a, int t, int pos, int lane) {
+  const int half = a.rot_dim / 2;
+  float2 v[2];
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const float2 c0 = cs[8 * (2 * e)], c1 = cs[8 * (2 * e + 1)];
-    const float a0 = __bfloat162float(a[2 * e]), a1 = __bfloat162float(a[2 * e + 1]);
-    const float b0 = __bfloat162float(b[2 * e]), b1 = __bfloat162float(b[2 * e + 1]);
-    oa[e] = pack_bf16(turn_x(a0, b0, c0), turn_x(a1, b1, c1));
-    ob[e] = pack_bf16(turn_y(a0, b0, c0), turn_y(a1, b1, c1));
+  for (int w = 0; w < 2; ++w) {
+    const int pr = lane + 32 * w;
+    v[w] = make_float2(1.f, 0.f);
+    if (pr < half) {
+      const int ax = a.axis ? min(static_cast<int>(a.axis[pr]), a.num_axes - 1) : 0;
+      const long long where =
+          a.positions ? a.positions[static_cast<size_t>(ax) * a.tokens + t] : pos;
+      // position x phase modulo one turn, exact in 64-bit integers whatever the position
+      v[w] = cos_sin_turn(static_cast<unsigned long long>(where) * a.phase[pr]);
+    }
   }
+  Turn r;
+  r.on = 4 * lane < a.rot_dim;
+  r.inside = a.interleaved;
+  const bool low = 4 * lane < half;
+  r.from = !r.on ? lane : low ? lane + half / 4 : lane - half / 4;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int pr = !r.on ? 0 : r.inside ? 2 * lane + i / 2 : low ? 4 * lane + i : 4 * lane - half + i;
+    const float c0 = __shfl_sync(0xffffffffu, v[0].x, pr & 31), c1 = __shfl_sync(0xffffffffu, v[1].x, pr & 31);
+    const float s0 = __shfl_sync(0xffffffffu, v[0].y, pr & 31), s1 = __shfl_sync(0xffffffffu, v[1].y, pr & 31);
+    const bool minus = r.inside ? i % 2 == 0 : low;
+    r.c[i] = pr < 32 ? c0 : c1;
+    r.s[i] = pr < 32 ? s0 : s1;
+    if (minus) r.s[i] = -r.s[i];
+  }
+  return r;
 }
 
-// 8 dims as four neighbouring pairs (their sines 8 words apart).
-DSA_DEV uint4 rotate_pairs(const uint4& x, const float2* cs) {
-  const __nv_bfloat16* v = reinterpret_cast<const __nv_bfloat16*>(&x);
-  uint4 y;
-  uint32_t* o = reinterpret_cast<uint32_t*>(&y);
+// `rows` rows of 256 bytes from src to dst, turned or as they are (strides in elements).
+template <bool TURN>
+DSA_DEV void move_rows(const __nv_bfloat16* src, long long src_step, __nv_bfloat16* dst,
+                       long long dst_step, int rows, const Turn& r) {
+  for (int r0 = 0; r0 < rows; r0 += kAppRows) {
+    uint2 x[kAppRows];
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const float a = __bfloat162float(v[2 * e]), b = __bfloat162float(v[2 * e + 1]);
-    o[e] = pack_bf16(turn_x(a, b, cs[8 * e]), turn_y(a, b, cs[8 * e]));
+    for (int i = 0; i < kAppRows; ++i)
+      if (r0 + i < rows) x[i] = *reinterpret_cast<const uint2*>(src + i * src_step);
+#pragma unroll
+    for (int i = 0; i < kAppRows; ++i)
+      if (r0 + i < rows)
+        *reinterpret_cast<uint2*>(dst + i * dst_step) = TURN ? turn_row(x[i], r) : x[i];
+    src += kAppRows * src_step;
+    dst += kAppRows * dst_step;
   }
-  return y;
 }
 
 template <int KIND>
-__global__ void __launch_bounds__(kAppThreads) append_chunk_kernel(const AppendArgs a) {
+__global__ void __launch_bounds__(kAppThreads, 4) append_chunk_kernel(const AppendArgs a) {
   launch_dependents();
-  // sines of pair 8 e + k at [k][e]: the 8 threads of a row read neighbouring words
-  __shared__ float2 s_cs[kAppTokens][8][8];
   grid_dependency_wait();
   const KvView& kv = a.kv;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int h0 = blockIdx.y * a.heads_per_cta;
   const int nh = min(a.heads_per_cta, kv.Hkv - h0);
-  const int G = kv.G, half = a.rot_dim / 2;
+  const int G = kv.G, g = kv.p / a.lp;
   const int t0 = blockIdx.x * kAppTokens, t1 = min(t0 + kAppTokens, a.tokens);
-  // this thread's two pieces of a turned row: the same dims of both halves, neighbours where pairs are
-  // neighbours, and behind the turned dims (piece 2 hp + 2 (e - hp) = 2 e)
-  const int e = tid & 7, hp = half / 8;
-  const int turn_a = !a.interleaved && e < hp ? e : 2 * e;
-  const int turn_b = !a.interleaved && e < hp ? e + hp : 2 * e + 1;
 
   // The runs that begin here, found by one warp: a token each, their dependent reads side by side.
+  // Token and metadata work of all runs are then one list each for the warps.
   struct Run {
-    int n, pos, len, phys, first_run, last_run;
+    int lead, pos, len, phys;  // first token, its position, the request's length, the page (-1: bad)
+    int sub0, subs;            // metadata records to renew: first, how many
+    int token_end, meta_end;   // tokens and (head, record) pairs of the runs up to this one
   };
   __shared__ Run s_run[kAppTokens];
-  __shared__ uint32_t s_leads;
   if (warp == 0) {
     const int t = t0 + lane;
-    bool leads = false;
+    Run r = {t, 0, 0, -1, 0, 0, 0, 0};
+    int n = 0;
     if (lane < kAppTokens && t < t1) {
       const int b = a.row[t], pos = a.pos[t];
       if (b >= 0 && b < kv.B && pos >= 0) {
         const int first = a.start[b], n_new = a.count[b];
-        leads = t >= first && t - first < n_new && (t == first || pos % a.unit == 0);
-        if (leads) {
-          Run r;
-          r.n = min(min(a.unit - pos % a.unit, first + n_new - t), a.tokens - t);
+        if (t >= first && t - first < n_new && (t == first || pos % a.unit == 0)) {
+          n = min(min(a.unit - pos % a.unit, first + n_new - t), a.tokens - t);
           r.pos = pos;
           r.len = request_len(kv, b);
           const int j = pos / kv.p;
-          r.phys = -1;
           if (j < kv.max_pages) r.phys = kv.page_table[static_cast<size_t>(b) * kv.max_pages + j];
           if (r.phys < 0 || r.phys >= kv.num_phys) {
             r.phys = -1;
             raise_status(kv.status, DSA_STATUS_BAD_PAGE);
+          } else if (a.meta != nullptr) {
+            // records of the run's unit; the request's first run also renews those before it in its
+            // page, its last run writes those behind it (no valid token: zeros), as the build does
+            const int u0 = (pos - j * kv.p) / a.unit * a.unit;
+            const bool last = t + n == first + n_new || (j + 1) * kv.p == pos + n;
+            r.sub0 = t == first ? 0 : u0 / a.lp;
+            r.subs = (last ? g : (u0 + a.unit) / a.lp) - r.sub0;
           }
-          r.first_run = t == first;
-          r.last_run = t + r.n == first + n_new || j != (pos + r.n) / kv.p;
-          s_run[lane] = r;
         }
       }
     }
-    const uint32_t m = __ballot_sync(0xffffffffu, leads);
-    if (lane == 0) s_leads = m;
+    int tokens = n, metas = r.subs * nh;
+#pragma unroll
+    for (int o = 1; o < kAppTokens; o <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, tokens, o), y = __shfl_up_sync(0xffffffffu, metas, o);
+      if (lane >= o) {
+        tokens += x;
+        metas += y;
+      }
+    }
+    r.token_end = tokens;
+    r.meta_end = metas;
+    if (lane < kAppTokens) s_run[lane] = r;
   }
   __syncthreads();
 
-  for (uint32_t todo = s_leads; todo != 0; todo &= todo - 1) {
-    const int at = __ffs(todo) - 1, lead = t0 + at;
-    const Run run = s_run[at];
-    const int n = run.n, pos = run.pos, phys = run.phys, j = pos / kv.p;
-    const bool ok = phys >= 0;
-    const int slot0 = pos - j * kv.p;
-
-    for (int c0 = 0; c0 < n; c0 += kAppTokens) {
-      const int nt = min(kAppTokens, n - c0);
-      if (a.phase) {
-        __syncthreads();
-        for (int i = tid; i < nt * half; i += kAppThreads) {
-          const int tt = i / half, pr = i - tt * half;
-          const int t = lead + c0 + tt;
-          const int ax = a.axis ? min(static_cast<int>(a.axis[pr]), a.num_axes - 1) : 0;
-          const long long where =
-              a.positions ? a.positions[static_cast<size_t>(ax) * a.tokens + t] : pos + c0 + tt;
-          // position x phase modulo one turn, exact in 64-bit integers whatever the position
-          s_cs[tt][pr & 7][pr >> 3] = cos_sin_turn(static_cast<unsigned long long>(where) * a.phase[pr]);
-        }
-        __syncthreads();
-      }
-      // Rows of a token: its query heads, its keys, its values; 8 threads a row, two 16-byte pieces
-      // each.  A thread walks the (token, row) pairs 32 apart, kAppBatch of them at a time with all
-      // their loads in flight.
-      const int nq = a.q ? nh * G : 0;
-      const int rows = nq + 2 * nh;
-      int tt = 0, rr = tid >> 3;
-      const int step_t = 32 / rows, step_r = 32 - step_t * rows;
-      while (rr >= rows) {
-        rr -= rows;
-        ++tt;
-      }
-      while (tt < nt) {
-        uint4 xa[kAppBatch], xb[kAppBatch];
-        __nv_bfloat16* dst[kAppBatch];
-        int cs_of[kAppBatch];  // token whose sines turn the row, -1: none
-#pragma unroll
-        for (int u = 0; u < kAppBatch; ++u) {
-          dst[u] = nullptr;
-          cs_of[u] = -1;
-          if (tt < nt) {
-            const int t = lead + c0 + tt;
-            const __nv_bfloat16* src;
-            if (rr < nq) {
-              const int hq = h0 * G + rr;
-              src = a.q + static_cast<size_t>(t) * a.q_stride + hq * kHeadDim;
-              dst[u] = a.q_out + (static_cast<size_t>(t) * kv.Hq + hq) * kHeadDim;
-              if (a.phase) cs_of[u] = tt;
-            } else {
-              const bool is_v = rr - nq >= nh;
-              const int h = h0 + rr - nq - (is_v ? nh : 0);
-              src = is_v ? a.v + static_cast<size_t>(t) * a.v_stride + h * kHeadDim
-                         : a.k + static_cast<size_t>(t) * a.k_stride + h * kHeadDim;
-              if (ok)
-                dst[u] = (is_v ? a.v_pages : a.k_pages) +
-                         ((static_cast<size_t>(phys) * kv.Hkv + h) * kv.p + slot0 + c0 + tt) * kHeadDim;
-              if (a.phase && !is_v) cs_of[u] = tt;
-            }
-            if (dst[u] != nullptr) {
-              const int ca = cs_of[u] >= 0 ? turn_a : 2 * e, cb = cs_of[u] >= 0 ? turn_b : 2 * e + 1;
-              xa[u] = *reinterpret_cast<const uint4*>(src + ca * 8);
-              xb[u] = *reinterpret_cast<const uint4*>(src + cb * 8);
-            }
-          }
-          tt += step_t;
-          rr += step_r;
-          if (rr >= rows) {
-            rr -= rows;
-            ++tt;
-          }
-        }
-#pragma unroll
-        for (int u = 0; u < kAppBatch; ++u) {
-          if (dst[u] == nullptr) continue;
-          const bool turn = cs_of[u] >= 0;
-          const int ca = turn ? turn_a : 2 * e, cb = turn ? turn_b : 2 * e + 1;
-          if (turn) {
-            const float2* cs = &s_cs[cs_of[u]][0][e];
-            if (e < hp) {
-              if (a.interleaved) {
-                xa[u] = rotate_pairs(xa[u], cs);
-                xb[u] = rotate_pairs(xb[u], cs + 4 * 8);
-              } else {
-                uint4 ya, yb;
-                rotate8(xa[u], xb[u], cs, ya, yb);
-                xa[u] = ya;
-                xb[u] = yb;
-              }
-            }
-          }
-          *reinterpret_cast<uint4*>(dst[u] + ca * 8) = xa[u];
-          *reinterpret_cast<uint4*>(dst[u] + cb * 8) = xb[u];
-        }
-      }
+  const int token_total = s_run[kAppTokens - 1].token_end, meta_total = s_run[kAppTokens - 1].meta_end;
+  const int my_token_end = s_run[lane & (kAppTokens - 1)].token_end;
+  for (int x = warp; x < token_total; x += kAppThreads / 32) {
+    const int at = __ffs(__ballot_sync(0xffffffffu, my_token_end > x)) - 1;
+    const Run& run = s_run[at];
+    const int i = x - (at > 0 ? s_run[at - 1].token_end : 0);  // token of the run
+    const int t = run.lead + i, pos = run.pos + i, phys = run.phys;
+    Turn r = {};
+    if (a.phase) r = make_turn(a, t, pos, lane);
+    if (a.q) {
+      const __nv_bfloat16* src = a.q + static_cast<size_t>(t) * a.q_stride + h0 * G * kHeadDim + 4 * lane;
+      __nv_bfloat16* dst = a.q_out + (static_cast<size_t>(t) * kv.Hq + h0 * G) * kHeadDim + 4 * lane;
+      if (a.phase)
+        move_rows<true>(src, kHeadDim, dst, kHeadDim, nh * G, r);
+      else
+        move_rows<false>(src, kHeadDim, dst, kHeadDim, nh * G, r);
     }
-    if (a.meta != nullptr && ok) {
-      // records of the run's unit; the request's first run also renews those before it in its page,
-      // its last run writes those behind it (no valid token: zeros), as the build does
-      const int g = kv.p / a.lp;
-      const int u0 = (pos % kv.p) / a.unit * a.unit;
-      const int sub0 = run.first_run ? 0 : u0 / a.lp;
-      const int sub1 = run.last_run ? g : (u0 + a.unit) / a.lp;
-      __threadfence_block();
-      __syncthreads();
-      for (int i = warp; i < nh * (sub1 - sub0); i += kAppThreads / 32) {
-        const int h = h0 + i / (sub1 - sub0), sub = sub0 + i % (sub1 - sub0);
-        page_meta<KIND, true>(kv, a.k_pages, a.lp, a.meta, j, h, phys, run.len, lane, sub, sub + 1);
-      }
-    }
+    if (phys < 0) continue;
+    const size_t at_row = ((static_cast<size_t>(phys) * kv.Hkv + h0) * kv.p + pos % kv.p) * kHeadDim + 4 * lane;
+    const long long page_step = static_cast<long long>(kv.p) * kHeadDim;
+    const __nv_bfloat16* src = a.k + static_cast<size_t>(t) * a.k_stride + h0 * kHeadDim + 4 * lane;
+    if (a.phase)
+      move_rows<true>(src, kHeadDim, a.k_pages + at_row, page_step, nh, r);
+    else
+      move_rows<false>(src, kHeadDim, a.k_pages + at_row, page_step, nh, r);
+    move_rows<false>(a.v + static_cast<size_t>(t) * a.v_stride + h0 * kHeadDim + 4 * lane, kHeadDim,
+                     a.v_pages + at_row, page_step, nh, r);
+  }
+  if (meta_total == 0) return;
+  __threadfence_block();
+  __syncthreads();  // the runs' keys are written
+  const int my_meta_end = s_run[lane & (kAppTokens - 1)].meta_end;
+  for (int x = warp; x < meta_total; x += kAppThreads / 32) {
+    const int at = __ffs(__ballot_sync(0xffffffffu, my_meta_end > x)) - 1;
+    const Run& run = s_run[at];
+    const int i = x - (at > 0 ? s_run[at - 1].meta_end : 0);
+    const int h = h0 + i / run.subs, sub = run.sub0 + i % run.subs;
+    page_meta<KIND, true>(kv, a.k_pages, a.lp, a.meta, run.pos / kv.p, h, run.phys, run.len, lane, sub,
+                          sub + 1);
   }
 }
 
