@@ -216,17 +216,19 @@ __global__ void __launch_bounds__(kPlanThreads) plan_chunk_kernel(const PlanArgs
 }
 
 // -------------------------------------------------------------------------------------- append
-// Work is cut at logical-page boundaries so that one CTA writes every new key of the metadata
-// records it makes: a "run" is the new tokens of one request inside one unit of `unit` positions (a
-// multiple of the logical page, at least 16 tokens where the page allows it).  CTA (x, y) takes the
-// runs whose first token lies in [16 x, 16 x + 16) of the chunk, for its group of KV heads and their
-// query heads.  A warp takes a token: its 32 lanes hold 4 of the 128 dims each, with their cosines and
-// sines in registers for all heads of the group, and the rows of 256 bytes stream through kAppRows at
-// a time.
+// Two kinds of CTA in one launch.  Query CTAs turn the queries, a warp a token (or some of its heads):
+// nothing there depends on a page.  Key CTAs turn and write keys and values and renew the metadata.
+// Their work is cut at logical-page boundaries so that one CTA writes every new key of the records it
+// makes: a "run" is the new tokens of one request inside one unit of `unit` positions (a multiple of
+// the logical page, at least 16 tokens where the page allows it), and CTA (x, y) takes the runs whose
+// first token lies in [16 x, 16 x + 16) of the chunk, for its group of KV heads.  In both a warp's 32
+// lanes hold 4 of the 128 dims each, with their cosines and sines in registers for all its rows of 256
+// bytes, and the first rows are on their way while the sines are worked out.
 constexpr int kAppThreads = 256;
 constexpr int kAppTokens = 16;
-constexpr int kAppRows = 8;
-constexpr int kAppCtas = 4 * 152;  // CTAs wanted before heads are shared
+constexpr int kAppRows = 4;
+constexpr int kAppCtas = 3 * 152;  // key CTAs wanted before heads share one
+constexpr int kAppWarps = 32 * 152;  // query warps wanted before heads share one
 
 // ---- cosine and sine of a fraction of a turn (64-bit fixed point), to the last bit of fp32 but for
 // about one value in 10^5: keys that lie next to a rounding border of bf16 then fall on the same side
@@ -323,23 +325,38 @@ DSA_DEV uint2 turn_row(const uint2& x, const Turn& r) {
   return r.on ? y : x;
 }
 
-// The lane's Turn for token t at chunk position pos: lane l works out pairs l and l + 32 and the warp
-// shares them.
-DSA_DEV Turn make_turn(const AppendArgs& a, int t, int pos, int lane) {
-  const int half = a.rot_dim / 2;
-  float2 v[2];
+// The pairs lane and lane + 32 of a token, which this lane works out: their phases and axes.
+struct Pairs {
+  unsigned long long phase[2];
+  int axis[2];
+};
+DSA_DEV Pairs lane_pairs(const AppendArgs& a, int lane) {
+  Pairs p = {};
+  if (a.phase == nullptr) return p;
 #pragma unroll
   for (int w = 0; w < 2; ++w) {
     const int pr = lane + 32 * w;
-    v[w] = make_float2(1.f, 0.f);
-    if (pr < half) {
-      const int ax = a.axis ? min(static_cast<int>(a.axis[pr]), a.num_axes - 1) : 0;
-      const long long where =
-          a.positions ? a.positions[static_cast<size_t>(ax) * a.tokens + t] : pos;
-      // position x phase modulo one turn, exact in 64-bit integers whatever the position
-      v[w] = cos_sin_turn(static_cast<unsigned long long>(where) * a.phase[pr]);
+    if (pr < a.rot_dim / 2) {
+      p.phase[w] = a.phase[pr];
+      p.axis[w] = a.axis ? min(static_cast<int>(a.axis[pr]), a.num_axes - 1) : 0;
     }
   }
+  return p;
+}
+
+// Where those pairs of token t stand (pos: its chunk position).
+DSA_DEV int2 pair_positions(const AppendArgs& a, const Pairs& p, int t, int pos) {
+  if (a.positions == nullptr) return make_int2(pos, pos);
+  return make_int2(a.positions[static_cast<size_t>(p.axis[0]) * a.tokens + t],
+                   a.positions[static_cast<size_t>(p.axis[1]) * a.tokens + t]);
+}
+
+// The lane's Turn: every lane works out its two pairs and the warp shares them.
+DSA_DEV Turn make_turn(const AppendArgs& a, const Pairs& p, int2 where, int lane) {
+  const int half = a.rot_dim / 2;
+  // position x phase modulo one turn, exact in 64-bit integers whatever the position
+  const float2 v0 = cos_sin_turn(static_cast<unsigned long long>(static_cast<long long>(where.x)) * p.phase[0]);
+  const float2 v1 = cos_sin_turn(static_cast<unsigned long long>(static_cast<long long>(where.y)) * p.phase[1]);
   Turn r;
   r.on = 4 * lane < a.rot_dim;
   r.inside = a.interleaved;
@@ -348,8 +365,8 @@ DSA_DEV Turn make_turn(const AppendArgs& a, int t, int pos, int lane) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int pr = !r.on ? 0 : r.inside ? 2 * lane + i / 2 : low ? 4 * lane + i : 4 * lane - half + i;
-    const float c0 = __shfl_sync(0xffffffffu, v[0].x, pr & 31), c1 = __shfl_sync(0xffffffffu, v[1].x, pr & 31);
-    const float s0 = __shfl_sync(0xffffffffu, v[0].y, pr & 31), s1 = __shfl_sync(0xffffffffu, v[1].y, pr & 31);
+    const float c0 = __shfl_sync(0xffffffffu, v0.x, pr & 31), c1 = __shfl_sync(0xffffffffu, v1.x, pr & 31);
+    const float s0 = __shfl_sync(0xffffffffu, v0.y, pr & 31), s1 = __shfl_sync(0xffffffffu, v1.y, pr & 31);
     const bool minus = r.inside ? i % 2 == 0 : low;
     r.c[i] = pr < 32 ? c0 : c1;
     r.s[i] = pr < 32 ? s0 : s1;
@@ -358,22 +375,19 @@ DSA_DEV Turn make_turn(const AppendArgs& a, int t, int pos, int lane) {
   return r;
 }
 
-// `rows` rows of 256 bytes from src to dst, turned or as they are (strides in elements).
-template <bool TURN>
-DSA_DEV void move_rows(const __nv_bfloat16* src, long long src_step, __nv_bfloat16* dst,
-                       long long dst_step, int rows, const Turn& r) {
-  for (int r0 = 0; r0 < rows; r0 += kAppRows) {
-    uint2 x[kAppRows];
+// N rows of 256 bytes, of which `rows` are there (strides in elements).
+template <int N>
+DSA_DEV void load_rows(uint2 (&x)[N], const __nv_bfloat16* src, int rows) {
 #pragma unroll
-    for (int i = 0; i < kAppRows; ++i)
-      if (r0 + i < rows) x[i] = *reinterpret_cast<const uint2*>(src + i * src_step);
+  for (int i = 0; i < N; ++i)
+    if (i < rows) x[i] = *reinterpret_cast<const uint2*>(src + i * kHeadDim);
+}
+template <int N>
+DSA_DEV void store_rows(const uint2 (&x)[N], __nv_bfloat16* dst, int step, int rows, bool turn,
+                        const Turn& r) {
 #pragma unroll
-    for (int i = 0; i < kAppRows; ++i)
-      if (r0 + i < rows)
-        *reinterpret_cast<uint2*>(dst + i * dst_step) = TURN ? turn_row(x[i], r) : x[i];
-    src += kAppRows * src_step;
-    dst += kAppRows * dst_step;
-  }
+  for (int i = 0; i < N; ++i)
+    if (i < rows) *reinterpret_cast<uint2*>(dst + i * step) = turn ? turn_row(x[i], r) : x[i];
 }
 
 template <int KIND>
@@ -382,10 +396,38 @@ __global__ void __launch_bounds__(kAppThreads, 4) append_chunk_kernel(const Appe
   grid_dependency_wait();
   const KvView& kv = a.kv;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int h0 = blockIdx.y * a.heads_per_cta;
+  const bool turn = a.phase != nullptr;
+  const Pairs pairs = lane_pairs(a, lane);
+
+  if (static_cast<int>(blockIdx.x) >= a.key_ctas) {  // queries
+    const long long x = static_cast<long long>(blockIdx.x - a.key_ctas) * (kAppThreads / 32) + warp;
+    const int t = static_cast<int>(x / a.q_parts), part = static_cast<int>(x - static_cast<long long>(t) * a.q_parts);
+    const int hq0 = part * a.q_heads, nq = min(a.q_heads, kv.Hq - hq0);
+    if (t >= a.tokens || nq <= 0) return;
+    const __nv_bfloat16* src = a.q + static_cast<size_t>(t) * a.q_stride + hq0 * kHeadDim + 4 * lane;
+    __nv_bfloat16* dst = a.q_out + (static_cast<size_t>(t) * kv.Hq + hq0) * kHeadDim + 4 * lane;
+    uint2 xq[kAppRows];
+    load_rows(xq, src, nq);
+    const int b = a.row[t], pos = a.pos[t];
+    const int2 where = pair_positions(a, pairs, t, pos);
+    if (b < 0) return;
+    Turn r = {};
+    if (turn) r = make_turn(a, pairs, where, lane);
+    for (int h = 0; h < nq; h += kAppRows) {
+      uint2 next[kAppRows];
+      load_rows(next, src + (h + kAppRows) * kHeadDim, nq - h - kAppRows);
+      store_rows(xq, dst + h * kHeadDim, kHeadDim, nq - h, turn, r);
+#pragma unroll
+      for (int i = 0; i < kAppRows; ++i) xq[i] = next[i];
+    }
+    return;
+  }
+
+  const int groups = (kv.Hkv + a.heads_per_cta - 1) / a.heads_per_cta;
+  const int h0 = blockIdx.x % groups * a.heads_per_cta;
   const int nh = min(a.heads_per_cta, kv.Hkv - h0);
-  const int G = kv.G, g = kv.p / a.lp;
-  const int t0 = blockIdx.x * kAppTokens, t1 = min(t0 + kAppTokens, a.tokens);
+  const int g = kv.p / a.lp;
+  const int t0 = blockIdx.x / groups * kAppTokens, t1 = min(t0 + kAppTokens, a.tokens);
 
   // The runs that begin here, found by one warp: a token each, their dependent reads side by side.
   // Token and metadata work of all runs are then one list each for the warps.
@@ -445,26 +487,24 @@ __global__ void __launch_bounds__(kAppThreads, 4) append_chunk_kernel(const Appe
     const Run& run = s_run[at];
     const int i = x - (at > 0 ? s_run[at - 1].token_end : 0);  // token of the run
     const int t = run.lead + i, pos = run.pos + i, phys = run.phys;
-    Turn r = {};
-    if (a.phase) r = make_turn(a, t, pos, lane);
-    if (a.q) {
-      const __nv_bfloat16* src = a.q + static_cast<size_t>(t) * a.q_stride + h0 * G * kHeadDim + 4 * lane;
-      __nv_bfloat16* dst = a.q_out + (static_cast<size_t>(t) * kv.Hq + h0 * G) * kHeadDim + 4 * lane;
-      if (a.phase)
-        move_rows<true>(src, kHeadDim, dst, kHeadDim, nh * G, r);
-      else
-        move_rows<false>(src, kHeadDim, dst, kHeadDim, nh * G, r);
-    }
+    const __nv_bfloat16* ksrc = a.k + static_cast<size_t>(t) * a.k_stride + h0 * kHeadDim + 4 * lane;
+    const __nv_bfloat16* vsrc = a.v + static_cast<size_t>(t) * a.v_stride + h0 * kHeadDim + 4 * lane;
     if (phys < 0) continue;
-    const size_t at_row = ((static_cast<size_t>(phys) * kv.Hkv + h0) * kv.p + pos % kv.p) * kHeadDim + 4 * lane;
-    const long long page_step = static_cast<long long>(kv.p) * kHeadDim;
-    const __nv_bfloat16* src = a.k + static_cast<size_t>(t) * a.k_stride + h0 * kHeadDim + 4 * lane;
-    if (a.phase)
-      move_rows<true>(src, kHeadDim, a.k_pages + at_row, page_step, nh, r);
-    else
-      move_rows<false>(src, kHeadDim, a.k_pages + at_row, page_step, nh, r);
-    move_rows<false>(a.v + static_cast<size_t>(t) * a.v_stride + h0 * kHeadDim + 4 * lane, kHeadDim,
-                     a.v_pages + at_row, page_step, nh, r);
+    uint2 xk[kAppRows], xv[kAppRows];
+    load_rows(xk, ksrc, nh);
+    load_rows(xv, vsrc, nh);
+    Turn r = {};
+    if (turn) r = make_turn(a, pairs, pair_positions(a, pairs, t, pos), lane);
+    const size_t at_row =
+        ((static_cast<size_t>(phys) * kv.Hkv + h0) * kv.p + pos % kv.p) * kHeadDim + 4 * lane;
+    const int page_step = kv.p * kHeadDim;
+    for (int h = 0; h < nh; h += kAppRows) {
+      const size_t to = at_row + static_cast<size_t>(h) * page_step;
+      store_rows(xv, a.v_pages + to, page_step, nh - h, false, r);
+      store_rows(xk, a.k_pages + to, page_step, nh - h, turn, r);
+      load_rows(xk, ksrc + (h + kAppRows) * kHeadDim, nh - h - kAppRows);
+      load_rows(xv, vsrc + (h + kAppRows) * kHeadDim, nh - h - kAppRows);
+    }
   }
   if (meta_total == 0) return;
   __threadfence_block();
@@ -509,10 +549,21 @@ cudaError_t launch_append_chunk(const AppendArgs& in, int kind, cudaStream_t s) 
   while (hpc > 1 && static_cast<long long>(gx) * ((a.kv.Hkv + hpc - 1) / hpc) < kAppCtas)
     hpc = (hpc + 1) / 2;
   a.heads_per_cta = hpc;
-  dim3 grid(gx, (a.kv.Hkv + hpc - 1) / hpc);
+  const long long key_ctas = static_cast<long long>(gx) * ((a.kv.Hkv + hpc - 1) / hpc);
+  // query heads of one warp: all of a token's heads share its sines, but few tokens need the warps
+  a.q_heads = a.kv.Hq;
+  while (a.q_heads > kAppRows &&
+         static_cast<long long>(a.tokens) * ((a.kv.Hq + a.q_heads - 1) / a.q_heads) < kAppWarps)
+    a.q_heads = (a.q_heads + 1) / 2;
+  a.q_parts = (a.kv.Hq + a.q_heads - 1) / a.q_heads;
+  const long long q_warps = a.q ? static_cast<long long>(a.tokens) * a.q_parts : 0;
+  const long long grid = key_ctas + (q_warps + kAppThreads / 32 - 1) / (kAppThreads / 32);
+  if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
+  a.key_ctas = static_cast<int>(key_ctas);
+  const unsigned n = static_cast<unsigned>(grid);
   return kind == DSA_META_MINMAX
-             ? launch_pdl(append_chunk_kernel<DSA_META_MINMAX>, grid, kAppThreads, 0, s, a)
-             : launch_pdl(append_chunk_kernel<DSA_META_MEAN>, grid, kAppThreads, 0, s, a);
+             ? launch_pdl(append_chunk_kernel<DSA_META_MINMAX>, n, kAppThreads, 0, s, a)
+             : launch_pdl(append_chunk_kernel<DSA_META_MEAN>, n, kAppThreads, 0, s, a);
 }
 
 }  // namespace dsa

@@ -267,7 +267,7 @@ struct AppendArgs {
   int num_axes, rot_dim, interleaved;
   int lp;
   void* meta;  // may be null
-  int unit, heads_per_cta;  // set by the launch
+  int unit, heads_per_cta, key_ctas, q_heads, q_parts;  // set by the launch
 };
 cudaError_t launch_append_chunk(const AppendArgs& a, int kind, cudaStream_t s);
 

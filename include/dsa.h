@@ -580,7 +580,7 @@ typedef struct dsa_rotary {
  *   meta         : as for dsa_append_kv, or NULL.  A caller keeping several metadata buffers calls
  *                  once per buffer, with q NULL after the first (turning q in place twice would turn
  *                  it twice; the KV write repeats harmlessly).
- * Tokens with row -1 and those behind start[B] are neither read nor written.  A token on a bad page
+ * Nothing is written for tokens with row -1 and those behind start[B].  A token on a bad page
  * id is skipped (its query is still turned) and raises DSA_STATUS_BAD_PAGE.
  */
 int dsa_append_chunk(const dsa_paged_kv* kv, const dsa_chunk* chunk, const void* k_new,
