@@ -10,24 +10,15 @@ namespace {
 // ---------------------------------------------------------------------------------------- plan
 // Three prefix sums over the requests decide everything: start (new tokens), gone (pages given
 // back) and need (pages taken).  Every CTA makes them for itself from the 8 bytes per request (B is
-// small against what follows, and no CTA then waits for another), keeps them in shared memory and
-// expands its share of the tokens, of the taken pages and of the returned pages, each with a binary
-// search.  Lengths and stack height may be updated in place, so they are written by the CTA that
-// takes the last ticket, when every other CTA has read them.
+// small against what follows, and no CTA then waits for another): a thread sums a run of neighbouring
+// requests, two block scans join the runs (need depends on start).  Kept in shared memory, they place
+// the CTA's share of the tokens, of the taken pages and of the returned pages by binary search.
+// Lengths and stack height may be updated in place, so they are written by the CTA that takes the last
+// ticket, when every other CTA has read them.
+// What bounds it is latency: a launch, one round of reads for the lengths, one for the table or the
+// stack, one atomic.
 constexpr int kPlanThreads = 512;
-constexpr int kPlanTokens = 2 * kPlanThreads;  // tokens per CTA
-
-struct Sums {
-  long long start, gone, need;
-};
-
-DSA_DEV Sums shfl_up(const Sums& s, int o) {
-  return {__shfl_up_sync(0xffffffffu, s.start, o), __shfl_up_sync(0xffffffffu, s.gone, o),
-          __shfl_up_sync(0xffffffffu, s.need, o)};
-}
-DSA_DEV Sums operator+(const Sums& a, const Sums& b) {
-  return {a.start + b.start, a.gone + b.gone, a.need + b.need};
-}
+constexpr int kPlanWarps = kPlanThreads / 32;
 
 DSA_DEV int clamp_i32(long long v) {
   return static_cast<int>(v < 0x7fffffffLL ? v : 0x7fffffffLL);
@@ -46,113 +37,110 @@ DSA_DEV int first_above(const int* end, int n, int v) {
   return lo;
 }
 
-struct PlanLen {
-  int len, delta, have, keep;  // clamped length, change, pages held, pages kept (delta < 0)
-};
-
-DSA_DEV PlanLen plan_len(const PlanArgs& a, int b) {
-  PlanLen r;
-  r.len = min(max(a.lens_in[b], 0), a.p * a.max_pages);
-  r.delta = a.delta[b];
-  r.have = (r.len + a.p - 1) / a.p;
-  r.keep = r.have;
-  if (r.delta < 0) {
-    const long long left = static_cast<long long>(r.len) + r.delta;
-    r.keep = left > 0 ? static_cast<int>((left + a.p - 1) / a.p) : 0;
+// Exclusive prefix over the block of one value per thread; `part` holds kPlanWarps words.
+template <typename T>
+DSA_DEV T block_prefix(T v, T* part, T* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  T inc = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const T up = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += up;
   }
-  return r;
+  if (lane == 31) part[warp] = inc;
+  __syncthreads();
+  T base = 0, sum = 0;
+#pragma unroll
+  for (int w = 0; w < kPlanWarps; ++w) {
+    if (w < warp) base += part[w];
+    sum += part[w];
+  }
+  *total = sum;
+  return base + inc - v;
 }
 
 __global__ void __launch_bounds__(kPlanThreads) plan_chunk_kernel(const PlanArgs a) {
   launch_dependents();
   extern __shared__ int sm[];
-  int* s_start = sm;                // [B]: first token of each request
-  int* s_start_end = sm + a.B;      // [B]: one past its last token
-  int* s_gone = sm + 2 * a.B;       // [B]: pages given back by requests 0..b
-  int* s_need = sm + 3 * a.B;       // [B]: pages needed by requests 0..b
-  int* s_count = sm + 4 * a.B;      // [B]: new tokens wanted, 0 when the request cannot hold them
-  __shared__ Sums s_warp[kPlanThreads / 32];
+  int* s_end = sm;              // [B]: one past each request's last token
+  int* s_gone = sm + a.B;       // [B]: pages given back by requests 0..b
+  int* s_need = sm + 2 * a.B;   // [B]: pages needed by requests 0..b
+  int* s_count = sm + 3 * a.B;  // [B]: new tokens that take part
+  int* s_len = sm + 4 * a.B;    // [B]: length before
+  int* s_keep = sm + 5 * a.B;   // [B]: length kept (below s_len where tokens are dropped)
+  __shared__ long long s_part_ll[kPlanWarps];
+  __shared__ int s_part[2][kPlanWarps];
   __shared__ int s_taken, s_last;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x;
   if (tid == 0) s_taken = 0;
+  const int most = a.p * a.max_pages;
+  auto pages = [&](int len) { return (len + a.p - 1) / a.p; };
   grid_dependency_wait();
 
-  Sums carry = {0, 0, 0};
-  for (int b0 = 0; b0 < a.B; b0 += kPlanThreads) {
-    const int b = b0 + tid;
-    PlanLen r = {0, 0, 0, 0};
-    if (b < a.B) r = plan_len(a, b);
-    Sums own = {max(r.delta, 0), r.have - r.keep, 0};
-    Sums inc = own;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const Sums up = shfl_up(inc, o);
-      if (lane >= o) inc = inc + up;
-    }
-    if (lane == 31) s_warp[warp] = inc;
-    __syncthreads();
-    Sums base = carry;
-    for (int w = 0; w < warp; ++w) base = base + s_warp[w];
-    for (int w = 0; w < kPlanThreads / 32; ++w) carry = carry + s_warp[w];
-    inc = base + inc;
-    // a request takes part when its tokens lie inside the chunk and its table row can hold them
-    const long long grown = static_cast<long long>(r.len) + own.start;
-    const bool fits = inc.start <= a.tokens && grown <= static_cast<long long>(a.p) * a.max_pages;
-    const int need =
-        fits && own.start > 0 ? static_cast<int>((grown + a.p - 1) / a.p) - r.have : 0;
-    Sums nd = {0, 0, need};
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long up = __shfl_up_sync(0xffffffffu, nd.need, o);
-      if (lane >= o) nd.need += up;
-    }
-    __syncthreads();
-    if (lane == 31) s_warp[warp].need = nd.need;
-    __syncthreads();
-    long long need_base = carry.need, need_total = 0;
-    for (int w = 0; w < kPlanThreads / 32; ++w) {
-      if (w < warp) need_base += s_warp[w].need;
-      need_total += s_warp[w].need;
-    }
-    if (b < a.B) {
-      s_start[b] = clamp_i32(inc.start - own.start);
-      s_start_end[b] = clamp_i32(inc.start);
-      s_gone[b] = clamp_i32(inc.gone);
-      s_need[b] = clamp_i32(need_base + nd.need);
-      s_count[b] = fits ? max(r.delta, 0) : 0;
-    }
-    carry.need += need_total;
-    __syncthreads();
+  const int each = (a.B + kPlanThreads - 1) / kPlanThreads;  // neighbouring requests of a thread
+  const int b0 = min(tid * each, a.B), b1 = min(b0 + each, a.B);
+  const int held = min(max(a.free_in[0], 0), a.free_capacity);  // pages on the stack
+  long long start = 0;
+  int gone = 0;
+  for (int b = b0; b < b1; ++b) {
+    const int len = min(max(a.lens_in[b], 0), most), delta = a.delta[b];
+    const int keep =
+        delta < 0 ? static_cast<int>(max(static_cast<long long>(len) + delta, 0LL)) : len;
+    s_len[b] = len;
+    s_keep[b] = keep;
+    s_count[b] = max(delta, 0);
+    start += max(delta, 0);
+    gone += pages(len) - pages(keep);
   }
-
-  const int cap = a.free_capacity;
-  const int held = min(max(a.free_in[0], 0), cap);  // pages on the stack
-  const int gone = s_gone[a.B - 1];
-  const int top = clamp_i32(static_cast<long long>(held) + gone);
+  long long start_total;
+  int gone_total, need_total;
+  start = block_prefix(start, s_part_ll, &start_total);
+  gone = block_prefix(gone, s_part[0], &gone_total);
+  int need = 0;
+  for (int b = b0; b < b1; ++b) {
+    const int want = s_count[b], len = s_len[b];
+    start += want;
+    gone += pages(len) - pages(s_keep[b]);
+    // a request takes part when its tokens lie inside the chunk and its table row can hold them
+    const bool fits = start <= a.tokens && static_cast<long long>(len) + want <= most;
+    if (want > 0 && fits) need += pages(len + want) - pages(len);
+    if (want > 0 && !fits) s_count[b] = -1;
+    s_end[b] = clamp_i32(start);
+    s_gone[b] = gone;
+    s_need[b] = need;
+  }
+  need = block_prefix(need, s_part[1], &need_total);
   // Admission: a request that needs pages gets them when those of all requests up to it fit; one
   // that needs none is always admitted.  s_need never falls, so the pages taken are its last value
   // that fits.
+  const int top = clamp_i32(static_cast<long long>(held) + gone_total);
   bool refused = false;
-  for (int b = tid; b < a.B; b += kPlanThreads) {
-    const int end = s_need[b], before = b > 0 ? s_need[b - 1] : 0;
-    if (end <= top) atomicMax(&s_taken, end);
-    if (end > before && end > top) s_count[b] = 0;
-    if (s_count[b] == 0 && s_start_end[b] > s_start[b]) refused = true;
+  int before = need, taken = 0;
+  for (int b = b0; b < b1; ++b) {
+    const int end = s_need[b] + need;
+    s_need[b] = end;
+    if (end <= top) taken = end;
+    const int want = s_count[b];
+    if (want < 0 || (end > before && end > top)) {
+      s_count[b] = 0;
+      refused |= want != 0;
+    }
+    before = end;
   }
+  if (taken > 0) atomicMax(&s_taken, taken);
   if (__syncthreads_or(refused) && tid == 0 && blockIdx.x == 0)
     raise_status(a.status, DSA_STATUS_NO_PAGES);
-  const int taken = s_taken;
+  taken = s_taken;
   int left = top - taken;
-  if (left > cap) {
-    left = cap;
+  if (left > a.free_capacity) {
+    left = a.free_capacity;
     if (tid == 0 && blockIdx.x == 0) raise_status(a.status, DSA_STATUS_OVERFLOW);
   }
 
   // i-th page given back in this call, in request then position order
   auto returned = [&](int i) {
     const int b = first_above(s_gone, a.B, i);
-    const PlanLen r = plan_len(a, b);
-    const int j = r.keep + i - (b > 0 ? s_gone[b - 1] : 0);
+    const int j = pages(s_keep[b]) + i - (b > 0 ? s_gone[b - 1] : 0);
     return a.page_table[static_cast<size_t>(b) * a.max_pages + j];
   };
   // k-th page taken in this call: from the top of the stack, returned pages included
@@ -163,20 +151,21 @@ __global__ void __launch_bounds__(kPlanThreads) plan_chunk_kernel(const PlanArgs
 
   const int first = blockIdx.x * kPlanThreads + tid, step = gridDim.x * kPlanThreads;
   for (int t = first; t < a.tokens; t += step) {
-    const int b = first_above(s_start_end, a.B, t);
+    const int b = first_above(s_end, a.B, t);
     int row = -1, pos = -1, slot = -1;
     if (b < a.B && s_count[b] > 0) {
-      const int len = min(max(a.lens_in[b], 0), a.p * a.max_pages);
-      const int have = (len + a.p - 1) / a.p;
+      const int len = s_len[b], have = pages(len);
       row = b;
-      pos = len + (t - s_start[b]);
-      const int j = pos / a.p;
-      const int phys = j < have ? a.page_table[static_cast<size_t>(b) * a.max_pages + j]
-                                : page_taken((b > 0 ? s_need[b - 1] : 0) + j - have);
-      if (phys >= 0 && phys < a.num_phys)
-        slot = phys * a.p + pos % a.p;
-      else
-        raise_status(a.status, DSA_STATUS_BAD_PAGE);
+      pos = len + t - (b > 0 ? s_end[b - 1] : 0);
+      if (a.slot) {
+        const int j = pos / a.p;
+        const int phys = j < have ? a.page_table[static_cast<size_t>(b) * a.max_pages + j]
+                                  : page_taken((b > 0 ? s_need[b - 1] : 0) + j - have);
+        if (phys >= 0 && phys < a.num_phys)
+          slot = phys * a.p + pos - j * a.p;
+        else
+          raise_status(a.status, DSA_STATUS_BAD_PAGE);
+      }
     }
     a.row[t] = row;
     a.pos[t] = pos;
@@ -184,11 +173,15 @@ __global__ void __launch_bounds__(kPlanThreads) plan_chunk_kernel(const PlanArgs
   }
   for (int k = first; k < taken; k += step) {
     const int b = first_above(s_need, a.B, k);
-    const PlanLen r = plan_len(a, b);
-    a.page_table[static_cast<size_t>(b) * a.max_pages + r.have + k - (b > 0 ? s_need[b - 1] : 0)] =
+    a.page_table[static_cast<size_t>(b) * a.max_pages + pages(s_len[b]) + k - (b > 0 ? s_need[b - 1] : 0)] =
         page_taken(k);
   }
   for (int s = held + first; s < left; s += step) a.free_pages[s] = returned(s - held);
+  for (int b = first; b < a.B; b += step) {
+    a.start[b + 1] = s_end[b];
+    a.count[b] = s_count[b];
+  }
+  if (first == 0) a.start[0] = 0;
 
   if (gridDim.x > 1) {
     __syncthreads();
@@ -199,20 +192,9 @@ __global__ void __launch_bounds__(kPlanThreads) plan_chunk_kernel(const PlanArgs
     __syncthreads();
     if (!s_last) return;
     if (tid == 0) *a.ticket = 0;
-  } else {
-    __syncthreads();
   }
-  for (int b = tid; b < a.B; b += kPlanThreads) {
-    const PlanLen r = plan_len(a, b);
-    a.start[b] = s_start[b];
-    a.count[b] = s_count[b];
-    a.lens_out[b] = r.delta < 0 ? static_cast<int>(max(static_cast<long long>(r.len) + r.delta, 0LL))
-                                : r.len + s_count[b];
-  }
-  if (tid == 0) {
-    a.start[a.B] = s_start_end[a.B - 1];
-    a.free_out[0] = left;
-  }
+  for (int b = tid; b < a.B; b += kPlanThreads) a.lens_out[b] = s_keep[b] + s_count[b];
+  if (tid == 0) a.free_out[0] = left;
 }
 
 // -------------------------------------------------------------------------------------- append
@@ -522,13 +504,13 @@ __global__ void __launch_bounds__(kAppThreads, 4) append_chunk_kernel(const Appe
 
 }  // namespace
 
-size_t plan_smem_bytes(int B) { return static_cast<size_t>(B) * 5 * sizeof(int); }
+size_t plan_smem_bytes(int B) { return static_cast<size_t>(B) * 6 * sizeof(int); }
 
 cudaError_t launch_plan_chunk(const PlanArgs& a, cudaStream_t s) {
   const size_t bytes = plan_smem_bytes(a.B);
   cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(plan_chunk_kernel), bytes);
   if (e != cudaSuccess) return e;
-  int grid = (a.tokens + kPlanTokens - 1) / kPlanTokens;
+  int grid = (a.tokens + kPlanThreads - 1) / kPlanThreads;  // a token a thread, up to a CTA per SM
   grid = grid < 1 ? 1 : grid > 152 ? 152 : grid;
   return launch_pdl(plan_chunk_kernel, grid, kPlanThreads, bytes, s, a);
 }
