@@ -166,7 +166,8 @@ def _io_ptr(t) -> int:
 
 def _stream(stream) -> int | None:
     if stream is None:
-        stream = torch.cuda.current_stream()
+        # the handle alone: building the Stream object takes as long as the library call itself
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     return stream.cuda_stream
 
 
@@ -481,8 +482,8 @@ def _i32(t, shape, what: str, optional: bool = False):
     """A contiguous int32 CUDA tensor of the given shape (or None), else a ValueError."""
     if t is None and optional:
         return None
-    if t.dtype != torch.int32 or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
-        raise ValueError(f"{what} must be a contiguous int32 tensor of shape {tuple(shape)}, got "
+    if t.dtype is not torch.int32 or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous int32 tensor of shape {shape}, got "
                          f"{t.dtype} {tuple(t.shape)}")
     return _ptr(t)
 
@@ -561,24 +562,28 @@ def dsa_plan_chunk(kv: PagedKV, lens_in, delta, free_pages, free_in, free_out, c
     """Block tables, slot maps and the page stack of a step: writes ``kv``'s page table and lengths,
     ``free_pages`` / ``free_out`` and the chunk's arrays.  ``lens_in`` may be the lengths' own tensor
     and ``free_out`` may be ``free_in``."""
+    rows = (kv.batch,)
     if chunk.batch != kv.batch:
         raise ValueError(f"the chunk holds {chunk.batch} requests, the tables {kv.batch}")
+    n = free_pages.numel()
     _check("dsa_plan_chunk", load().dsa_plan_chunk(
-        ctypes.byref(kv), _i32(lens_in, (kv.batch,), "lens_in"),
-        _i32(delta, (kv.batch,), "delta"), _i32(free_pages, (free_pages.numel(),), "free_pages"),
-        free_pages.numel(), _i32(free_in, (1,), "free_in"), _i32(free_out, (1,), "free_out"),
-        ctypes.byref(chunk), _ptr(workspace), workspace.numel() * workspace.element_size(),
+        ctypes.byref(kv), _i32(lens_in, rows, "lens_in"), _i32(delta, rows, "delta"),
+        _i32(free_pages, (n,), "free_pages"), n, _i32(free_in, (1,), "free_in"),
+        _i32(free_out, (1,), "free_out"), ctypes.byref(chunk), _ptr(workspace), workspace.nbytes,
         _stream(stream)))
 
 
 def _token_rows(t, tokens: int, heads: int, what: str) -> int:
     """Token stride of bf16 ``[tokens][heads][128]`` whose heads are contiguous."""
-    if t.dtype != torch.bfloat16 or tuple(t.shape) != (tokens, heads, 128):
+    if t.dtype is not torch.bfloat16 or t.shape != (tokens, heads, 128):
         raise ValueError(f"{what} must be bf16 [{tokens}][{heads}][128], got {t.dtype} "
                          f"{tuple(t.shape)}")
-    if tokens and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != 128)):
+    if t.is_contiguous():
+        return heads * 128
+    step, head, dim = t.stride()
+    if dim != 1 or (heads > 1 and head != 128):
         raise ValueError(f"{what}: the heads of a token must be contiguous")
-    return t.stride(0) if tokens > 1 else heads * 128
+    return step if tokens > 1 else heads * 128
 
 
 def dsa_append_chunk(kv: PagedKV, chunk: Chunk, k_new, v_new, rotary: Rotary | None = None, q=None,
@@ -620,10 +625,10 @@ def dsa_chunk_attn(kv: PagedKV, chunk: Chunk, q, scale: float, out, m=None, l=No
         if _token_rows(t, n, hq, what) != hq * 128:
             raise ValueError(f"{what} must be contiguous")
     for t, what in ((m, "m"), (l, "l")):
-        if t is not None and (t.dtype != torch.float32 or tuple(t.shape) != (n, hq)
+        if t is not None and (t.dtype is not torch.float32 or t.shape != (n, hq)
                               or not t.is_contiguous()):
             raise ValueError(f"{what} must be contiguous fp32 [{n}][{hq}]")
     _check("dsa_chunk_attn", load().dsa_chunk_attn(
         ctypes.byref(kv), ctypes.byref(chunk), _ptr(q), sink, local, scale, _ptr(out), _ptr(m),
         _ptr(l), _ptr(workspace),
-        0 if workspace is None else workspace.numel() * workspace.element_size(), _stream(stream)))
+        0 if workspace is None else workspace.nbytes, _stream(stream)))
