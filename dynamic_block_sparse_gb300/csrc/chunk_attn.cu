@@ -21,11 +21,13 @@
 // No CTA waits for another.
 //
 // Inside a CTA: warps 0-3 and 4-7 are the streams' softmax warpgroups (a thread owns a row: S from
-// TMEM in one load, P back to TMEM over S as bf16), warps 8 and 11 load (TMA: Q and K tiles; V
-// tiles; of 128 tokens, assembled from page pieces, into a ring of five 32 KB stages, K and V in turn:
-// with pages of 16 tokens one warp issues the 32 pieces of a K and a V tile in more time than the
-// products take), one thread of warp 9 issues the tcgen05 products (S = Q K^T from shared memory, O += P V with P from TMEM), and
-// warp 10 clears the rows behind a request's last token in the V tile that holds it.
+// TMEM, P back to TMEM over S as bf16), warps 8-11 take a finished unit's accumulators out (normalised
+// to the output, or to a record, and the merges) while the softmax is at the next unit, warps 12 and 15
+// load (TMA: Q and K tiles; V tiles; of 128 tokens, assembled from page pieces, into a ring of five
+// 32 KB stages, K and V in turn: with pages of 16 tokens one warp issues the 32 pieces of a K and a V
+// tile in more time than the products take), one thread of warp 13 issues the tcgen05 products (S =
+// Q K^T from shared memory, O += P V with P from TMEM), and warp 14 clears the rows behind a request's
+// last token in the V tile that holds it.
 #include "common.cuh"
 #include "internal.h"
 
@@ -34,17 +36,22 @@
 namespace dsa {
 namespace {
 
-constexpr int kThreads = 384;
-constexpr int kLoadWarp = 8, kMmaWarp = 9, kTailWarp = 10, kValueWarp = 11;
+constexpr int kThreads = 512;
+constexpr int kOutWarp = 8;  // 8 .. 11: the epilogue warpgroup
+constexpr int kLoadWarp = 12, kMmaWarp = 13, kTailWarp = 14, kValueWarp = 15;
 constexpr int kRing = 5;
 constexpr uint32_t kHalfBytes = 128 * 128;  // 64 dims of 128 rows, 128-byte swizzled lines
 constexpr uint32_t kTileBytes = 2 * kHalfBytes;
+// The line of work counts an item's tiles and kItemPad more, what starting and ending a unit costs;
+// and no CTA takes less than kMinWork of it: a cut costs a record, a ticket and a share of a merge,
+// about as much as four tiles.
+constexpr int kItemPad = 1, kMinWork = 5;
 constexpr float kLazyLog2 = 8.f;  // P stays below 2^8 times its weight at the true maximum
 
-// Registers per thread: a softmax thread holds a row of 128 logits.  The launch has 168 x 384 = 64512,
-// and 208 x 256 + 88 x 128 is exactly that.
-constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
-static_assert(kSoftmaxRegs * 256 + kOtherRegs * 128 <= 168 * kThreads, "registers of the launch");
+// Registers per thread of the softmax, the epilogue and the other warps.  The launch has 128 x 512, and
+// 144 x 256 + 128 x 128 + 96 x 128 is exactly that.
+constexpr int kSoftmaxRegs = 144, kOutRegs = 128, kOtherRegs = 96;
+static_assert(kSoftmaxRegs * 256 + (kOutRegs + kOtherRegs) * 128 <= 128 * kThreads, "registers");
 template <int N>
 DSA_DEV void regs_inc() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
@@ -65,23 +72,30 @@ struct Unit {  // a run of key tiles of one item, as published by the load warp
   int cta0, cta1, slot;    // CTAs of a cut item, this unit's record
 };
 
+struct Merge {  // a cut item whose records are all there
+  int tok0, ntok, h, cta0, parts;
+};
+
 // ---- shared memory
 constexpr uint32_t kOffRing = 2 * kTileBytes;
 constexpr uint32_t kOffCtl = kOffRing + kRing * kTileBytes;
 struct Ctl {
   unsigned long long full[kRing], empty[kRing];
-  unsigned long long qfull, qempty, sfull[2], pready[2][2], odone[2], ufull[2], uempty[2], both,
-      tail[4];
+  unsigned long long qfull, qempty, sfull[2], pready[2][2], odone[2], ufull[2], uempty[2],
+      sdone[2], ofree, meet, help, tail[4];
   uint32_t tmem;
   int abort, last, pad;
   Unit unit[2];
+  Merge merge[2];  // cut items to merge at the CTA's end, where the softmax warps lend a hand
+  int merges;
   int tail_stage[4], tail_row[4];  // V tiles with rows to clear: ring stage (-1: the end), first row
   uint32_t kmask[8];      // valid 16-token groups of a key tile
-  float xm[2][128], xl[2][128], xtrue[128];
+  float xm[2][128], xl[2][128];  // a finished unit's reference and sum per stream and row
 };
 constexpr uint32_t kSmemBytes = kOffCtl + sizeof(Ctl);
 static_assert(kSmemBytes <= 227 * 1024, "shared memory of one CTA");
 static_assert(kChunkMaxBatch * 16 + 512 <= kRing * kTileBytes, "the prefix sums overlay the ring");
+static_assert(kChunkMaxBatch * 8 <= 2 * kTileBytes, "the requests overlay the query tiles");
 
 // 32 columns of this thread's TMEM lane.
 DSA_DEV void tmem_ld_32(uint32_t addr, uint32_t (&r)[32]) {
@@ -327,12 +341,19 @@ DSA_DEV void expo(const uint32_t* r, uint64_t sc2, uint64_t mm2, uint64_t& la, u
   }
 }
 
-// The d-th KV head of a kind (streaming or not), found by the whole warp; -1 when there is none.
-DSA_DEV int nth_head(const KvView& kv, bool win, int d, int lane) {
+// The streaming heads among heads h0 .. h0 + 31, and how many of these there are, by the whole warp.
+DSA_DEV uint32_t window_heads(const KvView& kv, int h0, int lane, uint32_t* there) {
+  const int h = h0 + lane;
+  *there = __ballot_sync(0xffffffffu, h < kv.Hkv);
+  return kv.streaming == nullptr ? 0u
+                                 : __ballot_sync(0xffffffffu, h < kv.Hkv && kv.streaming[h] != 0);
+}
+
+// The d-th KV head of a kind (streaming or not); `first` and `there` are window_heads of heads 0 .. 31.
+DSA_DEV int nth_head(const KvView& kv, bool win, int d, int lane, uint32_t first, uint32_t there) {
   for (int h0 = 0; h0 < kv.Hkv; h0 += 32) {
-    const int h = h0 + lane;
-    const bool is_win = h < kv.Hkv && kv.streaming != nullptr && kv.streaming[h] != 0;
-    const uint32_t m = __ballot_sync(0xffffffffu, h < kv.Hkv && is_win == win);
+    if (h0 > 0) first = window_heads(kv, h0, lane, &there);
+    const uint32_t m = win ? first : there & ~first;
     const int c = __popc(m);
     if (d < c) return h0 + static_cast<int>(__fns(m, 0, d + 1));
     d -= c;
@@ -340,10 +361,84 @@ DSA_DEV int nth_head(const KvView& kv, bool win, int d, int lane) {
   return -1;
 }
 
+// a / b for a >= 0, b > 0: places on the line nearly always fit 32 bits, where a division takes a
+// tenth of the time.
+DSA_DEV long long quotient(long long a, long long b) {
+  if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+  return a / b;
+}
+
 // Sets *abort when a wait has given up; true for the whole warp only when it succeeded in every lane.
 DSA_DEV bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort, int32_t* status) {
   const bool ok = mbar_wait(bar, parity, abort, status);
   return __all_sync(0xffffffffu, ok);
+}
+
+// Merges a cut item's records in CTA order with `threads` threads: `per` threads a row, each with 32 / per float4s of it.  Not inlined: its registers are its own.
+__device__ __noinline__ void merge_records(const ChunkAttnArgs& a, const Merge& w, int me, int threads) {
+  const int G = a.kv.G, rows = w.ntok * G;
+  const float sc = a.scale_log2;
+  const size_t R = a.rec_rows;
+  int per = 1;
+  while (per < 32 && 2 * per * rows <= threads) per *= 2;
+  const int at_once = threads / per;
+  const size_t rec4 = R * (kRecordFloats / 4);  // float4s of a record
+  const float4* first = reinterpret_cast<const float4*>(a.records) + 2 * w.cta0 * rec4;
+  auto record = [&](int q) { return first + (2 * q + (q == 0)) * rec4; };
+  for (int r0 = 0; r0 < rows; r0 += at_once) {
+    const int mr = r0 + me % at_once, sub = me / at_once;
+    if (mr >= rows) continue;
+    auto sums = [&](int q) { return reinterpret_cast<const float*>(record(q) + 32 * R) + mr; };
+    float M = -INFINITY, Mt = -INFINITY, ls = 0.f;
+#pragma unroll 4
+    for (int q = 0; q < w.parts; ++q) {
+      M = fmaxf(M, __ldcg(sums(q)));
+      Mt = fmaxf(Mt, __ldcg(sums(q) + 2 * R));
+    }
+    const float Mz = M > -INFINITY ? M : 0.f;
+#pragma unroll 4
+    for (int q = 0; q < w.parts; ++q) ls += __ldcg(sums(q) + R) * fast_exp2((__ldcg(sums(q)) - Mz) * sc);
+    const float iv = ls == 0.f ? 0.f : 1.f / ls;
+    const size_t at = static_cast<size_t>(w.tok0 + mr / G) * a.kv.Hq + w.h * G + mr % G;
+    auto sum = [&](auto width, int c) {  // float4s c .. c + width - 1
+      constexpr int N = decltype(width)::value;
+      float4 o[N];
+#pragma unroll
+      for (int e = 0; e < N; ++e) o[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll (N >= 8 ? 2 : 8 / N)
+      for (int q = 0; q < w.parts; ++q) {
+        const float4* rq = record(q) + c * R + mr;
+        float4 v[N];
+#pragma unroll
+        for (int e = 0; e < N; ++e) v[e] = __ldcg(rq + e * R);
+        const float wq = fast_exp2((__ldcg(sums(q)) - Mz) * sc);
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+          o[e].x = fmaf(v[e].x, wq, o[e].x);
+          o[e].y = fmaf(v[e].y, wq, o[e].y);
+          o[e].z = fmaf(v[e].z, wq, o[e].z);
+          o[e].w = fmaf(v[e].w, wq, o[e].w);
+        }
+      }
+      __nv_bfloat16* dst = a.out + at * kHeadDim + 4 * c;
+#pragma unroll
+      for (int e = 0; e < N; ++e) {
+        uint2 v;
+        v.x = pack_bf16(o[e].x * iv, o[e].y * iv);
+        v.y = pack_bf16(o[e].z * iv, o[e].w * iv);
+        *reinterpret_cast<uint2*>(dst + 4 * e) = v;
+      }
+    };
+    const int each = 32 / per, c_end = (sub + 1) * each;
+    if (each >= 8)
+      for (int c = sub * each; c < c_end; c += 8) sum(std::integral_constant<int, 8>(), c);
+    else
+      for (int c = sub * each; c < c_end; ++c) sum(std::integral_constant<int, 1>(), c);
+    if (sub == 0) {
+      if (a.m) a.m[at] = Mt * sc * kLn2;
+      if (a.l) a.l[at] = Mt > -INFINITY ? ls * fast_exp2((M - Mt) * sc) : ls;
+    }
+  }
 }
 
 __global__ void __launch_bounds__(kThreads, 1)
@@ -373,9 +468,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(smem_u32(&ctl->pready[t][1]), 4);
       mbar_init(smem_u32(&ctl->odone[t]), 1);
       mbar_init(smem_u32(&ctl->ufull[t]), 1);
-      mbar_init(smem_u32(&ctl->uempty[t]), 10);  // eight softmax warps, issue warp, value warp
+      mbar_init(smem_u32(&ctl->uempty[t]), 14);  // softmax and epilogue warps, issue and value warp
+      mbar_init(smem_u32(&ctl->sdone[t]), 4);
     }
-    mbar_init(smem_u32(&ctl->both), 8);          // the eight softmax warps
+    mbar_init(smem_u32(&ctl->ofree), 4);
+    mbar_init(smem_u32(&ctl->meet), 4);
+    mbar_init(smem_u32(&ctl->help), 1);
     for (int s = 0; s < 4; ++s) mbar_init(smem_u32(&ctl->tail[s]), 1);
     ctl->abort = 0;
     fence_mbar_init();
@@ -397,70 +495,76 @@ __global__ void __launch_bounds__(kThreads, 1)
   // ---- the line of work: prefix sums over the requests of an item row's tiles, dense and streaming
   long long* cum_d = reinterpret_cast<long long*>(smem + kOffRing);  // [B]
   long long* cum_s = cum_d + kv.B;
-  long long* s_warp = cum_s + kv.B;  // [2][12]
+  long long* s_warp = cum_s + kv.B;  // [2][kThreads / 32]
+  int2* s_req = reinterpret_cast<int2*>(smem);  // [B]: tokens before the chunk, new tokens
+  const int warps = min((kv.B + 31) / 32, kThreads / 32);  // with requests of their own
   long long carry_d = 0, carry_s = 0;
   for (int b0 = 0; b0 < kv.B; b0 += kThreads) {
-    const int b = b0 + tid;
-    int n = 0, base = 0;
-    if (b < kv.B) {
-      const int L = request_len(kv, b);
-      n = min(max(a.count[b], 0), L);
-      base = L - n;
-    }
-    const int nq = (n + W - 1) / W;
     long long cd = 0, cs = 0;
-    int ns, w0;
-    if (nq <= 4)
-      for (int i = 0; i < nq; ++i) {
-        cd += item_tiles(base, n, i, W, false, 0, 0, &ns, &w0);
-        cs += item_tiles(base, n, i, W, true, a.sink, a.local, &ns, &w0);
+    const int b = b0 + tid;
+    if (warp < warps) {
+      int n = 0, base = 0;
+      if (b < kv.B) {
+        const int L = request_len(kv, b);
+        n = min(max(a.count[b], 0), L);
+        base = L - n;
+        s_req[b] = make_int2(base, n);
       }
-    uint32_t longer = __ballot_sync(0xffffffffu, nq > 4);
-    while (longer) {  // long prompts: the warp shares one request's query tiles
-      const int src = __ffs(longer) - 1;
-      longer &= longer - 1;
-      const int wn = __shfl_sync(0xffffffffu, n, src), wb = __shfl_sync(0xffffffffu, base, src);
-      const int wq = __shfl_sync(0xffffffffu, nq, src);
-      long long d = 0, s = 0;
-      for (int i = lane; i < wq; i += 32) {
-        d += item_tiles(wb, wn, i, W, false, 0, 0, &ns, &w0);
-        s += item_tiles(wb, wn, i, W, true, a.sink, a.local, &ns, &w0);
+      const int nq = n > W ? (n + W - 1) / W : n > 0;
+      int ns, w0;
+      if (nq <= 4)
+        for (int i = 0; i < nq; ++i) {
+          cd += item_tiles(base, n, i, W, false, 0, 0, &ns, &w0) + kItemPad;
+          cs += item_tiles(base, n, i, W, true, a.sink, a.local, &ns, &w0) + kItemPad;
+        }
+      uint32_t longer = __ballot_sync(0xffffffffu, nq > 4);
+      while (longer) {  // long prompts: the warp shares one request's query tiles
+        const int src = __ffs(longer) - 1;
+        longer &= longer - 1;
+        const int wn = __shfl_sync(0xffffffffu, n, src), wb = __shfl_sync(0xffffffffu, base, src);
+        const int wq = __shfl_sync(0xffffffffu, nq, src);
+        long long d = 0, s = 0;
+        for (int i = lane; i < wq; i += 32) {
+          d += item_tiles(wb, wn, i, W, false, 0, 0, &ns, &w0) + kItemPad;
+          s += item_tiles(wb, wn, i, W, true, a.sink, a.local, &ns, &w0) + kItemPad;
+        }
+        d = warp_sum_ll(d);
+        s = warp_sum_ll(s);
+        if (lane == src) {
+          cd = d;
+          cs = s;
+        }
       }
-      d = warp_sum_ll(d);
-      s = warp_sum_ll(s);
-      if (lane == src) {
-        cd = d;
-        cs = s;
+      cd = warp_scan_ll(cd, lane);
+      cs = warp_scan_ll(cs, lane);
+      if (lane == 31) {
+        s_warp[warp] = cd;
+        s_warp[kThreads / 32 + warp] = cs;
       }
-    }
-    cd = warp_scan_ll(cd, lane);
-    cs = warp_scan_ll(cs, lane);
-    if (lane == 31) {
-      s_warp[warp] = cd;
-      s_warp[12 + warp] = cs;
     }
     __syncthreads();
     long long bd = carry_d, bs = carry_s;
-    for (int w = 0; w < kThreads / 32; ++w) {
+    for (int w = 0; w < warps; ++w) {
       if (w < warp) {
         bd += s_warp[w];
-        bs += s_warp[12 + w];
+        bs += s_warp[kThreads / 32 + w];
       }
       carry_d += s_warp[w];
-      carry_s += s_warp[12 + w];
+      carry_s += s_warp[kThreads / 32 + w];
     }
     if (b < kv.B) {
       cum_d[b] = bd + cd;
       cum_s[b] = bs + cs;
     }
-    __syncthreads();
+    if (b0 + kThreads < kv.B) __syncthreads();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = ctl->tmem;
+  float* scratch = a.maxima + 256 * blockIdx.x;  // true maxima of a finished unit, [2][128]
 
-  if (warp >= 8) {
+  if (warp >= kLoadWarp) {
   regs_dec<kOtherRegs>();
   const int lseg = 31 - __clz(seg), nseg = 128 >> lseg, my_seg = lane & (nseg - 1), my_half = lane / nseg;
   const bool loads = my_half < 2;  // a lane loads one half (of the dims) of one piece of a tile
@@ -504,17 +608,21 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == kLoadWarp) {
     // =============================================================================== load warp
 
-    int hd = 0;  // dense heads
-    for (int h0 = 0; h0 < kv.Hkv; h0 += 32) {
-      const int h = h0 + lane;
-      hd += __popc(__ballot_sync(0xffffffffu, h < kv.Hkv && (kv.streaming == nullptr || kv.streaming[h] == 0)));
+    uint32_t there;
+    const uint32_t win_heads = window_heads(kv, 0, lane, &there);
+    int hd = __popc(there & ~win_heads);  // dense heads
+    for (int h0 = 32; h0 < kv.Hkv; h0 += 32) {
+      uint32_t t;
+      const uint32_t w = window_heads(kv, h0, lane, &t);
+      hd += __popc(t & ~w);
     }
     const long long dense_work = hd * carry_d, work = dense_work + (kv.Hkv - hd) * carry_s;
-    const long long ctas = min(static_cast<long long>(gridDim.x), work);
+    const long long ctas = min(static_cast<long long>(gridDim.x), quotient(work + kMinWork - 1, kMinWork));
     const long long c = blockIdx.x;
-    long long x = c < ctas ? c * work / ctas : work, x1 = c < ctas ? (c + 1) * work / ctas : work;
-    // where x lies: head, request, query tile, key tile
-    bool win = x >= dense_work;
+    long long x = c < ctas ? quotient(c * work, ctas) : work,
+              x1 = c < ctas ? quotient((c + 1) * work, ctas) : work;
+    // a place on the line: head, request, query tile, key tile
+    bool win = false;
     int d = 0, h = 0, b = 0, i = 0, k = 0, n = 0, base = 0, len = 0, nq = 0;
     auto load_request = [&]() {
       len = request_len(kv, b);
@@ -522,11 +630,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       base = len - n;
       nq = (n + W - 1) / W;
     };
-    if (x < x1) {
-      const long long per = win ? carry_s : carry_d, y = win ? x - dense_work : x;
-      d = static_cast<int>(y / per);
+    auto locate = [&](long long at) {
+      win = at >= dense_work;
+      const long long per = win ? carry_s : carry_d, y = win ? at - dense_work : at;
+      d = static_cast<int>(quotient(y, per));
       long long r = y - d * per;
-      h = nth_head(kv, win, d, lane);
+      h = nth_head(kv, win, d, lane, win_heads, there);
       const long long* cum = win ? cum_s : cum_d;
       int lo = 0, hi = kv.B - 1;
       while (lo < hi) {
@@ -538,11 +647,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       b = lo;
       if (b > 0) r -= cum[b - 1];
-      load_request();
+      base = s_req[b].x;
+      n = s_req[b].y;
+      len = base + n;
+      nq = (n + W - 1) / W;
       for (int i0 = 0; i0 < nq; i0 += 32) {
         int ns, w0;
         const long long cost =
-            i0 + lane < nq ? item_tiles(base, n, i0 + lane, W, win, a.sink, a.local, &ns, &w0) : 0;
+            i0 + lane < nq ? item_tiles(base, n, i0 + lane, W, win, a.sink, a.local, &ns, &w0) + kItemPad
+                           : 0;
         const long long end = warp_scan_ll(cost, lane);
         const uint32_t above = __ballot_sync(0xffffffffu, end > r);
         if (above) {
@@ -553,18 +666,41 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         r -= __shfl_sync(0xffffffffu, end, 31);
       }
+    };
+    // An item cut at the range's end is done first, one cut at its start next, the whole ones then: the
+    // parts of cut items are all there early, and their merges run beside the rest.
+    const long long x_first = x;
+    bool cut_first = false;
+    int fd = 0, fh = 0, fb = 0, fi = 0, fk = 0;
+    bool fwin = false;
+    if (x < x1) {
+      locate(x);
+      fwin = win, fd = d, fh = h, fb = b, fi = i, fk = k;
+      locate(x1 - 1);
+      int ns, w0;
+      const int cnt = item_tiles(base, n, i, W, win, a.sink, a.local, &ns, &w0);
+      const long long item0 = x1 - 1 - k;
+      cut_first = item0 > x && x1 < item0 + cnt;
+      if (cut_first) {
+        k = 0;
+        x = item0;
+      } else {
+        win = fwin, d = fd, h = fh, b = fb, i = fi, k = fk;
+        load_request();
+      }
     }
+    const long long x_cut = cut_first ? x : x1;  // what begins here is done first
     __syncwarp();
     fence_proxy_async_smem();  // the prefix sums are read; the ring takes their place
 
-    const long long x_begin = x;
     uint32_t tiles = 0;      // key tiles before this unit
     Place pk = {0, 1};       // of the next K tile (a fresh barrier passes a wait for phase 1)
     int u = 0;
     bool ok = true;
-    for (; x < x1 && ok; ++u) {
+    while (x < x1 && ok) {
       Unit un;
       const int cnt = item_tiles(base, n, i, W, win, a.sink, a.local, &un.ns, &un.w0);
+      if (k < cnt) {
       un.valid = 1;
       un.b = b;
       un.h = h;
@@ -578,9 +714,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       un.split = un.ntok <= TQ;
       un.whole = un.kb == 0 && un.ke == cnt;
       const long long item0 = x - k, item1 = item0 + cnt;
-      un.cta0 = static_cast<int>(((item0 + 1) * ctas - 1) / work);
-      un.cta1 = static_cast<int>((item1 * ctas - 1) / work);
-      un.slot = 2 * blockIdx.x + (x == x_begin && k > 0 ? 0 : 1);
+      un.cta0 = un.cta1 = blockIdx.x;
+      if (!un.whole) {
+        un.cta0 = static_cast<int>(quotient((item0 + 1) * ctas - 1, work));
+        un.cta1 = static_cast<int>(quotient(item1 * ctas - 1, work));
+      }
+      un.slot = 2 * blockIdx.x + (k > 0 ? 0 : 1);
       const int nk = un.ke - un.kb;
       // stream 0 of a pair ends at its own last token's tile
       un.n0 = nk;
@@ -629,9 +768,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         page = page_next;
         page_next = page_after;
       }
+      if (!ok) break;
       tiles += nk;
+      ++u;
+      }  // (a range may begin in the pad behind an item's tiles)
+      if (cut_first) {  // back to the range's start
+        cut_first = false;
+        x = x_first;
+        x1 = x_cut;
+        win = fwin, d = fd, h = fh, b = fb, i = fi, k = fk;
+        load_request();
+        continue;
+      }
       // the next unit starts at the next item
-      x += nk;
+      x += cnt + kItemPad - k;
       k = 0;
       if (x < x1) {
         if (++i >= nq) {
@@ -644,7 +794,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 win = true;
                 d = 0;
               }
-              h = nth_head(kv, win, d, lane);
+              h = nth_head(kv, win, d, lane, win_heads, there);
             }
             load_request();
           } while (n == 0);
@@ -720,6 +870,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int kk = 0; kk < nk; ++kk) {
             const bool more = kk + 1 < nk;
             if (!(ok = wait(&ctl->full[pv.st], pv.ph))) break;
+            if (kk == 0 && u > 0 && !(ok = wait(&ctl->ofree, (u - 1) & 1))) break;
             if (kk < n0 && !(ok = product(0, pv.st, kk > 0))) break;
             if (more) {
               if (!(ok = wait(&ctl->full[pk.st], pk.ph))) break;
@@ -751,6 +902,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int t = 0; t < 2; ++t) {
               if (kk + t >= nk) break;
               if (!(ok = wait(&ctl->full[pv.st], pv.ph))) break;
+              if (kk + t == 0 && u > 0 && !(ok = wait(&ctl->ofree, (u - 1) & 1))) break;
               if (!(ok = product(t, pv.st, kk > 0))) break;
               tc_commit(smem_u32(&ctl->empty[pv.st]));
               pv.next2();
@@ -834,21 +986,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) mbar_arrive(smem_u32(&ctl->full[st]));
     }
   }
-  } else {
+  } else if (warp < kOutWarp) {
     regs_inc<kSoftmaxRegs>();
     // ================================================================================= softmax
     const int t = warp >> 2, row = tid & 127;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + lanes + kS0 + 128 * t, tO = tmem + lanes + kO0;
     const float sc = a.scale_log2;
-    const int r_tok = row / G, r_head = row - r_tok * G;
-    uint32_t scnt = 0, ocnt = 0, xcnt = 0, tiles = 0;
+    const int r_tok = row / G;
+    uint32_t scnt = 0, ocnt = 0, tiles = 0;
     bool ok = true;
-    auto meet = [&]() {  // both warpgroups (bounded, unlike a named barrier)
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&ctl->both));
-      return warp_wait(smem_u32(&ctl->both), (xcnt++) & 1, abort, kv.status);
-    };
     for (int u = 0; ok; ++u) {
       const int us = u & 1;
       if (!warp_wait(smem_u32(&ctl->ufull[us]), (u >> 1) & 1, abort, kv.status)) break;
@@ -958,174 +1105,178 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (!ok) break;
-      // ---- the unit's end: this stream's last product
-      if (nt > 0 && !(ok = warp_wait(smem_u32(&ctl->odone[t]), (ocnt + nt - 1) & 1, abort, kv.status)))
-        break;
-      tc_fence_after();
       ocnt += nt;
       tiles += nk;
-      float w0 = 1.f, w1 = 0.f;  // weights of O_0 and O_1 (split), or of O_t (pair)
-      bool has0 = nt > 0, has1 = false;
-      if (un.split) {
-        ctl->xm[t][row] = mref;
-        ctl->xl[t][row] = l;
-        if (t == 1) ctl->xtrue[row] = mtrue;
-        if (!(ok = meet())) break;
-        has0 = true;
-        has1 = nk > 1;
-        const float ma = ctl->xm[0][row], mb = ctl->xm[1][row];
-        const float m = fmaxf(ma, mb);
-        const float mz = m > -INFINITY ? m : 0.f;
-        w0 = fast_exp2((ma - mz) * sc);
-        w1 = has1 ? fast_exp2((mb - mz) * sc) : 0.f;
-        l = ctl->xl[0][row] * w0 + ctl->xl[1][row] * w1;
-        mtrue = fmaxf(mtrue, t == 0 ? ctl->xtrue[row] : mtrue);  // (used by stream 0 alone)
-        mref = m;
+      // the unit's sums go to the epilogue, once it has taken the unit before it out
+      if (u > 0 && !(ok = warp_wait(smem_u32(&ctl->ofree), (u - 1) & 1, abort, kv.status))) break;
+      ctl->xm[t][row] = mref;
+      ctl->xl[t][row] = l;
+      __stcg(scratch + 128 * t + row, mtrue);
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(smem_u32(&ctl->sdone[t]));
+        mbar_arrive(smem_u32(&ctl->uempty[us]));
       }
-      const size_t R = a.rec_rows;
-      float* rec = a.records + static_cast<size_t>(un.slot) * R * kRecordFloats;
-      const int rr = my_tok * G + r_head;  // the unit's row
-      const float inv = l == 0.f ? 0.f : 1.f / l;
-      __nv_bfloat16* dst =
-          a.out + (static_cast<size_t>(un.tok0 + my_tok) * kv.Hq + un.h * G + r_head) * kHeadDim;
-      if (any) {
-        const int c_beg = un.split ? 64 * t : 0, c_end = un.split ? 64 * t + 64 : 128;
-#pragma unroll 1
-        for (int c0 = c_beg; c0 < c_end; c0 += 32) {
-          float o[32];
-          if (!un.split) {
-            uint32_t r[32];
-            if (has0) tmem_ld_32(tO + 128 * t + c0, r);
+    }
+  } else {
+    regs_dec<kOutRegs>();
+    // ================================================================================= epilogue
+    const int row = tid & 127;
+    const uint32_t tO = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + kO0;
+    const float sc = a.scale_log2;
+    const int r_tok = row / G, r_head = row - r_tok * G;
+    const size_t R = a.rec_rows;
+    uint32_t ocnt0 = 0, ocnt1 = 0, mcnt = 0;
+    int merges = 0;
+    bool ok = true;
+    auto meet = [&]() {  // the warpgroup (bounded, unlike a named barrier)
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&ctl->meet));
+      return warp_wait(smem_u32(&ctl->meet), (mcnt++) & 1, abort, kv.status);
+    };
+    for (int u = 0; ok; ++u) {
+      const int us = u & 1;
+      if (!warp_wait(smem_u32(&ctl->ufull[us]), (u >> 1) & 1, abort, kv.status)) break;
+      const volatile Unit& un = ctl->unit[us];
+      if (!un.valid) break;
+      const int ntok = un.ntok, whole = un.whole, nk = un.ke - un.kb;
+      // this lane's first row in the output (head 0 of its token in the unit) and in the record
+      auto out_row = [&](int my_tok) {
+        return static_cast<size_t>(un.tok0 + my_tok) * kv.Hq + un.h * G + r_head;
+      };
+      auto rec_row = [&](int my_tok) {
+        return a.records + static_cast<size_t>(un.slot) * R * kRecordFloats + 4 * (my_tok * G + r_head);
+      };
+
+      // 32 columns of this row to the output or the record
+      auto put = [&](int my_tok, float inv, int c0, const float (&o)[32]) {
+        if (whole) {
+          __nv_bfloat16* dst = a.out + out_row(my_tok) * kHeadDim + c0;
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = has0 ? __uint_as_float(r[e]) : 0.f;
-          } else {
-            uint32_t r[32], v[32];
-            tmem_ld_32(tO + c0, r);
-            if (has1) tmem_ld_32(tO + 128 + c0, v);
+          for (int e = 0; e < 32; e += 16) {  // whole 32-byte sectors
+            uint32_t v[8];
 #pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              o[e] = __uint_as_float(r[e]) * w0;
-              if (has1) o[e] = fmaf(__uint_as_float(v[e]), w1, o[e]);
-            }
+            for (int x = 0; x < 8; ++x) v[x] = pack_bf16(o[e + 2 * x] * inv, o[e + 2 * x + 1] * inv);
+            store32(dst + e, v);
           }
-          if (live) {
-            if (un.whole) {
-#pragma unroll
-              for (int e = 0; e < 32; e += 16) {  // whole 32-byte sectors
-                uint32_t v[8];
-#pragma unroll
-                for (int x = 0; x < 8; ++x)
-                  v[x] = pack_bf16(o[e + 2 * x] * inv, o[e + 2 * x + 1] * inv);
-                store32(dst + c0 + e, v);
-              }
-            } else {
-#pragma unroll
-              for (int e = 0; e < 32; e += 4)
-                reinterpret_cast<float4*>(rec)[static_cast<size_t>((c0 + e) / 4) * R + rr] =
-                    make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
-            }
-          }
-        }
-      }
-      if (live && !(un.split && t == 1)) {
-        const float lt = mtrue > -INFINITY ? l * fast_exp2((mref - mtrue) * sc) : l;
-        if (un.whole) {
-          const size_t at = static_cast<size_t>(un.tok0 + my_tok) * kv.Hq + un.h * G + r_head;
-          if (a.m) a.m[at] = mtrue * sc * kLn2;
-          if (a.l) a.l[at] = lt;
         } else {
-          float* ml = rec + 128 * R;
-          ml[rr] = mref;
-          ml[R + rr] = l;
-          ml[2 * R + rr] = mtrue;
+          float* dst = rec_row(my_tok) + c0 * R;
+#pragma unroll
+          for (int e = 0; e < 32; e += 4)
+            *reinterpret_cast<float4*>(dst + e * R) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
         }
-      }
-      if (un.split) {  // both accumulators are read before either stream's next product
+      };
+      // its sums (reference m, sum l relative to it, true maximum)
+      auto put_sums = [&](int my_tok, float m, float l, float mtrue) {
+        if (whole) {
+          const size_t at = out_row(my_tok);
+          if (a.m) a.m[at] = mtrue * sc * kLn2;
+          if (a.l) a.l[at] = mtrue > -INFINITY ? l * fast_exp2((m - mtrue) * sc) : l;
+        } else {
+          float* ml = rec_row(0) - 4 * r_head + 128 * R + my_tok * G + r_head;
+          ml[0] = m;
+          ml[R] = l;
+          ml[2 * R] = mtrue;
+        }
+      };
+      auto take = [&](int t, int nt) {  // stream t's sums, and its last product
+        if (!warp_wait(smem_u32(&ctl->sdone[t]), u & 1, abort, kv.status)) return false;
+        uint32_t& done = t ? ocnt1 : ocnt0;
+        if (nt > 0 && !warp_wait(smem_u32(&ctl->odone[t]), (done + nt - 1) & 1, abort, kv.status))
+          return false;
+        done += nt;
+        tc_fence_after();
+        return true;
+      };
+      auto release = [&]() {  // accumulators and sums are read
         tc_fence_before();
-        if (!(ok = meet())) break;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&ctl->ofree));
+      };
+
+      if (!un.split) {
+#pragma unroll 1
+        for (int t = 0; t < 2; ++t) {
+          const int nt = t == 0 ? un.n0 : nk;
+          if (!(ok = take(t, nt))) break;
+          const int my_tok = t * TQ + r_tok;
+          const bool live = r_tok < TQ && my_tok < ntok;
+          const float m = ctl->xm[t][row], l = ctl->xl[t][row], mtrue = __ldcg(scratch + 128 * t + row);
+          const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll 1
+          for (int c0 = 0; c0 < 128; c0 += 32) {
+            uint32_t r[32];
+            if (nt > 0) tmem_ld_32(tO + 128 * t + c0, r);
+            if (t == 1 && c0 == 96) release();
+            float o[32];
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = nt > 0 ? __uint_as_float(r[e]) : 0.f;
+            if (live) put(my_tok, inv, c0, o);
+          }
+          if (live) put_sums(my_tok, m, l, mtrue);
+        }
+      } else {
+        // the streams saw alternate key tiles of the same rows: joined here
+        if (!(ok = take(0, (nk + 1) / 2) && take(1, nk / 2))) break;
+        const bool live = r_tok < TQ && r_tok < ntok, any = __any_sync(0xffffffffu, live);
+        const bool two = nk > 1;
+        const float ma = ctl->xm[0][row], mb = ctl->xm[1][row];
+        const float m = fmaxf(ma, mb), mz = m > -INFINITY ? m : 0.f;
+        const float w0 = fast_exp2((ma - mz) * sc), w1 = two ? fast_exp2((mb - mz) * sc) : 0.f;
+        const float l = ctl->xl[0][row] * w0 + ctl->xl[1][row] * w1;
+        const float mtrue = fmaxf(__ldcg(scratch + row), __ldcg(scratch + 128 + row));
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll 1
+        for (int c0 = 0; c0 < 128; c0 += 32) {
+          float o[32];
+          if (any) {
+            uint32_t r[32];
+            tmem_ld_32(tO + c0, r);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = __uint_as_float(r[e]) * w0;
+            if (two) {
+              tmem_ld_32(tO + 128 + c0, r);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = fmaf(__uint_as_float(r[e]), w1, o[e]);
+            }
+          }
+          if (c0 == 96) release();
+          if (live) put(r_tok, inv, c0, o);
+        }
+        if (live) put_sums(r_tok, m, l, mtrue);
       }
-      if (!un.whole) {
+      if (!ok) break;
+      if (!whole) {
+        // ---- a cut item: who takes its last ticket merges its records
         __threadfence();
         if (!(ok = meet())) break;
-        const int parts = un.cta1 - un.cta0 + 1;
-        if (tid == 0) {
+        if (row == 0) {
+          const int cta0 = un.cta0, parts = un.cta1 - cta0 + 1;
           __threadfence();
-          const int last = atomicAdd(a.tickets + un.cta0, 1) == parts - 1;
-          if (last) a.tickets[un.cta0] = 0;
-          __threadfence();
+          const int last = atomicAdd(a.tickets + cta0, 1) == parts - 1;
+          if (last) {
+            a.tickets[cta0] = 0;
+            __threadfence();
+            ctl->merge[merges] = {un.tok0, ntok, un.h, cta0, parts};
+          }
           ctl->last = last;
         }
         if (!(ok = meet())) break;
-        if (*const_cast<volatile int*>(&ctl->last)) {
-          // merge in CTA order: `per` threads a row, each with every per-th float4 of it
-          const int rows = un.ntok * G;
-          int per = 1;
-          while (per < 32 && 2 * per * rows <= 256) per *= 2;
-          for (int r0 = 0; r0 < rows; r0 += 256 / per) {
-            const int mr = r0 + tid % (256 / per), sub = tid / (256 / per);
-            if (mr >= rows) continue;
-            auto record = [&](int q) {
-              return a.records + static_cast<size_t>(2 * (un.cta0 + q) + (q == 0)) * R * kRecordFloats;
-            };
-            float M = -INFINITY, Mt = -INFINITY, ls = 0.f;
-#pragma unroll 4
-            for (int q = 0; q < parts; ++q) {
-              M = fmaxf(M, __ldcg(record(q) + 128 * R + mr));
-              Mt = fmaxf(Mt, __ldcg(record(q) + 130 * R + mr));
-            }
-            const float Mz = M > -INFINITY ? M : 0.f;
-#pragma unroll 4
-            for (int q = 0; q < parts; ++q)
-              ls += __ldcg(record(q) + 129 * R + mr) *
-                    fast_exp2((__ldcg(record(q) + 128 * R + mr) - Mz) * sc);
-            const float iv = ls == 0.f ? 0.f : 1.f / ls;
-            const size_t at = static_cast<size_t>(un.tok0 + mr / G) * kv.Hq + un.h * G + mr % G;
-            auto sum = [&](auto width, int c_first) {  // `width` float4s, per apart
-              constexpr int N = decltype(width)::value;
-              float4 o[N];
-#pragma unroll
-              for (int e = 0; e < N; ++e) o[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll (N >= 8 ? 1 : 8 / N)
-              for (int q = 0; q < parts; ++q) {
-                const float* rq = record(q);
-                float4 v[N];
-#pragma unroll
-                for (int e = 0; e < N; ++e)
-                  v[e] = __ldcg(reinterpret_cast<const float4*>(rq) +
-                                static_cast<size_t>(c_first + e * per) * R + mr);
-                const float wq = fast_exp2((__ldcg(rq + 128 * R + mr) - Mz) * sc);
-#pragma unroll
-                for (int e = 0; e < N; ++e) {
-                  o[e].x = fmaf(v[e].x, wq, o[e].x);
-                  o[e].y = fmaf(v[e].y, wq, o[e].y);
-                  o[e].z = fmaf(v[e].z, wq, o[e].z);
-                  o[e].w = fmaf(v[e].w, wq, o[e].w);
-                }
-              }
-#pragma unroll
-              for (int e = 0; e < N; ++e) {
-                uint2 v;
-                v.x = pack_bf16(o[e].x * iv, o[e].y * iv);
-                v.y = pack_bf16(o[e].z * iv, o[e].w * iv);
-                *reinterpret_cast<uint2*>(a.out + at * kHeadDim + 4 * (c_first + e * per)) = v;
-              }
-            };
-            if (per <= 2)
-              for (int c = sub; c < 32; c += 16 * per) sum(std::integral_constant<int, 16>(), c);
-            else if (per <= 8)
-              for (int c = sub; c < 32; c += 4 * per) sum(std::integral_constant<int, 4>(), c);
-            else
-              for (int c = sub; c < 32; c += per) sum(std::integral_constant<int, 1>(), c);
-            if (sub == 0) {
-              if (a.m) a.m[at] = Mt * sc * kLn2;
-              if (a.l) a.l[at] = Mt > -INFINITY ? ls * fast_exp2((M - Mt) * sc) : ls;
-            }
-          }
-        }
+        merges += *const_cast<volatile int*>(&ctl->last);
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&ctl->uempty[us]));
     }
+    if (ok && row == 0) {
+      ctl->merges = merges;
+      mbar_arrive(smem_u32(&ctl->help));
+    }
+    __syncwarp();
+  }
+  // ---- the merges, by softmax and epilogue warps
+  if (warp < kLoadWarp && warp_wait(smem_u32(&ctl->help), 0, abort, kv.status)) {
+    const int merges = *const_cast<volatile int*>(&ctl->merges);
+    for (int x = 0; x < merges; ++x) merge_records(a, ctl->merge[x], tid, kLoadWarp * 32);
   }
   __syncthreads();
   if (warp == kMmaWarp)
@@ -1142,13 +1293,14 @@ int chunk_attn_grid() {
   return sms < kChunkMaxGrid ? sms : kChunkMaxGrid;
 }
 
-// Tickets of the grid, then two partial records per CTA: [32][rows] float4 of O, then mref, l and mtrue
-// of the rows.
+// Tickets of the grid, 256 maxima per CTA, then two partial records per CTA: [32][rows] float4 of O,
+// then mref, l and mtrue of the rows.
 ChunkAttnWorkspace chunk_attn_workspace(int G, int tokens) {
   ChunkAttnWorkspace w;
   const long long rows = static_cast<long long>(tokens) * G;
   w.rows = static_cast<int>(rows < 256 ? (rows + 3) / 4 * 4 : 256);
-  w.records_off = kChunkMaxGrid * sizeof(int32_t);
+  w.maxima_off = kChunkMaxGrid * sizeof(int32_t);
+  w.records_off = w.maxima_off + static_cast<size_t>(chunk_attn_grid()) * 256 * sizeof(float);
   w.total = w.records_off +
             static_cast<size_t>(chunk_attn_grid()) * 2 * w.rows * kRecordFloats * sizeof(float);
   return w;
