@@ -1152,6 +1152,14 @@ int dsa_chunk_attn(const dsa_paged_kv* kv, const dsa_chunk* chunk, const void* q
                 v.max_pages, v.p);
   if (v.B > kChunkMaxBatch)
     return fail(DSA_ERR_UNSUPPORTED, "batch %d > %d", v.B, kChunkMaxBatch);
+  if (v.Hkv > kChunkMaxHeads)
+    return fail(DSA_ERR_UNSUPPORTED, "%d KV heads > %d", v.Hkv, kChunkMaxHeads);
+  // key tiles of all (KV head, query tile) items, were every query at the table's end
+  const long long q_tiles = chunk->tokens / (2 * (128 / v.G)) + v.B;
+  const long long k_tiles = static_cast<long long>(v.p) * v.max_pages / 128 + 4;
+  if (q_tiles * k_tiles >= (1LL << 31) / v.Hkv)
+    return fail(DSA_ERR_UNSUPPORTED, "%d tokens over up to %lld positions: more than 2^31 key tiles",
+                chunk->tokens, static_cast<long long>(v.p) * v.max_pages);
   const ChunkAttnWorkspace w = chunk_attn_workspace(v.G, chunk->tokens);
   if (!workspace || workspace_bytes < w.total)
     return fail(DSA_ERR_WORKSPACE, "dsa_chunk_attn: workspace too small");

@@ -94,7 +94,7 @@ struct Ctl {
 };
 constexpr uint32_t kSmemBytes = kOffCtl + sizeof(Ctl);
 static_assert(kSmemBytes <= 227 * 1024, "shared memory of one CTA");
-static_assert(kChunkMaxBatch * 16 + 512 <= kRing * kTileBytes, "the prefix sums overlay the ring");
+static_assert(kChunkMaxBatch * 8 + 512 <= kRing * kTileBytes, "the prefix sums overlay the ring");
 static_assert(kChunkMaxBatch * 8 <= 2 * kTileBytes, "the requests overlay the query tiles");
 
 // 32 columns of this thread's TMEM lane.
@@ -244,16 +244,10 @@ DSA_DEV int item_tiles(int base, int n, int i, int W, bool win, int sink, int lo
   return s + cnt;
 }
 
-DSA_DEV long long warp_sum_ll(long long v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
-}
-
-DSA_DEV long long warp_scan_ll(long long v, int lane) {
+DSA_DEV uint32_t warp_scan(uint32_t v, int lane) {
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const long long u = __shfl_up_sync(0xffffffffu, v, o);
+    const uint32_t u = __shfl_up_sync(0xffffffffu, v, o);
     if (lane >= o) v += u;
   }
   return v;
@@ -355,17 +349,13 @@ DSA_DEV int nth_head(const KvView& kv, bool win, int d, int lane, uint32_t first
     if (h0 > 0) first = window_heads(kv, h0, lane, &there);
     const uint32_t m = win ? first : there & ~first;
     const int c = __popc(m);
-    if (d < c) return h0 + static_cast<int>(__fns(m, 0, d + 1));
+    if (d < c) {  // the lane whose bit has d set bits below it
+      const bool it = (m >> lane & 1) != 0 && __popc(m & ((1u << lane) - 1u)) == d;
+      return h0 + __ffs(__ballot_sync(0xffffffffu, it)) - 1;
+    }
     d -= c;
   }
   return -1;
-}
-
-// a / b for a >= 0, b > 0: places on the line nearly always fit 32 bits, where a division takes a
-// tenth of the time.
-DSA_DEV long long quotient(long long a, long long b) {
-  if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
-  return a / b;
 }
 
 // Sets *abort when a wait has given up; true for the whole warp only when it succeeded in every lane.
@@ -493,14 +483,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   grid_dependency_wait();
 
   // ---- the line of work: prefix sums over the requests of an item row's tiles, dense and streaming
-  long long* cum_d = reinterpret_cast<long long*>(smem + kOffRing);  // [B]
-  long long* cum_s = cum_d + kv.B;
-  long long* s_warp = cum_s + kv.B;  // [2][kThreads / 32]
+  // (the host bounds the line by 2^31)
+  uint32_t* cum_d = reinterpret_cast<uint32_t*>(smem + kOffRing);  // [B]
+  uint32_t* cum_s = cum_d + kv.B;
+  uint32_t* s_warp = cum_s + kv.B;  // [2][kThreads / 32]
   int2* s_req = reinterpret_cast<int2*>(smem);  // [B]: tokens before the chunk, new tokens
   const int warps = min((kv.B + 31) / 32, kThreads / 32);  // with requests of their own
-  long long carry_d = 0, carry_s = 0;
+  uint32_t total_d = 0, total_s = 0;
   for (int b0 = 0; b0 < kv.B; b0 += kThreads) {
-    long long cd = 0, cs = 0;
+    uint32_t cd = 0, cs = 0;
     const int b = b0 + tid;
     if (warp < warps) {
       int n = 0, base = 0;
@@ -511,46 +502,45 @@ __global__ void __launch_bounds__(kThreads, 1)
         s_req[b] = make_int2(base, n);
       }
       const int nq = n > W ? (n + W - 1) / W : n > 0;
+      uint32_t several = __ballot_sync(0xffffffffu, nq > 1);
       int ns, w0;
-      if (nq <= 4)
-        for (int i = 0; i < nq; ++i) {
-          cd += item_tiles(base, n, i, W, false, 0, 0, &ns, &w0) + kItemPad;
-          cs += item_tiles(base, n, i, W, true, a.sink, a.local, &ns, &w0) + kItemPad;
-        }
-      uint32_t longer = __ballot_sync(0xffffffffu, nq > 4);
-      while (longer) {  // long prompts: the warp shares one request's query tiles
-        const int src = __ffs(longer) - 1;
-        longer &= longer - 1;
+      if (nq == 1) {
+        cd = item_tiles(base, n, 0, W, false, 0, 0, &ns, &w0) + kItemPad;
+        cs = item_tiles(base, n, 0, W, true, a.sink, a.local, &ns, &w0) + kItemPad;
+      }
+      while (several) {  // the warp shares a request's query tiles
+        const int src = __ffs(several) - 1;
+        several &= several - 1;
         const int wn = __shfl_sync(0xffffffffu, n, src), wb = __shfl_sync(0xffffffffu, base, src);
         const int wq = __shfl_sync(0xffffffffu, nq, src);
-        long long d = 0, s = 0;
+        uint32_t d = 0, s = 0;
         for (int i = lane; i < wq; i += 32) {
           d += item_tiles(wb, wn, i, W, false, 0, 0, &ns, &w0) + kItemPad;
           s += item_tiles(wb, wn, i, W, true, a.sink, a.local, &ns, &w0) + kItemPad;
         }
-        d = warp_sum_ll(d);
-        s = warp_sum_ll(s);
+        d = __reduce_add_sync(0xffffffffu, d);
+        s = __reduce_add_sync(0xffffffffu, s);
         if (lane == src) {
           cd = d;
           cs = s;
         }
       }
-      cd = warp_scan_ll(cd, lane);
-      cs = warp_scan_ll(cs, lane);
+      cd = warp_scan(cd, lane);
+      cs = warp_scan(cs, lane);
       if (lane == 31) {
         s_warp[warp] = cd;
         s_warp[kThreads / 32 + warp] = cs;
       }
     }
     __syncthreads();
-    long long bd = carry_d, bs = carry_s;
+    uint32_t bd = total_d, bs = total_s;
     for (int w = 0; w < warps; ++w) {
       if (w < warp) {
         bd += s_warp[w];
         bs += s_warp[kThreads / 32 + w];
       }
-      carry_d += s_warp[w];
-      carry_s += s_warp[kThreads / 32 + w];
+      total_d += s_warp[w];
+      total_s += s_warp[kThreads / 32 + w];
     }
     if (b < kv.B) {
       cum_d[b] = bd + cd;
@@ -616,27 +606,35 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t w = window_heads(kv, h0, lane, &t);
       hd += __popc(t & ~w);
     }
-    const long long dense_work = hd * carry_d, work = dense_work + (kv.Hkv - hd) * carry_s;
-    const long long ctas = min(static_cast<long long>(gridDim.x), quotient(work + kMinWork - 1, kMinWork));
-    const long long c = blockIdx.x;
-    long long x = c < ctas ? quotient(c * work, ctas) : work,
-              x1 = c < ctas ? quotient((c + 1) * work, ctas) : work;
-    // a place on the line: head, request, query tile, key tile
-    bool win = false;
-    int d = 0, h = 0, b = 0, i = 0, k = 0, n = 0, base = 0, len = 0, nq = 0;
-    auto load_request = [&]() {
-      len = request_len(kv, b);
-      n = min(max(a.count[b], 0), len);
-      base = len - n;
-      nq = (n + W - 1) / W;
+    const uint32_t dense_work = hd * total_d, work = dense_work + (kv.Hkv - hd) * total_s;
+    // equal ranges: CTA c has each + (c < more) places from c each + min(c, more) on
+    const uint32_t ctas = min(gridDim.x, (work + kMinWork - 1) / kMinWork);
+    const uint32_t each = ctas ? work / ctas : 0, more = work - each * ctas, c = blockIdx.x;
+    const uint32_t wide_end = more * (each + 1);
+    auto owner = [&](uint32_t at) {
+      return static_cast<int>(at < wide_end ? at / (each + 1) : more + (at - wide_end) / each);
     };
-    auto locate = [&](long long at) {
-      win = at >= dense_work;
-      const long long per = win ? carry_s : carry_d, y = win ? at - dense_work : at;
-      d = static_cast<int>(quotient(y, per));
-      long long r = y - d * per;
-      h = nth_head(kv, win, d, lane, win_heads, there);
-      const long long* cum = win ? cum_s : cum_d;
+    uint32_t x = c * each + min(c, more), x1 = x + each + (c < more);
+    if (c >= ctas) x1 = x = work;
+    // a place on the line: head, request, query tile, key tile
+    struct At {
+      int win, d, h, b, i, k, base, n;
+    };
+    At at = {}, begin = {};
+    // An item cut at the range's end is done first, one cut at its start next, the whole ones then: the
+    // parts of cut items are all there early.
+    bool cut_first = false;
+    uint32_t x_cut = x1;  // where the item done first begins
+#pragma unroll 1
+    for (int pass = 0; pass < 2 && x < x1; ++pass) {  // the range's last place, then its first
+      const uint32_t place = pass == 0 ? x1 - 1 : x;
+      At p;
+      p.win = place >= dense_work;
+      const uint32_t per = p.win ? total_s : total_d, y = p.win ? place - dense_work : place;
+      p.d = y / per;
+      uint32_t r = y - p.d * per;
+      p.h = nth_head(kv, p.win, p.d, lane, win_heads, there);
+      const uint32_t* cum = p.win ? cum_s : cum_d;
       int lo = 0, hi = kv.B - 1;
       while (lo < hi) {
         const int mid = (lo + hi) >> 1;
@@ -645,51 +643,41 @@ __global__ void __launch_bounds__(kThreads, 1)
         else
           lo = mid + 1;
       }
-      b = lo;
-      if (b > 0) r -= cum[b - 1];
-      base = s_req[b].x;
-      n = s_req[b].y;
-      len = base + n;
-      nq = (n + W - 1) / W;
-      for (int i0 = 0; i0 < nq; i0 += 32) {
-        int ns, w0;
-        const long long cost =
-            i0 + lane < nq ? item_tiles(base, n, i0 + lane, W, win, a.sink, a.local, &ns, &w0) + kItemPad
-                           : 0;
-        const long long end = warp_scan_ll(cost, lane);
+      p.b = lo;
+      if (lo > 0) r -= cum[lo - 1];
+      p.base = s_req[lo].x;
+      p.n = s_req[lo].y;
+      p.i = p.k = 0;
+      int cnt = 0;
+      for (int i0 = 0; i0 * W < p.n; i0 += 32) {
+        int ns, w0, mine = 0;
+        if ((i0 + lane) * W < p.n) mine = item_tiles(p.base, p.n, i0 + lane, W, p.win, a.sink, a.local, &ns, &w0);
+        const uint32_t cost = mine ? mine + kItemPad : 0, end = warp_scan(cost, lane);
         const uint32_t above = __ballot_sync(0xffffffffu, end > r);
         if (above) {
           const int src = __ffs(above) - 1;
-          i = i0 + src;
-          k = static_cast<int>(r - __shfl_sync(0xffffffffu, end - cost, src));
+          p.i = i0 + src;
+          p.k = static_cast<int>(r - __shfl_sync(0xffffffffu, end - cost, src));
+          cnt = __shfl_sync(0xffffffffu, mine, src);
           break;
         }
         r -= __shfl_sync(0xffffffffu, end, 31);
       }
-    };
-    // An item cut at the range's end is done first, one cut at its start next, the whole ones then: the
-    // parts of cut items are all there early, and their merges run beside the rest.
-    const long long x_first = x;
-    bool cut_first = false;
-    int fd = 0, fh = 0, fb = 0, fi = 0, fk = 0;
-    bool fwin = false;
-    if (x < x1) {
-      locate(x);
-      fwin = win, fd = d, fh = h, fb = b, fi = i, fk = k;
-      locate(x1 - 1);
-      int ns, w0;
-      const int cnt = item_tiles(base, n, i, W, win, a.sink, a.local, &ns, &w0);
-      const long long item0 = x1 - 1 - k;
-      cut_first = item0 > x && x1 < item0 + cnt;
-      if (cut_first) {
-        k = 0;
-        x = item0;
+      if (pass == 0) {
+        const uint32_t item0 = place - p.k;
+        cut_first = item0 > x && x1 < item0 + cnt;
+        if (cut_first) x_cut = item0;
+        at = p;
+        at.k = 0;
       } else {
-        win = fwin, d = fd, h = fh, b = fb, i = fi, k = fk;
-        load_request();
+        begin = p;
       }
     }
-    const long long x_cut = cut_first ? x : x1;  // what begins here is done first
+    const uint32_t x_first = x;
+    if (cut_first)
+      x = x_cut;
+    else
+      at = begin;
     __syncwarp();
     fence_proxy_async_smem();  // the prefix sums are read; the ring takes their place
 
@@ -699,28 +687,31 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     while (x < x1 && ok) {
       Unit un;
-      const int cnt = item_tiles(base, n, i, W, win, a.sink, a.local, &un.ns, &un.w0);
-      if (k < cnt) {
+      const int cnt = item_tiles(at.base, at.n, at.i, W, at.win, a.sink, a.local, &un.ns, &un.w0);
+      const int b = at.b, h = at.h, len = at.base + at.n;
+      if (at.k < cnt) {
+      un.kb = at.k;
+      un.ke = static_cast<int>(min(static_cast<uint32_t>(cnt), at.k + (x1 - x)));
+      const int nk = un.ke - un.kb;
+      int page = piece_page(piece_token(un.kb, un.ns, un.w0), b, len);
+      int page_next = nk > 1 ? piece_page(piece_token(un.kb + 1, un.ns, un.w0), b, len) : -2;
       un.valid = 1;
       un.b = b;
       un.h = h;
-      un.win = win;
-      un.tok0 = a.start[b] + i * W;
-      un.ntok = min(W, n - i * W);
-      un.pos0 = base + i * W;
+      un.win = at.win;
+      const int tok0 = a.start[b] + at.i * W;
+      un.ntok = min(W, at.n - at.i * W);
+      un.pos0 = at.base + at.i * W;
       un.len = len;
-      un.kb = k;
-      un.ke = static_cast<int>(min(static_cast<long long>(cnt), k + (x1 - x)));
       un.split = un.ntok <= TQ;
       un.whole = un.kb == 0 && un.ke == cnt;
-      const long long item0 = x - k, item1 = item0 + cnt;
-      un.cta0 = un.cta1 = blockIdx.x;
+      un.cta0 = un.cta1 = c;
       if (!un.whole) {
-        un.cta0 = static_cast<int>(quotient((item0 + 1) * ctas - 1, work));
-        un.cta1 = static_cast<int>(quotient(item1 * ctas - 1, work));
+        un.cta0 = owner(x - at.k);
+        un.cta1 = owner(x - at.k + cnt - 1);
       }
-      un.slot = 2 * blockIdx.x + (k > 0 ? 0 : 1);
-      const int nk = un.ke - un.kb;
+      un.slot = 2 * c + (at.k > 0 ? 0 : 1);
+      un.tok0 = tok0;
       // stream 0 of a pair ends at its own last token's tile
       un.n0 = nk;
       if (!un.split) {
@@ -730,14 +721,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const int us = u & 1;
       if (u >= 2 && !warp_wait(smem_u32(&ctl->uempty[us]), ((u >> 1) - 1) & 1, abort, kv.status)) break;
-      if (lane == 0) {
-        ctl->unit[us] = un;
-        mbar_arrive(smem_u32(&ctl->ufull[us]));
-      }
-      __syncwarp();
-
-      int page = piece_page(piece_token(un.kb, un.ns, un.w0), b, len);
-      int page_next = nk > 1 ? piece_page(piece_token(un.kb + 1, un.ns, un.w0), b, len) : -2;
+      auto publish = [&]() {
+        if (lane == 0) {
+          ctl->unit[us] = un;
+          mbar_arrive(smem_u32(&ctl->ufull[us]));
+        }
+        __syncwarp();
+      };
+      if (u > 0) publish();  // (the first unit's loads go out before it: nothing is there to wait for)
       if (u > 0 && !warp_wait(smem_u32(&ctl->qempty), (u - 1) & 1, abort, kv.status)) break;
       if (lane == 0) {
         const uint32_t bar = smem_u32(&ctl->qfull), bytes = static_cast<uint32_t>(G * TQ) * 128;
@@ -764,6 +755,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) ctl->kmask[(tiles + kk) & 7] = good;
         if (!(ok = warp_wait(smem_u32(&ctl->empty[pk.st]), pk.ph, abort, kv.status))) break;
         load_pieces(pk.st, &tmK, row, smem_u32(&ctl->full[pk.st]));
+        if (u == 0 && kk == 0) publish();
         pk.next2();
         page = page_next;
         page_next = page_after;
@@ -776,29 +768,28 @@ __global__ void __launch_bounds__(kThreads, 1)
         cut_first = false;
         x = x_first;
         x1 = x_cut;
-        win = fwin, d = fd, h = fh, b = fb, i = fi, k = fk;
-        load_request();
+        at = begin;
         continue;
       }
       // the next unit starts at the next item
-      x += cnt + kItemPad - k;
-      k = 0;
-      if (x < x1) {
-        if (++i >= nq) {
-          i = 0;
-          do {
-            if (++b >= kv.B) {
-              b = 0;
-              ++d;
-              if (!win && d >= hd) {
-                win = true;
-                d = 0;
-              }
-              h = nth_head(kv, win, d, lane, win_heads, there);
+      x += cnt + kItemPad - at.k;
+      at.k = 0;
+      if (x < x1 && ++at.i * W >= at.n) {
+        at.i = 0;
+        do {
+          if (++at.b >= kv.B) {
+            at.b = 0;
+            ++at.d;
+            if (!at.win && at.d >= hd) {
+              at.win = 1;
+              at.d = 0;
             }
-            load_request();
-          } while (n == 0);
-        }
+            at.h = nth_head(kv, at.win, at.d, lane, win_heads, there);
+          }
+          const int L = request_len(kv, at.b);
+          at.n = min(max(a.count[at.b], 0), L);
+          at.base = L - at.n;
+        } while (at.n == 0);
       }
     }
     if (!*abort) {
