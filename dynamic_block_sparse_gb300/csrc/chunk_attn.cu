@@ -607,34 +607,31 @@ __global__ void __launch_bounds__(kThreads, 1)
       hd += __popc(t & ~w);
     }
     const uint32_t dense_work = hd * total_d, work = dense_work + (kv.Hkv - hd) * total_s;
-    // equal ranges: CTA c has each + (c < more) places from c each + min(c, more) on
+    // Equal ranges: boundary c lies at c each + min(c, more), CTA c has what lies between boundaries c
+    // and c + 1.  A boundary that would cut less than `snap` off an item's start or end moves there: a
+    // sixteenth of a range more or less against a cut's record and merge.
     const uint32_t ctas = min(gridDim.x, (work + kMinWork - 1) / kMinWork);
     const uint32_t each = ctas ? work / ctas : 0, more = work - each * ctas, c = blockIdx.x;
-    const uint32_t wide_end = more * (each + 1);
+    const uint32_t wide_end = more * (each + 1), snap = max(each / 16, 1u);
     auto owner = [&](uint32_t at) {
-      return static_cast<int>(at < wide_end ? at / (each + 1) : more + (at - wide_end) / each);
+      return at < wide_end ? at / (each + 1) : more + (at - wide_end) / each;
     };
-    uint32_t x = c * each + min(c, more), x1 = x + each + (c < more);
-    if (c >= ctas) x1 = x = work;
+    auto boundary = [&](uint32_t c) { return c * each + min(c, more); };
+    uint32_t x = boundary(c);
+    const uint32_t x1 = c < ctas ? boundary(c + 1) : x;
+    if (c >= ctas) x = x1;
     // a place on the line: head, request, query tile, key tile
     struct At {
       int win, d, h, b, i, k, base, n;
     };
-    At at = {}, begin = {};
-    // An item cut at the range's end is done first, one cut at its start next, the whole ones then: the
-    // parts of cut items are all there early.
-    bool cut_first = false;
-    uint32_t x_cut = x1;  // where the item done first begins
-#pragma unroll 1
-    for (int pass = 0; pass < 2 && x < x1; ++pass) {  // the range's last place, then its first
-      const uint32_t place = pass == 0 ? x1 - 1 : x;
-      At p;
-      p.win = place >= dense_work;
-      const uint32_t per = p.win ? total_s : total_d, y = p.win ? place - dense_work : place;
-      p.d = y / per;
-      uint32_t r = y - p.d * per;
-      p.h = nth_head(kv, p.win, p.d, lane, win_heads, there);
-      const uint32_t* cum = p.win ? cum_s : cum_d;
+    At at = {};
+    if (x < x1) {
+      at.win = x >= dense_work;
+      const uint32_t per = at.win ? total_s : total_d, y = at.win ? x - dense_work : x;
+      at.d = y / per;
+      uint32_t r = y - at.d * per;
+      at.h = nth_head(kv, at.win, at.d, lane, win_heads, there);
+      const uint32_t* cum = at.win ? cum_s : cum_d;
       int lo = 0, hi = kv.B - 1;
       while (lo < hi) {
         const int mid = (lo + hi) >> 1;
@@ -643,41 +640,35 @@ __global__ void __launch_bounds__(kThreads, 1)
         else
           lo = mid + 1;
       }
-      p.b = lo;
+      at.b = lo;
       if (lo > 0) r -= cum[lo - 1];
-      p.base = s_req[lo].x;
-      p.n = s_req[lo].y;
-      p.i = p.k = 0;
-      int cnt = 0;
-      for (int i0 = 0; i0 * W < p.n; i0 += 32) {
-        int ns, w0, mine = 0;
-        if ((i0 + lane) * W < p.n) mine = item_tiles(p.base, p.n, i0 + lane, W, p.win, a.sink, a.local, &ns, &w0);
-        const uint32_t cost = mine ? mine + kItemPad : 0, end = warp_scan(cost, lane);
+      at.base = s_req[lo].x;
+      at.n = s_req[lo].y;
+      for (int i0 = 0; i0 * W < at.n; i0 += 32) {
+        int ns, w0;
+        uint32_t cost = 0;
+        if ((i0 + lane) * W < at.n)
+          cost = item_tiles(at.base, at.n, i0 + lane, W, at.win, a.sink, a.local, &ns, &w0) + kItemPad;
+        const uint32_t end = warp_scan(cost, lane);
         const uint32_t above = __ballot_sync(0xffffffffu, end > r);
         if (above) {
           const int src = __ffs(above) - 1;
-          p.i = i0 + src;
-          p.k = static_cast<int>(r - __shfl_sync(0xffffffffu, end - cost, src));
-          cnt = __shfl_sync(0xffffffffu, mine, src);
+          at.i = i0 + src;
+          const uint32_t k = r - __shfl_sync(0xffffffffu, end - cost, src);
+          const uint32_t whole = __shfl_sync(0xffffffffu, cost, src);
+          at.k = static_cast<int>(k);
+          if (k > 0 && k < snap) {
+            x -= k;
+            at.k = 0;
+          } else if (k > 0 && whole - k < snap) {
+            x += whole - k;  // nothing of it
+            at.k = static_cast<int>(whole);
+          }
           break;
         }
         r -= __shfl_sync(0xffffffffu, end, 31);
       }
-      if (pass == 0) {
-        const uint32_t item0 = place - p.k;
-        cut_first = item0 > x && x1 < item0 + cnt;
-        if (cut_first) x_cut = item0;
-        at = p;
-        at.k = 0;
-      } else {
-        begin = p;
-      }
     }
-    const uint32_t x_first = x;
-    if (cut_first)
-      x = x_cut;
-    else
-      at = begin;
     __syncwarp();
     fence_proxy_async_smem();  // the prefix sums are read; the ring takes their place
 
@@ -688,10 +679,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     while (x < x1 && ok) {
       Unit un;
       const int cnt = item_tiles(at.base, at.n, at.i, W, at.win, a.sink, a.local, &un.ns, &un.w0);
+      const uint32_t item0 = x - at.k, item1 = item0 + cnt + kItemPad;
+      int take = cnt;  // tiles of the item before the range's end
+      if (x1 < item1) {
+        if (x1 - item0 < snap) break;  // (it begins too near the end: the next CTA's)
+        if (item1 - x1 >= snap) take = min(cnt, static_cast<int>(x1 - item0));
+      }
       const int b = at.b, h = at.h, len = at.base + at.n;
-      if (at.k < cnt) {
+      if (at.k < take) {
       un.kb = at.k;
-      un.ke = static_cast<int>(min(static_cast<uint32_t>(cnt), at.k + (x1 - x)));
+      un.ke = take;
       const int nk = un.ke - un.kb;
       int page = piece_page(piece_token(un.kb, un.ns, un.w0), b, len);
       int page_next = nk > 1 ? piece_page(piece_token(un.kb + 1, un.ns, un.w0), b, len) : -2;
@@ -706,9 +703,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       un.split = un.ntok <= TQ;
       un.whole = un.kb == 0 && un.ke == cnt;
       un.cta0 = un.cta1 = c;
-      if (!un.whole) {
-        un.cta0 = owner(x - at.k);
-        un.cta1 = owner(x - at.k + cnt - 1);
+      if (!un.whole) {  // who has its first and its last tile
+        const uint32_t o0 = owner(item0), o1 = owner(item0 + cnt - 1);
+        un.cta0 = o0 + (boundary(o0 + 1) - item0 < snap);
+        un.cta1 = o1 - (item1 - boundary(o1) < snap);
       }
       un.slot = 2 * c + (at.k > 0 ? 0 : 1);
       un.tok0 = tok0;
@@ -764,15 +762,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       tiles += nk;
       ++u;
       }  // (a range may begin in the pad behind an item's tiles)
-      if (cut_first) {  // back to the range's start
-        cut_first = false;
-        x = x_first;
-        x1 = x_cut;
-        at = begin;
-        continue;
-      }
       // the next unit starts at the next item
-      x += cnt + kItemPad - at.k;
+      x = item1;
       at.k = 0;
       if (x < x1 && ++at.i * W >= at.n) {
         at.i = 0;
@@ -1019,32 +1010,29 @@ __global__ void __launch_bounds__(kThreads, 1)
           // half is read twice, so that a thread holds 64 of them at most.
           uint32_t ra[64];
           tmem_ld_64(tS + 64, ra);
-          if (__any_sync(0xffffffffu, cut || kmask != 0xffu)) {
-            // Tiles at an edge of the mask are masked in TMEM first, so that the common path holds its
-            // row in the registers the load wrote.  The row's visible columns as bits: up to its own
-            // position, in the sink or the window, on good pages.
-            const int pos = un.pos0 + min(my_tok, un.ntok - 1);
-            const int hi = pos - t0, lo = win ? max(pos - a.local, -1) - t0 : -1;
-            const int sk = win ? a.sink - t0 - 1 : -1;
-#pragma unroll 1
-            for (int w = 0; w < 4; ++w) {
-              const uint32_t groups = ((kmask >> (2 * w) & 1) ? 0x0000ffffu : 0u) |
-                                      ((kmask >> (2 * w + 1) & 1) ? 0xffff0000u : 0u);
-              const uint32_t seen = bits_to(hi - 32 * w) &
-                                    (~bits_to(lo - 32 * w) | bits_to(sk - 32 * w)) & groups;
-              if (__all_sync(0xffffffffu, seen == 0xffffffffu)) continue;
-              uint32_t r[32];
-              tmem_ld_32(tS + 32 * w, r);
+          // the row's visible columns as bits: up to its own position, in the sink or the window, on
+          // good pages
+          const bool masked = __any_sync(0xffffffffu, cut || kmask != 0xffu);
+          const int pos = un.pos0 + min(my_tok, un.ntok - 1);
+          const int hi = pos - t0, lo = win ? max(pos - a.local, -1) - t0 : -1;
+          const int sk = win ? a.sink - t0 - 1 : -1;
+          auto mask = [&](int c0) {
+#pragma unroll
+            for (int w = 0; w < 2; ++w) {
+              const int c = c0 + 32 * w, g = c / 16;
+              const uint32_t groups = ((kmask >> g & 1) ? 0x0000ffffu : 0u) |
+                                      ((kmask >> (g + 1) & 1) ? 0xffff0000u : 0u);
+              const uint32_t seen =
+                  bits_to(hi - c) & (~bits_to(lo - c) | bits_to(sk - c)) & groups;
 #pragma unroll
               for (int e = 0; e < 32; ++e)
-                if (!(seen >> e & 1)) r[e] = 0xff800000u;  // -inf
-              tmem_st_32(tS + 32 * w, r);
+                if (!(seen >> e & 1)) ra[32 * w + e] = 0xff800000u;  // -inf
             }
-            tmem_wait_st();
-            tmem_ld_64(tS + 64, ra);
-          }
+          };
+          if (masked) mask(64);
           float m0 = row_max(ra, mtrue);
           tmem_ld_64(tS, ra);
+          if (masked) mask(0);
           m0 = row_max(ra, m0);
           mtrue = m0;
           const bool up = mtrue * sc > mref * sc + kLazyLog2;
@@ -1082,6 +1070,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_st_16(tS + 16, p);
           deliver(0);
           tmem_ld_64(tS + 64, ra);
+          if (masked) mask(64);
           expo(ra, sc2, mm2, la, lb, p);
           tmem_st_16(tS + 32, p);
           expo(ra + 32, sc2, mm2, la, lb, p);
