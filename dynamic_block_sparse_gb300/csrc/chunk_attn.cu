@@ -82,7 +82,7 @@ constexpr uint32_t kOffCtl = kOffRing + kRing * kTileBytes;
 struct Ctl {
   unsigned long long full[kRing], empty[kRing];
   unsigned long long qfull, qempty, sfull[2], pready[2][2], odone[2], ufull[2], uempty[2],
-      sdone[2], ofree, meet, help, tail[4];
+      sdone[2], ofree, meet, help, all, tail[4], rows_in[12];
   uint32_t tmem;
   int abort, last, pad;
   Unit unit[2];
@@ -162,6 +162,9 @@ DSA_DEV void tmem_st_32(uint32_t addr, const uint32_t (&r)[32]) {
 DSA_DEV void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 DSA_DEV void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 DSA_DEV void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
+// Orders this thread's ordinary accesses before its later bulk copies, in every state space.
+DSA_DEV void fence_proxy_async() { asm volatile("fence.proxy.async;" ::: "memory"); }
 
 // One lane of the converged warp.
 DSA_DEV bool elect_one() {
@@ -364,71 +367,113 @@ DSA_DEV bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort, int32
   return __all_sync(0xffffffffu, ok);
 }
 
-// Merges a cut item's records in CTA order with `threads` threads: `per` threads a row, each with 32 / per float4s of it.  Not inlined: its registers are its own.
-__device__ __noinline__ void merge_records(const ChunkAttnArgs& a, const Merge& w, int me, int threads) {
-  const int G = a.kv.G, rows = w.ntok * G;
+// Merges a cut item's records in CTA order, with the softmax and epilogue warps, at the CTA's end (the
+// query tiles and the ring are free).  An output row is a weighted sum of the records' rows.  A warp
+// takes neighbouring rows, a lane a float4 of each; up to kMergeRows rows (over the parts) come at once
+// by bulk copies into places of its own, because plain loads of records that other SMs have just
+// written stay at some 16 bytes a cycle whatever their number.  Meanwhile the weights, one per part and
+// row, are worked out a row a thread.  A record: O [rows][128], then reference m, sum l and true maximum
+// of the rows, each [rec_rows].
+constexpr int kMergeWarps = kLoadWarp, kMergeRows = 26, kMergeWeights = 16384;
+static_assert(kMergeWeights * 4 <= kOffRing, "the weights overlay the query tiles");
+static_assert(kMergeWarps * kMergeRows * 512 <= kRing * kTileBytes, "the rows overlay the ring");
+__device__ __noinline__ bool merge_records(const ChunkAttnArgs& a, const Merge& w, uint8_t* smem, Ctl* ctl,
+                                           uint32_t* phase) {
+  const int G = a.kv.G, rows = w.ntok * G, parts = w.parts;
+  const int me = threadIdx.x, lane = me & 31, warp = me >> 5;
   const float sc = a.scale_log2;
-  const size_t R = a.rec_rows;
-  int per = 1;
-  while (per < 32 && 2 * per * rows <= threads) per *= 2;
-  const int at_once = threads / per;
-  const size_t rec4 = R * (kRecordFloats / 4);  // float4s of a record
-  const float4* first = reinterpret_cast<const float4*>(a.records) + 2 * w.cta0 * rec4;
-  auto record = [&](int q) { return first + (2 * q + (q == 0)) * rec4; };
-  for (int r0 = 0; r0 < rows; r0 += at_once) {
-    const int mr = r0 + me % at_once, sub = me / at_once;
-    if (mr >= rows) continue;
-    auto sums = [&](int q) { return reinterpret_cast<const float*>(record(q) + 32 * R) + mr; };
-    float M = -INFINITY, Mt = -INFINITY, ls = 0.f;
-#pragma unroll 4
-    for (int q = 0; q < w.parts; ++q) {
-      M = fmaxf(M, __ldcg(sums(q)));
-      Mt = fmaxf(Mt, __ldcg(sums(q) + 2 * R));
-    }
-    const float Mz = M > -INFINITY ? M : 0.f;
-#pragma unroll 4
-    for (int q = 0; q < w.parts; ++q) ls += __ldcg(sums(q) + R) * fast_exp2((__ldcg(sums(q)) - Mz) * sc);
-    const float iv = ls == 0.f ? 0.f : 1.f / ls;
-    const size_t at = static_cast<size_t>(w.tok0 + mr / G) * a.kv.Hq + w.h * G + mr % G;
-    auto sum = [&](auto width, int c) {  // float4s c .. c + width - 1
-      constexpr int N = decltype(width)::value;
-      float4 o[N];
-#pragma unroll
-      for (int e = 0; e < N; ++e) o[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll (N >= 8 ? 2 : 8 / N)
-      for (int q = 0; q < w.parts; ++q) {
-        const float4* rq = record(q) + c * R + mr;
-        float4 v[N];
-#pragma unroll
-        for (int e = 0; e < N; ++e) v[e] = __ldcg(rq + e * R);
-        const float wq = fast_exp2((__ldcg(sums(q)) - Mz) * sc);
-#pragma unroll
-        for (int e = 0; e < N; ++e) {
-          o[e].x = fmaf(v[e].x, wq, o[e].x);
-          o[e].y = fmaf(v[e].y, wq, o[e].y);
-          o[e].z = fmaf(v[e].z, wq, o[e].z);
-          o[e].w = fmaf(v[e].w, wq, o[e].w);
-        }
+  const size_t R = a.rec_rows, rec = R * kRecordFloats;
+  const float* first = a.records + (2 * w.cta0 + 1) * rec;  // part 0; part q > 0 lies 2 q - 1 behind it
+  auto part = [&](int q) { return first + (q > 0 ? 2 * q - 1 : 0) * rec; };
+  auto meet = [&]() {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&ctl->all));
+    return warp_wait(smem_u32(&ctl->all), phase[0]++ & 1, &ctl->abort, a.kv.status);
+  };
+  const uint32_t per_token = 65536u / G + 1;  // row / G = row * per_token >> 16 for rows below 256
+  auto out_row = [&](int r) {
+    const int t = static_cast<int>(r * per_token >> 16);
+    return static_cast<size_t>(w.tok0 + t) * a.kv.Hq + w.h * G + r - t * G;
+  };
+  const int group = min(rows, kMergeWeights / parts);       // rows whose weights fit
+  float* weight = reinterpret_cast<float*>(smem);           // [part][row of the group]
+  uint8_t* place = smem + kOffRing + warp * kMergeRows * 512;
+  const uint32_t bar = smem_u32(&ctl->rows_in[warp]);
+  const int nq = min(parts, kMergeRows), nr = kMergeRows / nq;  // parts and rows at once
+  for (int r0 = 0; r0 < rows; r0 += group) {
+    const int here = min(group, rows - r0);
+    // this warp's rows b0 .. b1 - 1 of the group, nr of them at once
+    const int share = (here + kMergeWarps - 1) / kMergeWarps;
+    const int b0 = min(warp * share, here), b1 = min(b0 + share, here);
+    auto fetch = [&](int b, int q0) {
+      const int n = min(nq, parts - q0);
+      const uint32_t bytes = min(nr, b1 - b) * 512;
+      if (lane == 0) {
+        fence_proxy_async();  // the records were written, and the places read, by ordinary accesses
+        mbar_arrive_expect_tx(bar, n * bytes);
+        for (int q = 0; q < n; ++q)
+          bulk_load(smem_u32(place) + q * bytes, part(q0 + q) + static_cast<size_t>(r0 + b) * kHeadDim, bytes,
+                    bar);
       }
-      __nv_bfloat16* dst = a.out + at * kHeadDim + 4 * c;
-#pragma unroll
-      for (int e = 0; e < N; ++e) {
-        uint2 v;
-        v.x = pack_bf16(o[e].x * iv, o[e].y * iv);
-        v.y = pack_bf16(o[e].z * iv, o[e].w * iv);
-        *reinterpret_cast<uint2*>(dst + 4 * e) = v;
-      }
+      __syncwarp();
     };
-    const int each = 32 / per, c_end = (sub + 1) * each;
-    if (each >= 8)
-      for (int c = sub * each; c < c_end; c += 8) sum(std::integral_constant<int, 8>(), c);
-    else
-      for (int c = sub * each; c < c_end; ++c) sum(std::integral_constant<int, 1>(), c);
-    if (sub == 0) {
-      if (a.m) a.m[at] = Mt * sc * kLn2;
-      if (a.l) a.l[at] = Mt > -INFINITY ? ls * fast_exp2((M - Mt) * sc) : ls;
+    if (b0 < b1) fetch(b0, 0);
+    for (int r = me; r < here; r += kMergeWarps * 32) {
+      const size_t off = kHeadDim * R + r0 + r;
+      float M = -INFINITY, Mt = -INFINITY, l = 0.f;
+#pragma unroll 4
+      for (int q = 0; q < parts; ++q) {
+        const float m = __ldcg(part(q) + off);
+        M = fmaxf(M, m);
+        Mt = fmaxf(Mt, __ldcg(part(q) + off + 2 * R));
+        weight[q * here + r] = m;
+      }
+      const float Mz = M > -INFINITY ? M : 0.f;
+#pragma unroll 4
+      for (int q = 0; q < parts; ++q) {
+        const float f = fast_exp2((weight[q * here + r] - Mz) * sc);
+        l += __ldcg(part(q) + off + R) * f;
+        weight[q * here + r] = f;
+      }
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      for (int q = 0; q < parts; ++q) weight[q * here + r] *= inv;
+      const size_t o = out_row(r0 + r);
+      if (a.m) a.m[o] = Mt * sc * kLn2;
+      if (a.l) a.l[o] = Mt > -INFINITY ? l * fast_exp2((M - Mt) * sc) : l;
     }
+    if (!meet()) return false;
+    for (int b = b0; b < b1; b += nr) {
+      const int nb = min(nr, b1 - b);              // rows of this batch
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);  // (carried over blocks of parts; nr is 1 then)
+      for (int q0 = 0; q0 < parts; q0 += nq) {
+        if (b != b0 || q0 != 0) fetch(b, q0);
+        if (!warp_wait(bar, phase[1]++ & 1, &ctl->abort, a.kv.status)) return false;
+        const int n = min(nq, parts - q0);
+#pragma unroll 2
+        for (int i = 0; i < nb; ++i) {
+#pragma unroll 2
+          for (int q = 0; q < n; ++q) {
+            const float4 v = *reinterpret_cast<const float4*>(place + (q * nb + i) * 512 + lane * 16);
+            const float f = weight[(q0 + q) * here + b + i];
+            o.x = fmaf(v.x, f, o.x);
+            o.y = fmaf(v.y, f, o.y);
+            o.z = fmaf(v.z, f, o.z);
+            o.w = fmaf(v.w, f, o.w);
+          }
+          if (q0 + nq >= parts) {
+            uint2 v;
+            v.x = pack_bf16(o.x, o.y);
+            v.y = pack_bf16(o.z, o.w);
+            *reinterpret_cast<uint2*>(a.out + out_row(r0 + b + i) * kHeadDim + lane * 4) = v;
+            o = make_float4(0.f, 0.f, 0.f, 0.f);
+          }
+        }
+        __syncwarp();  // the places are read
+      }
+    }
+    if (!meet()) return false;  // (the weights' and the rows' places are free again)
   }
+  return true;
 }
 
 __global__ void __launch_bounds__(kThreads, 1)
@@ -464,6 +509,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(smem_u32(&ctl->ofree), 4);
     mbar_init(smem_u32(&ctl->meet), 4);
     mbar_init(smem_u32(&ctl->help), 1);
+    mbar_init(smem_u32(&ctl->all), kLoadWarp);
+    for (int w = 0; w < 12; ++w) mbar_init(smem_u32(&ctl->rows_in[w]), 1);
     for (int s = 0; s < 4; ++s) mbar_init(smem_u32(&ctl->tail[s]), 1);
     ctl->abort = 0;
     fence_mbar_init();
@@ -1125,7 +1172,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         return static_cast<size_t>(un.tok0 + my_tok) * kv.Hq + un.h * G + r_head;
       };
       auto rec_row = [&](int my_tok) {
-        return a.records + static_cast<size_t>(un.slot) * R * kRecordFloats + 4 * (my_tok * G + r_head);
+        return a.records + static_cast<size_t>(un.slot) * R * kRecordFloats +
+               static_cast<size_t>(my_tok * G + r_head) * kHeadDim;
       };
 
       // 32 columns of this row to the output or the record
@@ -1140,10 +1188,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             store32(dst + e, v);
           }
         } else {
-          float* dst = rec_row(my_tok) + c0 * R;
+          float* dst = rec_row(my_tok) + c0;
 #pragma unroll
-          for (int e = 0; e < 32; e += 4)
-            *reinterpret_cast<float4*>(dst + e * R) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+          for (int e = 0; e < 32; e += 8) {
+            uint32_t v[8];
+#pragma unroll
+            for (int x = 0; x < 8; ++x) v[x] = __float_as_uint(o[e + x]);
+            store32(dst + e, v);
+          }
         }
       };
       // its sums (reference m, sum l relative to it, true maximum)
@@ -1153,7 +1205,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (a.m) a.m[at] = mtrue * sc * kLn2;
           if (a.l) a.l[at] = mtrue > -INFINITY ? l * fast_exp2((m - mtrue) * sc) : l;
         } else {
-          float* ml = rec_row(0) - 4 * r_head + 128 * R + my_tok * G + r_head;
+          float* ml = a.records + static_cast<size_t>(un.slot) * R * kRecordFloats + kHeadDim * R +
+                      my_tok * G + r_head;
           ml[0] = m;
           ml[R] = l;
           ml[2 * R] = mtrue;
@@ -1256,7 +1309,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   // ---- the merges, by softmax and epilogue warps
   if (warp < kLoadWarp && warp_wait(smem_u32(&ctl->help), 0, abort, kv.status)) {
     const int merges = *const_cast<volatile int*>(&ctl->merges);
-    for (int x = 0; x < merges; ++x) merge_records(a, ctl->merge[x], tid, kLoadWarp * 32);
+    uint32_t phase[2] = {0, 0};
+    for (int x = 0; x < merges; ++x)
+      if (!merge_records(a, ctl->merge[x], smem, ctl, phase)) break;
   }
   __syncthreads();
   if (warp == kMmaWarp)
@@ -1273,8 +1328,8 @@ int chunk_attn_grid() {
   return sms < kChunkMaxGrid ? sms : kChunkMaxGrid;
 }
 
-// Tickets of the grid, 256 maxima per CTA, then two partial records per CTA: [32][rows] float4 of O,
-// then mref, l and mtrue of the rows.
+// Tickets of the grid, 256 maxima per CTA, then two partial records per CTA: O [rows][128], then mref,
+// l and mtrue of the rows.
 ChunkAttnWorkspace chunk_attn_workspace(int G, int tokens) {
   ChunkAttnWorkspace w;
   const long long rows = static_cast<long long>(tokens) * G;
