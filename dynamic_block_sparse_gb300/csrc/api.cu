@@ -1180,7 +1180,6 @@ int dsa_chunk_attn(const dsa_paged_kv* kv, const dsa_chunk* chunk, const void* q
   a.m = m;
   a.l = l;
   a.tickets = static_cast<int32_t*>(workspace);
-  a.maxima = reinterpret_cast<float*>(static_cast<char*>(workspace) + w.maxima_off);
   a.records = reinterpret_cast<float*>(static_cast<char*>(workspace) + w.records_off);
   a.rec_rows = w.rows;
   cudaError_t e = launch_chunk_attn(tq, tk, tv, a, static_cast<cudaStream_t>(stream));

@@ -21,12 +21,11 @@
 // No CTA waits for another.
 //
 // Inside a CTA: warps 0-3 and 4-7 are the streams' softmax warpgroups (a thread owns a row: S from
-// TMEM, P back to TMEM over S as bf16), warps 8-11 take a finished unit's accumulators out (normalised
-// to the output, or to a record, and the merges) while the softmax is at the next unit, warps 12 and 15
-// load (TMA: Q and K tiles; V tiles; of 128 tokens, assembled from page pieces, into a ring of five
-// 32 KB stages, K and V in turn: with pages of 16 tokens one warp issues the 32 pieces of a K and a V
-// tile in more time than the products take), one thread of warp 13 issues the tcgen05 products (S =
-// Q K^T from shared memory, O += P V with P from TMEM), and warp 14 clears the rows behind a request's
+// TMEM, P back to TMEM over S as bf16, at a unit's end O from TMEM to the output or to a record), warps 8
+// and 11 load (TMA: Q and K tiles; V tiles; of 128 tokens, assembled from page pieces, into a ring of
+// five 32 KB stages, K and V in turn: with pages of 16 tokens one warp issues the 32 pieces of a K and
+// a V tile in more time than the products take), one thread of warp 9 issues the tcgen05 products (S =
+// Q K^T from shared memory, O += P V with P from TMEM), and warp 10 clears the rows behind a request's
 // last token in the V tile that holds it.
 #include "common.cuh"
 #include "internal.h"
@@ -36,9 +35,8 @@
 namespace dsa {
 namespace {
 
-constexpr int kThreads = 512;
-constexpr int kOutWarp = 8;  // 8 .. 11: the epilogue warpgroup
-constexpr int kLoadWarp = 12, kMmaWarp = 13, kTailWarp = 14, kValueWarp = 15;
+constexpr int kThreads = 384;
+constexpr int kLoadWarp = 8, kMmaWarp = 9, kTailWarp = 10, kValueWarp = 11;
 constexpr int kRing = 5;
 constexpr uint32_t kHalfBytes = 128 * 128;  // 64 dims of 128 rows, 128-byte swizzled lines
 constexpr uint32_t kTileBytes = 2 * kHalfBytes;
@@ -48,10 +46,10 @@ constexpr uint32_t kTileBytes = 2 * kHalfBytes;
 constexpr int kItemPad = 1, kMinWork = 5;
 constexpr float kLazyLog2 = 8.f;  // P stays below 2^8 times its weight at the true maximum
 
-// Registers per thread of the softmax, the epilogue and the other warps.  The launch has 128 x 512, and
-// 144 x 256 + 128 x 128 + 96 x 128 is exactly that.
-constexpr int kSoftmaxRegs = 144, kOutRegs = 128, kOtherRegs = 96;
-static_assert(kSoftmaxRegs * 256 + (kOutRegs + kOtherRegs) * 128 <= 128 * kThreads, "registers");
+// Registers per thread of the softmax and of the other warps.  The launch has 168 x 384 = 64512, and
+// 208 x 256 + 88 x 128 is exactly that.
+constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
+static_assert(kSoftmaxRegs * 256 + kOtherRegs * 128 <= 168 * kThreads, "registers of the launch");
 template <int N>
 DSA_DEV void regs_inc() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
@@ -65,15 +63,18 @@ DSA_DEV void regs_dec() {
 constexpr uint32_t kS0 = 0, kO0 = 256;  // S of stream t at 128 t, O of stream t at 256 + 128 t
 
 struct Unit {  // a run of key tiles of one item, as published by the load warp
-  int valid, b, h, win;
-  int tok0, ntok, pos0, len;
-  int kb, ke, ns, w0;      // tiles kb .. ke - 1 of the item's list: k < ns ? k : w0 + k - ns
-  int split, whole, n0;    // streams share the query tile; not cut; tiles of stream 0 (pair mode)
-  int cta0, cta1, slot;    // CTAs of a cut item, this unit's record
+  int b, h, tok0, ntok, pos0, len;
+  int kb, ke, ns, w0;  // tiles kb .. ke - 1 of the item's list: k < ns ? k : w0 + k - ns
+  int n0;              // tiles of stream 0 (pair mode)
+  int cta0, cta1;      // CTAs of a cut item
+  uint8_t valid, win;
+  uint8_t split, whole;  // the streams share the query tile; the item is not cut
 };
 
 struct Merge {  // a cut item whose records are all there
-  int tok0, ntok, h, cta0, parts;
+  int tok0, h;
+  uint16_t ntok, parts;
+  int cta0;
 };
 
 // ---- shared memory
@@ -82,15 +83,15 @@ constexpr uint32_t kOffCtl = kOffRing + kRing * kTileBytes;
 struct Ctl {
   unsigned long long full[kRing], empty[kRing];
   unsigned long long qfull, qempty, sfull[2], pready[2][2], odone[2], ufull[2], uempty[2],
-      sdone[2], ofree, meet, help, all, tail[4], rows_in[12];
+      both, help, tail[4], rows_in[8];
   uint32_t tmem;
   int abort, last, pad;
   Unit unit[2];
   Merge merge[2];  // cut items to merge at the CTA's end, where the softmax warps lend a hand
   int merges;
-  int tail_stage[4], tail_row[4];  // V tiles with rows to clear: ring stage (-1: the end), first row
-  uint32_t kmask[8];      // valid 16-token groups of a key tile
-  float xm[2][128], xl[2][128];  // a finished unit's reference and sum per stream and row
+  int16_t tail_stage[4], tail_row[4];  // V tiles with rows to clear: ring stage (-1: the end), first row
+  uint8_t kmask[8];  // valid 16-token groups of a key tile
+  float xm[2][128], xl[2][128], xtrue[128];  // a split unit's sums per stream and row
 };
 constexpr uint32_t kSmemBytes = kOffCtl + sizeof(Ctl);
 static_assert(kSmemBytes <= 227 * 1024, "shared memory of one CTA");
@@ -256,6 +257,32 @@ DSA_DEV uint32_t warp_scan(uint32_t v, int lane) {
   return v;
 }
 
+// The line's places of one KV head for 32 requests, one a lane (base tokens before its n new ones):
+// dense and, where `windows`, streaming.
+DSA_DEV uint2 line_places(int base, int n, int W, bool windows, int sink, int local, int lane) {
+  int ns, w0;
+  uint2 c = make_uint2(0, 0);
+  if (n > 0 && n <= W) {
+    c.x = item_tiles(base, n, 0, W, false, 0, 0, &ns, &w0) + kItemPad;
+    if (windows) c.y = item_tiles(base, n, 0, W, true, sink, local, &ns, &w0) + kItemPad;
+  }
+  uint32_t several = __ballot_sync(0xffffffffu, n > W);
+  while (several) {  // the warp shares a request's query tiles
+    const int src = __ffs(several) - 1;
+    several &= several - 1;
+    const int wn = __shfl_sync(0xffffffffu, n, src), wb = __shfl_sync(0xffffffffu, base, src);
+    uint32_t d = 0, s = 0;
+    for (int i = lane; i * W < wn; i += 32) {
+      d += item_tiles(wb, wn, i, W, false, 0, 0, &ns, &w0) + kItemPad;
+      if (windows) s += item_tiles(wb, wn, i, W, true, sink, local, &ns, &w0) + kItemPad;
+    }
+    d = __reduce_add_sync(0xffffffffu, d);
+    s = __reduce_add_sync(0xffffffffu, s);
+    if (lane == src) c = make_uint2(d, s);
+  }
+  return c;
+}
+
 // 32 bytes in one store; 16 where the rows of the caller's tensor are not 32-byte aligned.
 DSA_DEV void store32(void* dst, const uint32_t (&v)[8]) {
   if ((reinterpret_cast<uintptr_t>(dst) & 31) == 0) {
@@ -367,14 +394,14 @@ DSA_DEV bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort, int32
   return __all_sync(0xffffffffu, ok);
 }
 
-// Merges a cut item's records in CTA order, with the softmax and epilogue warps, at the CTA's end (the
-// query tiles and the ring are free).  An output row is a weighted sum of the records' rows.  A warp
+// Merges a cut item's records in CTA order, with the softmax warps, at the CTA's end (the query
+// tiles and the ring are free).  An output row is a weighted sum of the records' rows.  A warp
 // takes neighbouring rows, a lane a float4 of each; up to kMergeRows rows (over the parts) come at once
 // by bulk copies into places of its own, because plain loads of records that other SMs have just
 // written stay at some 16 bytes a cycle whatever their number.  Meanwhile the weights, one per part and
 // row, are worked out a row a thread.  A record: O [rows][128], then reference m, sum l and true maximum
 // of the rows, each [rec_rows].
-constexpr int kMergeWarps = kLoadWarp, kMergeRows = 26, kMergeWeights = 16384;
+constexpr int kMergeWarps = kLoadWarp, kMergeRows = 40, kMergeWeights = 16384;
 static_assert(kMergeWeights * 4 <= kOffRing, "the weights overlay the query tiles");
 static_assert(kMergeWarps * kMergeRows * 512 <= kRing * kTileBytes, "the rows overlay the ring");
 __device__ __noinline__ bool merge_records(const ChunkAttnArgs& a, const Merge& w, uint8_t* smem, Ctl* ctl,
@@ -387,8 +414,8 @@ __device__ __noinline__ bool merge_records(const ChunkAttnArgs& a, const Merge& 
   auto part = [&](int q) { return first + (q > 0 ? 2 * q - 1 : 0) * rec; };
   auto meet = [&]() {
     __syncwarp();
-    if (lane == 0) mbar_arrive(smem_u32(&ctl->all));
-    return warp_wait(smem_u32(&ctl->all), phase[0]++ & 1, &ctl->abort, a.kv.status);
+    if (lane == 0) mbar_arrive(smem_u32(&ctl->both));
+    return warp_wait(smem_u32(&ctl->both), phase[0]++ & 1, &ctl->abort, a.kv.status);
   };
   const uint32_t per_token = 65536u / G + 1;  // row / G = row * per_token >> 16 for rows below 256
   auto out_row = [&](int r) {
@@ -503,14 +530,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(smem_u32(&ctl->pready[t][1]), 4);
       mbar_init(smem_u32(&ctl->odone[t]), 1);
       mbar_init(smem_u32(&ctl->ufull[t]), 1);
-      mbar_init(smem_u32(&ctl->uempty[t]), 14);  // softmax and epilogue warps, issue and value warp
-      mbar_init(smem_u32(&ctl->sdone[t]), 4);
+      mbar_init(smem_u32(&ctl->uempty[t]), 10);  // softmax warps, issue warp, value warp
     }
-    mbar_init(smem_u32(&ctl->ofree), 4);
-    mbar_init(smem_u32(&ctl->meet), 4);
+    mbar_init(smem_u32(&ctl->both), 8);          // the softmax warps
     mbar_init(smem_u32(&ctl->help), 1);
-    mbar_init(smem_u32(&ctl->all), kLoadWarp);
-    for (int w = 0; w < 12; ++w) mbar_init(smem_u32(&ctl->rows_in[w]), 1);
+    for (int w = 0; w < 8; ++w) mbar_init(smem_u32(&ctl->rows_in[w]), 1);
     for (int s = 0; s < 4; ++s) mbar_init(smem_u32(&ctl->tail[s]), 1);
     ctl->abort = 0;
     fence_mbar_init();
@@ -530,58 +554,32 @@ __global__ void __launch_bounds__(kThreads, 1)
   grid_dependency_wait();
 
   // ---- the line of work: prefix sums over the requests of an item row's tiles, dense and streaming
-  // (the host bounds the line by 2^31)
+  // (the host bounds the line by 2^31).  Up to 32 requests the load warp keeps them in its lanes;
+  // otherwise the whole CTA makes them in shared memory.
   uint32_t* cum_d = reinterpret_cast<uint32_t*>(smem + kOffRing);  // [B]
   uint32_t* cum_s = cum_d + kv.B;
   uint32_t* s_warp = cum_s + kv.B;  // [2][kThreads / 32]
   int2* s_req = reinterpret_cast<int2*>(smem);  // [B]: tokens before the chunk, new tokens
-  const int warps = min((kv.B + 31) / 32, kThreads / 32);  // with requests of their own
+  const bool in_lanes = kv.B <= 32;
   uint32_t total_d = 0, total_s = 0;
-  for (int b0 = 0; b0 < kv.B; b0 += kThreads) {
-    uint32_t cd = 0, cs = 0;
+  for (int b0 = 0; b0 < kv.B && !in_lanes; b0 += kThreads) {
     const int b = b0 + tid;
-    if (warp < warps) {
-      int n = 0, base = 0;
-      if (b < kv.B) {
-        const int L = request_len(kv, b);
-        n = min(max(a.count[b], 0), L);
-        base = L - n;
-        s_req[b] = make_int2(base, n);
-      }
-      const int nq = n > W ? (n + W - 1) / W : n > 0;
-      uint32_t several = __ballot_sync(0xffffffffu, nq > 1);
-      int ns, w0;
-      if (nq == 1) {
-        cd = item_tiles(base, n, 0, W, false, 0, 0, &ns, &w0) + kItemPad;
-        cs = item_tiles(base, n, 0, W, true, a.sink, a.local, &ns, &w0) + kItemPad;
-      }
-      while (several) {  // the warp shares a request's query tiles
-        const int src = __ffs(several) - 1;
-        several &= several - 1;
-        const int wn = __shfl_sync(0xffffffffu, n, src), wb = __shfl_sync(0xffffffffu, base, src);
-        const int wq = __shfl_sync(0xffffffffu, nq, src);
-        uint32_t d = 0, s = 0;
-        for (int i = lane; i < wq; i += 32) {
-          d += item_tiles(wb, wn, i, W, false, 0, 0, &ns, &w0) + kItemPad;
-          s += item_tiles(wb, wn, i, W, true, a.sink, a.local, &ns, &w0) + kItemPad;
-        }
-        d = __reduce_add_sync(0xffffffffu, d);
-        s = __reduce_add_sync(0xffffffffu, s);
-        if (lane == src) {
-          cd = d;
-          cs = s;
-        }
-      }
-      cd = warp_scan(cd, lane);
-      cs = warp_scan(cs, lane);
-      if (lane == 31) {
-        s_warp[warp] = cd;
-        s_warp[kThreads / 32 + warp] = cs;
-      }
+    int n = 0, base = 0;
+    if (b < kv.B) {
+      const int L = request_len(kv, b);
+      n = min(max(a.count[b], 0), L);
+      base = L - n;
+      s_req[b] = make_int2(base, n);
+    }
+    const uint2 cost = line_places(base, n, W, kv.streaming != nullptr, a.sink, a.local, lane);
+    const uint32_t cd = warp_scan(cost.x, lane), cs = warp_scan(cost.y, lane);
+    if (lane == 31) {
+      s_warp[warp] = cd;
+      s_warp[kThreads / 32 + warp] = cs;
     }
     __syncthreads();
     uint32_t bd = total_d, bs = total_s;
-    for (int w = 0; w < warps; ++w) {
+    for (int w = 0; w < kThreads / 32; ++w) {
       if (w < warp) {
         bd += s_warp[w];
         bs += s_warp[kThreads / 32 + w];
@@ -593,13 +591,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       cum_d[b] = bd + cd;
       cum_s[b] = bs + cs;
     }
-    if (b0 + kThreads < kv.B) __syncthreads();
+    __syncthreads();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = ctl->tmem;
-  float* scratch = a.maxima + 256 * blockIdx.x;  // true maxima of a finished unit, [2][128]
+  uint32_t met = 0;  // phases of `both` seen by a softmax warp
 
   if (warp >= kLoadWarp) {
   regs_dec<kOtherRegs>();
@@ -645,8 +643,22 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == kLoadWarp) {
     // =============================================================================== load warp
 
+    int my_base = 0, my_n = 0;  // of request `lane`
+    if (in_lanes && lane < kv.B) {
+      const int L = request_len(kv, lane);
+      my_n = min(max(a.count[lane], 0), L);
+      my_base = L - my_n;
+    }
     uint32_t there;
     const uint32_t win_heads = window_heads(kv, 0, lane, &there);
+    uint32_t my_d = 0, my_s = 0;
+    if (in_lanes) {
+      const uint2 cost = line_places(my_base, my_n, W, kv.streaming != nullptr, a.sink, a.local, lane);
+      my_d = warp_scan(cost.x, lane);
+      my_s = warp_scan(cost.y, lane);
+      total_d = __shfl_sync(0xffffffffu, my_d, 31);
+      total_s = __shfl_sync(0xffffffffu, my_s, 31);
+    }
     int hd = __popc(there & ~win_heads);  // dense heads
     for (int h0 = 32; h0 < kv.Hkv; h0 += 32) {
       uint32_t t;
@@ -678,19 +690,28 @@ __global__ void __launch_bounds__(kThreads, 1)
       at.d = y / per;
       uint32_t r = y - at.d * per;
       at.h = nth_head(kv, at.win, at.d, lane, win_heads, there);
-      const uint32_t* cum = at.win ? cum_s : cum_d;
-      int lo = 0, hi = kv.B - 1;
-      while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if (cum[mid] > r)
-          hi = mid;
-        else
-          lo = mid + 1;
+      if (in_lanes) {
+        const uint32_t end = at.win ? my_s : my_d;
+        at.b = __ffs(__ballot_sync(0xffffffffu, end > r)) - 1;
+        const uint32_t before = __shfl_sync(0xffffffffu, end, max(at.b - 1, 0));
+        if (at.b > 0) r -= before;
+        at.base = __shfl_sync(0xffffffffu, my_base, at.b);
+        at.n = __shfl_sync(0xffffffffu, my_n, at.b);
+      } else {
+        const uint32_t* cum = at.win ? cum_s : cum_d;
+        int lo = 0, hi = kv.B - 1;
+        while (lo < hi) {
+          const int mid = (lo + hi) >> 1;
+          if (cum[mid] > r)
+            hi = mid;
+          else
+            lo = mid + 1;
+        }
+        at.b = lo;
+        if (lo > 0) r -= cum[lo - 1];
+        at.base = s_req[lo].x;
+        at.n = s_req[lo].y;
       }
-      at.b = lo;
-      if (lo > 0) r -= cum[lo - 1];
-      at.base = s_req[lo].x;
-      at.n = s_req[lo].y;
       for (int i0 = 0; i0 * W < at.n; i0 += 32) {
         int ns, w0;
         uint32_t cost = 0;
@@ -755,7 +776,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         un.cta0 = o0 + (boundary(o0 + 1) - item0 < snap);
         un.cta1 = o1 - (item1 - boundary(o1) < snap);
       }
-      un.slot = 2 * c + (at.k > 0 ? 0 : 1);
       un.tok0 = tok0;
       // stream 0 of a pair ends at its own last token's tile
       un.n0 = nk;
@@ -824,9 +844,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             at.h = nth_head(kv, at.win, at.d, lane, win_heads, there);
           }
-          const int L = request_len(kv, at.b);
-          at.n = min(max(a.count[at.b], 0), L);
-          at.base = L - at.n;
+          if (in_lanes) {
+            at.base = __shfl_sync(0xffffffffu, my_base, at.b);
+            at.n = __shfl_sync(0xffffffffu, my_n, at.b);
+          } else {
+            const int L = request_len(kv, at.b);
+            at.n = min(max(a.count[at.b], 0), L);
+            at.base = L - at.n;
+          }
         } while (at.n == 0);
       }
     }
@@ -899,7 +924,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int kk = 0; kk < nk; ++kk) {
             const bool more = kk + 1 < nk;
             if (!(ok = wait(&ctl->full[pv.st], pv.ph))) break;
-            if (kk == 0 && u > 0 && !(ok = wait(&ctl->ofree, (u - 1) & 1))) break;
             if (kk < n0 && !(ok = product(0, pv.st, kk > 0))) break;
             if (more) {
               if (!(ok = wait(&ctl->full[pk.st], pk.ph))) break;
@@ -931,7 +955,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int t = 0; t < 2; ++t) {
               if (kk + t >= nk) break;
               if (!(ok = wait(&ctl->full[pv.st], pv.ph))) break;
-              if (kk + t == 0 && u > 0 && !(ok = wait(&ctl->ofree, (u - 1) & 1))) break;
               if (!(ok = product(t, pv.st, kk > 0))) break;
               tc_commit(smem_u32(&ctl->empty[pv.st]));
               pv.next2();
@@ -1015,16 +1038,23 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) mbar_arrive(smem_u32(&ctl->full[st]));
     }
   }
-  } else if (warp < kOutWarp) {
+  } else {
     regs_inc<kSoftmaxRegs>();
     // ================================================================================= softmax
     const int t = warp >> 2, row = tid & 127;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + lanes + kS0 + 128 * t, tO = tmem + lanes + kO0;
     const float sc = a.scale_log2;
-    const int r_tok = row / G;
+    const int r_tok = row / G, r_head = row - r_tok * G;
+    const size_t R = a.rec_rows;
     uint32_t scnt = 0, ocnt = 0, tiles = 0;
+    int merges = 0;
     bool ok = true;
+    auto meet = [&]() {  // both warpgroups (bounded, unlike a named barrier)
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&ctl->both));
+      return warp_wait(smem_u32(&ctl->both), (met++) & 1, abort, kv.status);
+    };
     for (int u = 0; ok; ++u) {
       const int us = u & 1;
       if (!warp_wait(smem_u32(&ctl->ufull[us]), (u >> 1) & 1, abort, kv.status)) break;
@@ -1052,7 +1082,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++scnt;
         tc_fence_after();
         if (any) {
-          const uint32_t kmask = *const_cast<volatile uint32_t*>(&ctl->kmask[(tiles + kk) & 7]);
+          const uint32_t kmask = *const_cast<volatile uint8_t*>(&ctl->kmask[(tiles + kk) & 7]);
           // The maximum needs all 128 columns, the exponentials take them 32 at a time: the second
           // half is read twice, so that a thread holds 64 of them at most.
           uint32_t ra[64];
@@ -1132,184 +1162,121 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (!ok) break;
+      // ---- the unit's end: out of TMEM to the output, or to a record
+      if (nt > 0 && !(ok = warp_wait(smem_u32(&ctl->odone[t]), (ocnt + nt - 1) & 1, abort, kv.status)))
+        break;
+      tc_fence_after();
       ocnt += nt;
       tiles += nk;
-      // the unit's sums go to the epilogue, once it has taken the unit before it out
-      if (u > 0 && !(ok = warp_wait(smem_u32(&ctl->ofree), (u - 1) & 1, abort, kv.status))) break;
-      ctl->xm[t][row] = mref;
-      ctl->xl[t][row] = l;
-      __stcg(scratch + 128 * t + row, mtrue);
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(smem_u32(&ctl->sdone[t]));
-        mbar_arrive(smem_u32(&ctl->uempty[us]));
+      const bool whole = un.whole, split = un.split;
+      float w0 = 1.f, w1 = 0.f;  // weights of O_0 and O_1 where the streams shared the rows
+      if (split) {
+        ctl->xm[t][row] = mref;
+        ctl->xl[t][row] = l;
+        if (t == 1) ctl->xtrue[row] = mtrue;
+        if (!(ok = meet())) break;
+        const float ma = ctl->xm[0][row], mb = ctl->xm[1][row];
+        const float m = fmaxf(ma, mb), mz = m > -INFINITY ? m : 0.f;
+        w0 = fast_exp2((ma - mz) * sc);
+        w1 = nk > 1 ? fast_exp2((mb - mz) * sc) : 0.f;
+        l = ctl->xl[0][row] * w0 + ctl->xl[1][row] * w1;
+        if (t == 0) mtrue = fmaxf(mtrue, ctl->xtrue[row]);
+        mref = m;
       }
-    }
-  } else {
-    regs_dec<kOutRegs>();
-    // ================================================================================= epilogue
-    const int row = tid & 127;
-    const uint32_t tO = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + kO0;
-    const float sc = a.scale_log2;
-    const int r_tok = row / G, r_head = row - r_tok * G;
-    const size_t R = a.rec_rows;
-    uint32_t ocnt0 = 0, ocnt1 = 0, mcnt = 0;
-    int merges = 0;
-    bool ok = true;
-    auto meet = [&]() {  // the warpgroup (bounded, unlike a named barrier)
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&ctl->meet));
-      return warp_wait(smem_u32(&ctl->meet), (mcnt++) & 1, abort, kv.status);
-    };
-    for (int u = 0; ok; ++u) {
-      const int us = u & 1;
-      if (!warp_wait(smem_u32(&ctl->ufull[us]), (u >> 1) & 1, abort, kv.status)) break;
-      const volatile Unit& un = ctl->unit[us];
-      if (!un.valid) break;
-      const int ntok = un.ntok, whole = un.whole, nk = un.ke - un.kb;
-      // this lane's first row in the output (head 0 of its token in the unit) and in the record
-      auto out_row = [&](int my_tok) {
-        return static_cast<size_t>(un.tok0 + my_tok) * kv.Hq + un.h * G + r_head;
-      };
-      auto rec_row = [&](int my_tok) {
-        return a.records + static_cast<size_t>(un.slot) * R * kRecordFloats +
-               static_cast<size_t>(my_tok * G + r_head) * kHeadDim;
-      };
-
-      // 32 columns of this row to the output or the record
-      auto put = [&](int my_tok, float inv, int c0, const float (&o)[32]) {
-        if (whole) {
-          __nv_bfloat16* dst = a.out + out_row(my_tok) * kHeadDim + c0;
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      const int rr = my_tok * G + r_head;  // the unit's row
+      const size_t at = static_cast<size_t>(un.tok0 + my_tok) * kv.Hq + un.h * G + r_head;
+      float* rec = a.records + static_cast<size_t>(2 * blockIdx.x + (un.kb == 0)) * R * kRecordFloats;
+      if (any) {
+        // a shared row's first 64 columns are stream 0's to take out, the others stream 1's
+        const int c_beg = split ? 64 * t : 0, c_end = split ? 64 * t + 64 : 128;
+#pragma unroll 1
+        for (int c0 = c_beg; c0 < c_end; c0 += 64) {
+          uint32_t r[64];
+          if (!split) {
+            if (nt > 0) {
+              tmem_ld_64(tO + 128 * t + c0, r);
+            } else {
 #pragma unroll
-          for (int e = 0; e < 32; e += 16) {  // whole 32-byte sectors
-            uint32_t v[8];
+              for (int e = 0; e < 64; ++e) r[e] = 0;
+            }
+          } else {
+            tmem_ld_64(tO + c0, r);
 #pragma unroll
-            for (int x = 0; x < 8; ++x) v[x] = pack_bf16(o[e + 2 * x] * inv, o[e + 2 * x + 1] * inv);
-            store32(dst + e, v);
+            for (int e = 0; e < 64; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * w0);
+            if (nk > 1) {
+              uint32_t v[64];
+              tmem_ld_64(tO + 128 + c0, v);
+#pragma unroll
+              for (int e = 0; e < 64; ++e)
+                r[e] = __float_as_uint(fmaf(__uint_as_float(v[e]), w1, __uint_as_float(r[e])));
+            }
           }
-        } else {
-          float* dst = rec_row(my_tok) + c0;
+          if (live && whole) {
+            __nv_bfloat16* dst = a.out + at * kHeadDim + c0;
 #pragma unroll
-          for (int e = 0; e < 32; e += 8) {
-            uint32_t v[8];
+            for (int e = 0; e < 64; e += 16) {  // whole 32-byte sectors
+              uint32_t v[8];
 #pragma unroll
-            for (int x = 0; x < 8; ++x) v[x] = __float_as_uint(o[e + x]);
-            store32(dst + e, v);
+              for (int x = 0; x < 8; ++x)
+                v[x] = pack_bf16(__uint_as_float(r[e + 2 * x]) * inv, __uint_as_float(r[e + 2 * x + 1]) * inv);
+              store32(dst + e, v);
+            }
+          } else if (live) {
+            float* dst = rec + static_cast<size_t>(rr) * kHeadDim + c0;
+#pragma unroll
+            for (int e = 0; e < 64; e += 8) {
+              uint32_t v[8];
+#pragma unroll
+              for (int x = 0; x < 8; ++x) v[x] = r[e + x];
+              store32(dst + e, v);
+            }
           }
         }
-      };
-      // its sums (reference m, sum l relative to it, true maximum)
-      auto put_sums = [&](int my_tok, float m, float l, float mtrue) {
+      }
+      if (live && !(split && t == 1)) {
         if (whole) {
-          const size_t at = out_row(my_tok);
           if (a.m) a.m[at] = mtrue * sc * kLn2;
-          if (a.l) a.l[at] = mtrue > -INFINITY ? l * fast_exp2((m - mtrue) * sc) : l;
+          if (a.l) a.l[at] = mtrue > -INFINITY ? l * fast_exp2((mref - mtrue) * sc) : l;
         } else {
-          float* ml = a.records + static_cast<size_t>(un.slot) * R * kRecordFloats + kHeadDim * R +
-                      my_tok * G + r_head;
-          ml[0] = m;
+          float* ml = rec + kHeadDim * R + rr;
+          ml[0] = mref;
           ml[R] = l;
           ml[2 * R] = mtrue;
         }
-      };
-      auto take = [&](int t, int nt) {  // stream t's sums, and its last product
-        if (!warp_wait(smem_u32(&ctl->sdone[t]), u & 1, abort, kv.status)) return false;
-        uint32_t& done = t ? ocnt1 : ocnt0;
-        if (nt > 0 && !warp_wait(smem_u32(&ctl->odone[t]), (done + nt - 1) & 1, abort, kv.status))
-          return false;
-        done += nt;
-        tc_fence_after();
-        return true;
-      };
-      auto release = [&]() {  // accumulators and sums are read
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&ctl->ofree));
-      };
-
-      if (!un.split) {
-#pragma unroll 1
-        for (int t = 0; t < 2; ++t) {
-          const int nt = t == 0 ? un.n0 : nk;
-          if (!(ok = take(t, nt))) break;
-          const int my_tok = t * TQ + r_tok;
-          const bool live = r_tok < TQ && my_tok < ntok;
-          const float m = ctl->xm[t][row], l = ctl->xl[t][row], mtrue = __ldcg(scratch + 128 * t + row);
-          const float inv = l == 0.f ? 0.f : 1.f / l;
-#pragma unroll 1
-          for (int c0 = 0; c0 < 128; c0 += 32) {
-            uint32_t r[32];
-            if (nt > 0) tmem_ld_32(tO + 128 * t + c0, r);
-            if (t == 1 && c0 == 96) release();
-            float o[32];
-#pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = nt > 0 ? __uint_as_float(r[e]) : 0.f;
-            if (live) put(my_tok, inv, c0, o);
-          }
-          if (live) put_sums(my_tok, m, l, mtrue);
-        }
-      } else {
-        // the streams saw alternate key tiles of the same rows: joined here
-        if (!(ok = take(0, (nk + 1) / 2) && take(1, nk / 2))) break;
-        const bool live = r_tok < TQ && r_tok < ntok, any = __any_sync(0xffffffffu, live);
-        const bool two = nk > 1;
-        const float ma = ctl->xm[0][row], mb = ctl->xm[1][row];
-        const float m = fmaxf(ma, mb), mz = m > -INFINITY ? m : 0.f;
-        const float w0 = fast_exp2((ma - mz) * sc), w1 = two ? fast_exp2((mb - mz) * sc) : 0.f;
-        const float l = ctl->xl[0][row] * w0 + ctl->xl[1][row] * w1;
-        const float mtrue = fmaxf(__ldcg(scratch + row), __ldcg(scratch + 128 + row));
-        const float inv = l == 0.f ? 0.f : 1.f / l;
-#pragma unroll 1
-        for (int c0 = 0; c0 < 128; c0 += 32) {
-          float o[32];
-          if (any) {
-            uint32_t r[32];
-            tmem_ld_32(tO + c0, r);
-#pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = __uint_as_float(r[e]) * w0;
-            if (two) {
-              tmem_ld_32(tO + 128 + c0, r);
-#pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] = fmaf(__uint_as_float(r[e]), w1, o[e]);
-            }
-          }
-          if (c0 == 96) release();
-          if (live) put(r_tok, inv, c0, o);
-        }
-        if (live) put_sums(r_tok, m, l, mtrue);
       }
-      if (!ok) break;
-      if (!whole) {
-        // ---- a cut item: who takes its last ticket merges its records
+      if (split) {  // both accumulators are read before either stream's next product
+        tc_fence_before();
+        if (!(ok = meet())) break;
+      }
+      if (!whole) {  // a cut item: who takes its last ticket merges its records
         __threadfence();
         if (!(ok = meet())) break;
-        if (row == 0) {
+        if (tid == 0) {
           const int cta0 = un.cta0, parts = un.cta1 - cta0 + 1;
           __threadfence();
           const int last = atomicAdd(a.tickets + cta0, 1) == parts - 1;
           if (last) {
             a.tickets[cta0] = 0;
             __threadfence();
-            ctl->merge[merges] = {un.tok0, ntok, un.h, cta0, parts};
+            ctl->merge[merges] = {un.tok0, un.h, static_cast<uint16_t>(un.ntok), static_cast<uint16_t>(parts), cta0};
+            ++merges;
           }
-          ctl->last = last;
         }
-        if (!(ok = meet())) break;
-        merges += *const_cast<volatile int*>(&ctl->last);
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&ctl->uempty[us]));
     }
-    if (ok && row == 0) {
+    if (ok && tid == 0) {
       ctl->merges = merges;
       mbar_arrive(smem_u32(&ctl->help));
     }
     __syncwarp();
   }
-  // ---- the merges, by softmax and epilogue warps
+  // ---- the merges, by the softmax warps
   if (warp < kLoadWarp && warp_wait(smem_u32(&ctl->help), 0, abort, kv.status)) {
     const int merges = *const_cast<volatile int*>(&ctl->merges);
-    uint32_t phase[2] = {0, 0};
+    uint32_t phase[2] = {met, 0};
     for (int x = 0; x < merges; ++x)
       if (!merge_records(a, ctl->merge[x], smem, ctl, phase)) break;
   }
@@ -1328,14 +1295,13 @@ int chunk_attn_grid() {
   return sms < kChunkMaxGrid ? sms : kChunkMaxGrid;
 }
 
-// Tickets of the grid, 256 maxima per CTA, then two partial records per CTA: O [rows][128], then mref,
+// Tickets of the grid, then two partial records per CTA: O [rows][128], then mref,
 // l and mtrue of the rows.
 ChunkAttnWorkspace chunk_attn_workspace(int G, int tokens) {
   ChunkAttnWorkspace w;
   const long long rows = static_cast<long long>(tokens) * G;
   w.rows = static_cast<int>(rows < 256 ? (rows + 3) / 4 * 4 : 256);
-  w.maxima_off = kChunkMaxGrid * sizeof(int32_t);
-  w.records_off = w.maxima_off + static_cast<size_t>(chunk_attn_grid()) * 256 * sizeof(float);
+  w.records_off = kChunkMaxGrid * sizeof(int32_t);
   w.total = w.records_off +
             static_cast<size_t>(chunk_attn_grid()) * 2 * w.rows * kRecordFloats * sizeof(float);
   return w;

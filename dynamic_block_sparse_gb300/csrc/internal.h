@@ -285,12 +285,11 @@ struct ChunkAttnArgs {
   float* m;  // may be null
   float* l;  // may be null
   int32_t* tickets;  // [grid], zero on entry; left zero
-  float* maxima;     // [grid][2][128]
   float* records;    // [grid][2][rec_rows][kRecordFloats]
   int rec_rows;
 };
 struct ChunkAttnWorkspace {
-  size_t maxima_off, records_off, total;
+  size_t records_off, total;
   int rows;
 };
 ChunkAttnWorkspace chunk_attn_workspace(int G, int tokens);
