@@ -566,11 +566,19 @@ def dsa_plan_chunk(kv: PagedKV, lens_in, delta, free_pages, free_in, free_out, c
     if chunk.batch != kv.batch:
         raise ValueError(f"the chunk holds {chunk.batch} requests, the tables {kv.batch}")
     n = free_pages.numel()
+    _here(delta, "delta")
     _check("dsa_plan_chunk", load().dsa_plan_chunk(
         ctypes.byref(kv), _i32(lens_in, rows, "lens_in"), _i32(delta, rows, "delta"),
         _i32(free_pages, (n,), "free_pages"), n, _i32(free_in, (1,), "free_in"),
         _i32(free_out, (1,), "free_out"), ctypes.byref(chunk), _ptr(workspace), workspace.nbytes,
         _stream(stream)))
+
+
+def _here(t, what: str) -> None:
+    """Kernels run on the current device: a tensor of another one is refused."""
+    if t.is_cuda and t.get_device() != torch._C._cuda_getDevice():
+        raise ValueError(f"{what} is on {t.device}, the current device is "
+                         f"cuda:{torch._C._cuda_getDevice()}")
 
 
 def _token_rows(t, tokens: int, heads: int, what: str) -> int:
@@ -592,6 +600,7 @@ def dsa_append_chunk(kv: PagedKV, chunk: Chunk, k_new, v_new, rotary: Rotary | N
     and renews the metadata of every touched page in ``meta`` (if given).  ``k_new``, ``v_new`` and
     ``q`` are bf16 ``[tokens][heads][128]`` and may be slices of one projection."""
     n = chunk.tokens
+    _here(k_new, "k_new")
     if chunk.batch != kv.batch:
         raise ValueError(f"the chunk holds {chunk.batch} requests, the cache {kv.batch}")
     if rotary is not None and rotary.tokens is not None and rotary.tokens != n:
@@ -619,6 +628,7 @@ def dsa_chunk_attn(kv: PagedKV, chunk: Chunk, q, scale: float, out, m=None, l=No
     those marked streaming.  ``q`` and ``out`` bf16 ``[tokens][Hq][128]``, ``m`` and ``l`` fp32
     ``[tokens][Hq]`` or None."""
     n, hq = chunk.tokens, kv.num_q_heads
+    _here(q, "q")
     if chunk.batch != kv.batch:
         raise ValueError(f"the chunk holds {chunk.batch} requests, the cache {kv.batch}")
     for t, what in ((q, "q"), (out, "out")):

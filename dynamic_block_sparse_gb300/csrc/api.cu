@@ -1142,6 +1142,7 @@ int dsa_chunk_attn(const dsa_paged_kv* kv, const dsa_chunk* chunk, const void* q
     return fail(DSA_ERR_INVALID_ARG, "dsa_chunk_attn: NULL pointer");
   if (!aligned(q, 16) || !aligned(out, 16))
     return fail(DSA_ERR_ALIGNMENT, "q and out must be 16-byte aligned");
+  if (q == out) return fail(DSA_ERR_INVALID_ARG, "out may not be q");
   if (sink_tokens < 0 || local_tokens < 0)
     return fail(DSA_ERR_INVALID_ARG, "negative sink or local tokens");
   const float sl = scale_log2(scale);
@@ -1173,6 +1174,7 @@ int dsa_chunk_attn(const dsa_paged_kv* kv, const dsa_chunk* chunk, const void* q
   a.kv = v;
   a.start = chunk->start;
   a.count = chunk->count;
+  a.tokens = chunk->tokens;
   a.sink = sink_tokens;
   a.local = local_tokens;
   a.scale_log2 = sl;

@@ -43,7 +43,7 @@ constexpr uint32_t kTileBytes = 2 * kHalfBytes;
 // The line of work counts an item's tiles and kItemPad more, what starting and ending a unit costs;
 // and no CTA takes less than kMinWork of it: a cut costs a record, a ticket and a share of a merge,
 // about as much as four tiles.
-constexpr int kItemPad = 1, kMinWork = 5;
+constexpr int kItemPad = 3, kMinWork = 7;
 constexpr float kLazyLog2 = 8.f;  // P stays below 2^8 times its weight at the true maximum
 
 // Registers per thread of the softmax and of the other warps.  The launch has 168 x 384 = 64512, and
@@ -766,6 +766,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       un.win = at.win;
       const int tok0 = a.start[b] + at.i * W;
       un.ntok = min(W, at.n - at.i * W);
+      if (tok0 < 0 || tok0 > a.tokens - un.ntok) {  // outside the token axis: nothing is written there
+        un.ntok = tok0 < 0 ? 0 : max(a.tokens - tok0, 0);
+        if (lane == 0) raise_status(kv.status, DSA_STATUS_OVERFLOW);
+      }
       un.pos0 = at.base + at.i * W;
       un.len = len;
       un.split = un.ntok <= TQ;

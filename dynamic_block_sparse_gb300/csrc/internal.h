@@ -279,6 +279,7 @@ struct ChunkAttnArgs {
   KvView kv;
   const int32_t* start;
   const int32_t* count;
+  int tokens;
   int sink, local;  // of streaming heads
   float scale_log2;
   __nv_bfloat16* out;

@@ -121,6 +121,7 @@ class Chunk:
         self.count = torch.zeros(c.batch, **i32)
         self.row, self.pos, self.slot = (torch.full((tokens,), -1, **i32) for _ in range(3))
         self.chunk = B.chunk(self.start, self.count, self.row, self.pos, self.slot)
+        self.free_pages = self.free_count = None
         if free_pages is not None:
             # every page of the pool can come back
             self.free_pages = torch.full((max(c.num_phys_pages, free_pages.numel()),), -1, **i32)
@@ -141,6 +142,8 @@ class Chunk:
         with pages from the stack.  Advances the cache's lengths and page table and fills the chunk; a
         request that does not fit gets ``count[b] = 0`` and raises DSA_STATUS_NO_PAGES."""
         c = self.cache
+        if self.free_pages is None:
+            raise ValueError("this chunk has no stack of free pages to plan with")
         B.dsa_plan_chunk(c.kv, c.seq_lens, delta, self.free_pages, self.free_count, self.free_count,
                          self.chunk, self.plan_workspace, stream)
 

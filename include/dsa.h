@@ -603,7 +603,12 @@ int dsa_append_chunk(const dsa_paged_kv* kv, const dsa_chunk* chunk, const void*
  *               the first use (each completed call leaves the words it counts with at zero; zero-fill
  *               it again after DSA_STATUS_TIMEOUT).  Calls that share a workspace must be ordered
  *               (one stream, or captured graphs that never run at once).
- * Sums run in fp32; the probabilities are rounded to bf16 for the P.V product.
+ * Sums run in fp32; the probabilities are rounded to bf16 for the P.V product.  Values of tokens
+ * 0 .. L_b - 1 must be finite: queries are worked off in tiles against tiles of 128 keys, and a
+ * non-finite value reaches the rows of a tile that do not see it, too (0 times infinity).  Keys need
+ * not be finite, and what lies in a page behind the last token is never looked at.  A request whose
+ * tokens leave the token axis raises DSA_STATUS_OVERFLOW; what lies outside is not written.
+ * batch <= 8192; p * max_pages_per_seq <= 2^31 - 1024.
  */
 int dsa_chunk_attn(const dsa_paged_kv* kv, const dsa_chunk* chunk, const void* q,
                    int32_t sink_tokens, int32_t local_tokens, float scale, void* out, float* m,

@@ -284,6 +284,10 @@ DENSE = [
     ([(0, 700)], 16, 2, 2),
     ([(1500, 200)], 64, 6, 1),
     ([(i * 13, 1 + i % 3) for i in range(40)], 16, 4, 2),
+    ([(i % 70, (i % 5) * (i % 3)) for i in range(600)], 16, 2, 1),
+    ([(200, 40)], 32, 80, 40),
+    ([(70000, 16)], 64, 16, 1),    # 78 parts of a 256-row item
+    ([(100000, 1), (3, 1)], 64, 8, 1),
 ]
 
 
@@ -305,6 +309,7 @@ def test_chunk_attn_dense(spec, page, hq, hkv):
     ([(0, 1), (500, 1), (1000, 3)], 16, 8, 2, [1, 1]),
     ([(0, 400), (700, 130)], 64, 4, 2, [0, 1]),
     ([(333, 260)], 48, 6, 3, [1, 0, 1]),
+    ([(70, 3), (600, 1)], 16, 36, 36, [i % 3 == 1 for i in range(36)]),
 ])
 def test_chunk_attn_streaming(spec, page, hq, hkv, streaming, sink, local):
     """Streaming heads beside dense ones, windows and sinks of every relation to the lengths; a window
@@ -385,6 +390,21 @@ def test_chunk_attn_refused_requests_and_bad_pages():
                                    np.nan_to_num(V), ok, SCALE)
             check_rows((out[t0:t0 + n, hh], m[t0:t0 + n, hh], l[t0:t0 + n, hh]), ref,
                        f"request {b} head {hh}")
+
+
+def test_chunk_attn_tokens_outside_the_axis():
+    """A chunk whose arrays point behind the token axis: a status, and nothing written outside."""
+    c = ChunkCase([(40, 60), (10, 30)], 16, 4, 2, seed=8)
+    kv = B.paged_kv(c.k, c.v, c.table, c.lens, 4, None, c.status)
+    T = 70  # the axis ends inside request 1
+    big = torch.full((c.tokens, 4, 128), 5.0, dtype=torch.bfloat16, device="cuda")
+    m, l = (torch.full((c.tokens, 4), 5.0, device="cuda") for _ in range(2))
+    ws = torch.zeros(B.dsa_chunk_attn_workspace_size(kv, T), dtype=torch.uint8, device="cuda")
+    B.dsa_chunk_attn(kv, B.chunk(c.start, c.count, tokens=T), c.q[:T], SCALE, big[:T], m[:T], l[:T], ws)
+    torch.cuda.synchronize()
+    assert int(c.status) == B.DSA_STATUS_OVERFLOW
+    assert (big[T:] == 5).all() and (m[T:] == 5).all()
+    c.check(big, m, l, SCALE, requests=[0])
 
 
 def test_chunk_attn_large_logits():

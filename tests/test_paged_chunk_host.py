@@ -140,12 +140,16 @@ def test_chunk_attn_refusals(lib):
     assert call(q=None) == -1 and call(out=None) == -1
     assert call(chunk=_chunk(start=None)) == -1 and call(chunk=_chunk(count=None)) == -1
     assert call(q=4104) == -2 and call(out=8200) == -2
+    assert call(q=8192) == -1                                        # out may not be q
     assert call(sink=-1) == -1 and call(local=-1) == -1
     for bad in (0.0, -0.1, math.inf, -math.inf, math.nan, 1e-45, 3e38):
         assert call(scale=bad) == -1, bad
     assert call(ws=None) == -5 and call(ws_bytes=0) == -5 and call(ws=16392) == -2
     assert call(kv=_kv(head_dim=64)) == -3
     assert call(kv=_kv(page_size=256, max_pages_per_seq=1 << 23, batch=1)) == -3
+    assert call(kv=_kv(batch=8193)) == -3
+    # more than 2^31 key tiles, were every query at the end of its table
+    assert call(kv=_kv(page_size=256, max_pages_per_seq=1 << 22, batch=1), chunk=_chunk(1 << 20)) == -3
 
 
 def test_binding_refuses_wrong_tensors(lib):
