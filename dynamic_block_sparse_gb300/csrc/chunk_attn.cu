@@ -43,7 +43,8 @@ constexpr uint32_t kTileBytes = 2 * kHalfBytes;
 // The line of work counts an item's tiles and kItemPad more, what starting and ending a unit costs;
 // and no CTA takes less than kMinWork of it: a cut costs a record, a ticket and a share of a merge,
 // about as much as four tiles.
-constexpr int kItemPad = 3, kMinWork = 7;
+constexpr int kItemPad = 3, kMinWork = 5;
+constexpr int kWholeTiles = 20, kWholeShare = 3, kWholeEnds = 4;
 constexpr float kLazyLog2 = 8.f;  // P stays below 2^8 times its weight at the true maximum
 
 // Registers per thread of the softmax and of the other warps.  The launch has 168 x 384 = 64512, and
@@ -677,14 +678,44 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     auto boundary = [&](uint32_t c) { return c * each + min(c, more); };
     uint32_t x = boundary(c);
-    const uint32_t x1 = c < ctas ? boundary(c + 1) : x;
+    uint32_t x1 = c < ctas ? boundary(c + 1) : x;
     if (c >= ctas) x = x1;
+    // Where cuts would not pay the line is the items, one place each: CTA c takes whole ones, c first and
+    // then one a round, back and forth, each request's query tiles from the last (the largest) down.
+    // That is so when the items are of a few tiles, and when they are many and end on small ones.
+    const uint32_t my_tiles = my_n > 0 ? (my_n + W - 1) / W : 0, my_end = warp_scan(my_tiles, lane);
+    const uint32_t items = __shfl_sync(0xffffffffu, my_end, 31) * kv.Hkv;
+    int biggest = __reduce_max_sync(0xffffffffu, my_n > 0 ? (my_base + my_n - 1) / 128 + 1 : 0);
+    int ends_on = __reduce_max_sync(0xffffffffu, my_n > 0 ? (my_base + min(my_n, W) - 1) / 128 + 1 : 0);
+    if (hd == 0) {  // a streaming item is its sink and window at most
+      const int most = min(a.sink, 1 << 20) / 128 + (min(a.local, 1 << 20) + W) / 128 + 3;
+      biggest = min(biggest, most);
+      ends_on = min(ends_on, most);
+    }
+    const bool whole_items = in_lanes && (biggest <= kWholeTiles || max(biggest, kWholeEnds * ends_on) <=
+                                                                        static_cast<int>(each / kWholeShare));
+    uint32_t round = 0;
+    if (whole_items) {
+      x = c;
+      x1 = items;
+    }
     // a place on the line: head, request, query tile, key tile
     struct At {
       int win, d, h, b, i, k, base, n;
     };
     At at = {};
-    if (x < x1) {
+    auto place_item = [&]() {
+      const uint32_t tile = x / kv.Hkv;
+      at.b = __ffs(__ballot_sync(0xffffffffu, my_end > tile)) - 1;
+      at.h = static_cast<int>(x - tile * kv.Hkv);
+      at.i = static_cast<int>(__shfl_sync(0xffffffffu, my_end, at.b) - 1 - tile);
+      at.base = __shfl_sync(0xffffffffu, my_base, at.b);
+      at.n = __shfl_sync(0xffffffffu, my_n, at.b);
+      at.win = kv.streaming != nullptr && kv.streaming[at.h] != 0;
+    };
+    if (whole_items) {
+      if (x < x1) place_item();
+    } else if (x < x1) {
       at.win = x >= dense_work;
       const uint32_t per = at.win ? total_s : total_d, y = at.win ? x - dense_work : x;
       at.d = y / per;
@@ -749,7 +780,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int cnt = item_tiles(at.base, at.n, at.i, W, at.win, a.sink, a.local, &un.ns, &un.w0);
       const uint32_t item0 = x - at.k, item1 = item0 + cnt + kItemPad;
       int take = cnt;  // tiles of the item before the range's end
-      if (x1 < item1) {
+      if (x1 < item1 && !whole_items) {
         if (x1 - item0 < snap) break;  // (it begins too near the end: the next CTA's)
         if (item1 - x1 >= snap) take = min(cnt, static_cast<int>(x1 - item0));
       }
@@ -833,6 +864,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       tiles += nk;
       ++u;
       }  // (a range may begin in the pad behind an item's tiles)
+      if (whole_items) {
+        // back and forth: what a CTA gets more of in one round it gets less of in the next
+        x += ++round & 1 ? 2 * (gridDim.x - 1 - c) + 1 : 2 * c + 1;
+        if (x < x1) place_item();
+        continue;
+      }
       // the next unit starts at the next item
       x = item1;
       at.k = 0;
