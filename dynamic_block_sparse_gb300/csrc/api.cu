@@ -147,6 +147,14 @@ int query_map(const void* q, const KvView& v, int tokens, CUtensorMap* map) {
   return encode_map(map, q, 4, dims, strides, box);
 }
 
+// Positions of a request, and a tile more, count in 32 bits in the kernels of a chunk.
+int check_positions(const KvView& v) {
+  if (static_cast<long long>(v.p) * v.max_pages > (1LL << 31) - 1024)
+    return fail(DSA_ERR_UNSUPPORTED, "%d pages of %d tokens per request exceed 2^31 - 1024 tokens",
+                v.max_pages, v.p);
+  return DSA_OK;
+}
+
 int attn_stages(int page, int pages_per_cta) {
   int s = 131072 / (512 * page);
   if (s < 1) s = 1;
@@ -1014,8 +1022,8 @@ int dsa_plan_chunk(const dsa_paged_kv* kv, const int32_t* lens_in, const int32_t
     return fail(DSA_ERR_INVALID_ARG, "dsa_plan_chunk: NULL pointer");
   if (v.B > kPlanMaxBatch)
     return fail(DSA_ERR_UNSUPPORTED, "batch %d > %d", v.B, kPlanMaxBatch);
-  if (static_cast<long long>(v.B) * v.max_pages >= (1LL << 31) ||
-      static_cast<long long>(v.p) * v.max_pages >= (1LL << 31))
+  if ((rc = check_positions(v))) return rc;
+  if (static_cast<long long>(v.B) * v.max_pages >= (1LL << 31))
     return fail(DSA_ERR_UNSUPPORTED, "page table of %d x %d entries is too large", v.B, v.max_pages);
   if (!workspace || workspace_bytes < dsa_plan_chunk_workspace_size(v.B))
     return fail(DSA_ERR_WORKSPACE, "dsa_plan_chunk: workspace too small");
@@ -1055,6 +1063,7 @@ int dsa_append_chunk(const dsa_paged_kv* kv, const dsa_chunk* chunk, const void*
   if (rc) return rc;
   if (!chunk) return fail(DSA_ERR_INVALID_ARG, "chunk is NULL");
   if (chunk->tokens < 0) return fail(DSA_ERR_INVALID_ARG, "negative tokens");
+  if ((rc = check_positions(v))) return rc;
   if (chunk->tokens == 0) return ok();
   if (!chunk->start || !chunk->count || !chunk->row || !chunk->pos || !k_new || !v_new)
     return fail(DSA_ERR_INVALID_ARG, "dsa_append_chunk: NULL pointer");
@@ -1148,16 +1157,14 @@ int dsa_chunk_attn(const dsa_paged_kv* kv, const dsa_chunk* chunk, const void* q
   const float sl = scale_log2(scale);
   if (!(sl >= FLT_MIN && sl <= FLT_MAX))
     return fail(DSA_ERR_INVALID_ARG, "scale must be positive and finite");
-  if (static_cast<long long>(v.p) * v.max_pages > (1LL << 31) - 1024)
-    return fail(DSA_ERR_UNSUPPORTED, "%d pages of %d tokens per request exceed 2^31 - 1024 tokens",
-                v.max_pages, v.p);
+  if ((rc = check_positions(v))) return rc;
   if (v.B > kChunkMaxBatch)
     return fail(DSA_ERR_UNSUPPORTED, "batch %d > %d", v.B, kChunkMaxBatch);
   if (v.Hkv > kChunkMaxHeads)
     return fail(DSA_ERR_UNSUPPORTED, "%d KV heads > %d", v.Hkv, kChunkMaxHeads);
-  // key tiles of all (KV head, query tile) items, were every query at the table's end
+  // places on the line of work of all (KV head, query tile) items, were every query at the table's end
   const long long q_tiles = chunk->tokens / (2 * (128 / v.G)) + v.B;
-  const long long k_tiles = static_cast<long long>(v.p) * v.max_pages / 128 + 4;
+  const long long k_tiles = static_cast<long long>(v.p) * v.max_pages / 128 + 1 + kChunkItemPad;
   if (q_tiles * k_tiles >= (1LL << 31) / v.Hkv)
     return fail(DSA_ERR_UNSUPPORTED, "%d tokens over up to %lld positions: more than 2^31 key tiles",
                 chunk->tokens, static_cast<long long>(v.p) * v.max_pages);

@@ -43,7 +43,7 @@ constexpr uint32_t kTileBytes = 2 * kHalfBytes;
 // The line of work counts an item's tiles and kItemPad more, what starting and ending a unit costs;
 // and no CTA takes less than kMinWork of it: a cut costs a record, a ticket and a share of a merge,
 // about as much as four tiles.
-constexpr int kItemPad = 3, kMinWork = 5;
+constexpr int kItemPad = kChunkItemPad, kMinWork = 6;
 constexpr int kWholeTiles = 20, kWholeShare = 3, kWholeEnds = 4;
 constexpr float kLazyLog2 = 8.f;  // P stays below 2^8 times its weight at the true maximum
 
@@ -92,7 +92,8 @@ struct Ctl {
   int merges;
   int16_t tail_stage[4], tail_row[4];  // V tiles with rows to clear: ring stage (-1: the end), first row
   uint8_t kmask[8];  // valid 16-token groups of a key tile
-  float xm[2][128], xl[2][128], xtrue[128];  // a split unit's sums per stream and row
+  alignas(16) float xm[2][128];  // a split unit's sums per stream and row
+  float xl[2][128], xtrue[128];
 };
 constexpr uint32_t kSmemBytes = kOffCtl + sizeof(Ctl);
 static_assert(kSmemBytes <= 227 * 1024, "shared memory of one CTA");
@@ -258,6 +259,14 @@ DSA_DEV uint32_t warp_scan(uint32_t v, int lane) {
   return v;
 }
 
+// Tokens of request b before its new ones, and its new ones (cut to the token axis, which keeps the
+// line below what the host bounds it by).
+DSA_DEV int2 request_span(const ChunkAttnArgs& a, int b) {
+  const int L = request_len(a.kv, b), n = min(max(a.count[b], 0), L);
+  if (n > a.tokens) raise_status(a.kv.status, DSA_STATUS_OVERFLOW);
+  return make_int2(L - n, min(n, a.tokens));
+}
+
 // The line's places of one KV head for 32 requests, one a lane (base tokens before its n new ones):
 // dense and, where `windows`, streaming.
 DSA_DEV uint2 line_places(int base, int n, int W, bool windows, int sink, int local, int lane) {
@@ -282,6 +291,14 @@ DSA_DEV uint2 line_places(int base, int n, int W, bool windows, int sink, int lo
     if (lane == src) c = make_uint2(d, s);
   }
   return c;
+}
+
+// The sum over a warp of the larger of both kinds of places.  A line of 2^31 places or more comes of
+// counts whose sum is beyond the token axis; it is found before the 32-bit prefix sums are used.
+DSA_DEV unsigned long long line_bound(uint2 c) {
+  const uint32_t most = max(c.x, c.y);
+  return 32ull * __reduce_add_sync(0xffffffffu, most >> 5) +
+         __reduce_add_sync(0xffffffffu, most & 31u);
 }
 
 // 32 bytes in one store; 16 where the rows of the caller's tensor are not 32-byte aligned.
@@ -405,8 +422,8 @@ DSA_DEV bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort, int32
 constexpr int kMergeWarps = kLoadWarp, kMergeRows = 40, kMergeWeights = 16384;
 static_assert(kMergeWeights * 4 <= kOffRing, "the weights overlay the query tiles");
 static_assert(kMergeWarps * kMergeRows * 512 <= kRing * kTileBytes, "the rows overlay the ring");
-__device__ __noinline__ bool merge_records(const ChunkAttnArgs& a, const Merge& w, uint8_t* smem, Ctl* ctl,
-                                           uint32_t* phase) {
+__device__ __noinline__ bool merge_records(const ChunkAttnArgs& a, const Merge& w, uint8_t* smem,
+                                           Ctl* ctl, uint32_t* phase) {
   const int G = a.kv.G, rows = w.ntok * G, parts = w.parts;
   const int me = threadIdx.x, lane = me & 31, warp = me >> 5;
   const float sc = a.scale_log2;
@@ -440,8 +457,8 @@ __device__ __noinline__ bool merge_records(const ChunkAttnArgs& a, const Merge& 
         fence_proxy_async();  // the records were written, and the places read, by ordinary accesses
         mbar_arrive_expect_tx(bar, n * bytes);
         for (int q = 0; q < n; ++q)
-          bulk_load(smem_u32(place) + q * bytes, part(q0 + q) + static_cast<size_t>(r0 + b) * kHeadDim, bytes,
-                    bar);
+          bulk_load(smem_u32(place) + q * bytes,
+                    part(q0 + q) + static_cast<size_t>(r0 + b) * kHeadDim, bytes, bar);
       }
       __syncwarp();
     };
@@ -555,26 +572,25 @@ __global__ void __launch_bounds__(kThreads, 1)
   grid_dependency_wait();
 
   // ---- the line of work: prefix sums over the requests of an item row's tiles, dense and streaming
-  // (the host bounds the line by 2^31).  Up to 32 requests the load warp keeps them in its lanes;
+  // (the host bounds the line by 2^31 places).  Up to 32 requests the load warp keeps them in its lanes;
   // otherwise the whole CTA makes them in shared memory.
   uint32_t* cum_d = reinterpret_cast<uint32_t*>(smem + kOffRing);  // [B]
   uint32_t* cum_s = cum_d + kv.B;
   uint32_t* s_warp = cum_s + kv.B;  // [2][kThreads / 32]
+  unsigned long long* s_bound = reinterpret_cast<unsigned long long*>(ctl->xm);  // [kThreads / 32]
   int2* s_req = reinterpret_cast<int2*>(smem);  // [B]: tokens before the chunk, new tokens
   const bool in_lanes = kv.B <= 32;
   uint32_t total_d = 0, total_s = 0;
+  unsigned long long bound = 0;
   for (int b0 = 0; b0 < kv.B && !in_lanes; b0 += kThreads) {
     const int b = b0 + tid;
-    int n = 0, base = 0;
-    if (b < kv.B) {
-      const int L = request_len(kv, b);
-      n = min(max(a.count[b], 0), L);
-      base = L - n;
-      s_req[b] = make_int2(base, n);
-    }
-    const uint2 cost = line_places(base, n, W, kv.streaming != nullptr, a.sink, a.local, lane);
+    int2 r = make_int2(0, 0);
+    if (b < kv.B) s_req[b] = r = request_span(a, b);
+    const uint2 cost = line_places(r.x, r.y, W, kv.streaming != nullptr, a.sink, a.local, lane);
     const uint32_t cd = warp_scan(cost.x, lane), cs = warp_scan(cost.y, lane);
+    const unsigned long long most = line_bound(cost);
     if (lane == 31) {
+      s_bound[warp] = most;
       s_warp[warp] = cd;
       s_warp[kThreads / 32 + warp] = cs;
     }
@@ -585,6 +601,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         bd += s_warp[w];
         bs += s_warp[kThreads / 32 + w];
       }
+      bound += s_bound[w];
       total_d += s_warp[w];
       total_s += s_warp[kThreads / 32 + w];
     }
@@ -601,484 +618,493 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t met = 0;  // phases of `both` seen by a softmax warp
 
   if (warp >= kLoadWarp) {
-  regs_dec<kOtherRegs>();
-  const int lseg = 31 - __clz(seg), nseg = 128 >> lseg, my_seg = lane & (nseg - 1), my_half = lane / nseg;
-  const bool loads = my_half < 2;  // a lane loads one half (of the dims) of one piece of a tile
-  const uint32_t per_page = kv.p >> lseg, magic = 0xffffffffu / per_page + 1;  // pieces of a page
-  const int oob = kv.num_phys * kv.Hkv * kv.p;  // first row behind the pools: loads zeros
-  // first token of a lane's piece of list entry `list`
-  auto piece_token = [&](int list, int ns, int w0) {
-    return (list < ns ? list : w0 + list - ns) * 128 + (my_seg << lseg);
-  };
-  // its page-table entry (-2: behind the request's tokens)
-  auto piece_page = [&](int s, int b, int len) {
-    if (!loads || s >= len) return -2;
-    const uint32_t x = s >> lseg;  // below 2^27, so the product below is the exact quotient
-    const uint32_t j = per_page == 1 ? x : __umulhi(x, magic);
-    return max(kv.page_table[static_cast<size_t>(b) * kv.max_pages + j], -1);
-  };
-  // the pool row it gives (oob where there is nothing to load)
-  auto piece_row = [&](int s, int phys, int h) {
-    if (phys < 0 || phys >= kv.num_phys) return oob;
-    const uint32_t x = s >> lseg;
-    const uint32_t in_page = per_page == 1 ? 0 : x - __umulhi(x, magic) * per_page;
-    return (phys * kv.Hkv + h) * kv.p + static_cast<int>(in_page << lseg);
-  };
-  struct Place {  // of a ring position: stage, phase; K and V positions alternate
-    uint32_t st, ph;
-    DSA_DEV void next2() {
-      st += 2;
-      if (st >= kRing) {
-        st -= kRing;
-        ph ^= 1;
+    regs_dec<kOtherRegs>();
+    const int lseg = 31 - __clz(seg), nseg = 128 >> lseg;
+    const int my_seg = lane & (nseg - 1), my_half = lane / nseg;
+    const bool loads = my_half < 2;  // a lane loads one half (of the dims) of one piece of a tile
+    const uint32_t per_page = kv.p >> lseg, magic = 0xffffffffu / per_page + 1;  // pieces of a page
+    const int oob = kv.num_phys * kv.Hkv * kv.p;  // first row behind the pools: loads zeros
+    // first token of a lane's piece of list entry `list`
+    auto piece_token = [&](int list, int ns, int w0) {
+      return (list < ns ? list : w0 + list - ns) * 128 + (my_seg << lseg);
+    };
+    // its page-table entry (-2: behind the request's tokens)
+    auto piece_page = [&](int s, int b, int len) {
+      if (!loads || s >= len) return -2;
+      const uint32_t x = s >> lseg;  // below 2^27, so the product below is the exact quotient
+      const uint32_t j = per_page == 1 ? x : __umulhi(x, magic);
+      return max(kv.page_table[static_cast<size_t>(b) * kv.max_pages + j], -1);
+    };
+    // the pool row it gives (oob where there is nothing to load)
+    auto piece_row = [&](int s, int phys, int h) {
+      if (phys < 0 || phys >= kv.num_phys) return oob;
+      const uint32_t x = s >> lseg;
+      const uint32_t in_page = per_page == 1 ? 0 : x - __umulhi(x, magic) * per_page;
+      return (phys * kv.Hkv + h) * kv.p + static_cast<int>(in_page << lseg);
+    };
+    struct Place {  // of a ring position: stage, phase; K and V positions alternate
+      uint32_t st, ph;
+      DSA_DEV void next2() {
+        st += 2;
+        if (st >= kRing) {
+          st -= kRing;
+          ph ^= 1;
+        }
       }
-    }
-  };
-  auto load_pieces = [&](uint32_t st, const CUtensorMap* map, int row, uint32_t bar) {
-    if (lane == 0) mbar_arrive_expect_tx(bar, kTileBytes);
-    __syncwarp();
-    if (loads)
-      tma_load_kv(smem_base + kOffRing + st * kTileBytes + my_half * kHalfBytes + ((my_seg * 128) << lseg),
-                  map, row, my_half, bar);
-  };
-  if (warp == kLoadWarp) {
-    // =============================================================================== load warp
-
-    int my_base = 0, my_n = 0;  // of request `lane`
-    if (in_lanes && lane < kv.B) {
-      const int L = request_len(kv, lane);
-      my_n = min(max(a.count[lane], 0), L);
-      my_base = L - my_n;
-    }
-    uint32_t there;
-    const uint32_t win_heads = window_heads(kv, 0, lane, &there);
-    uint32_t my_d = 0, my_s = 0;
-    if (in_lanes) {
-      const uint2 cost = line_places(my_base, my_n, W, kv.streaming != nullptr, a.sink, a.local, lane);
-      my_d = warp_scan(cost.x, lane);
-      my_s = warp_scan(cost.y, lane);
-      total_d = __shfl_sync(0xffffffffu, my_d, 31);
-      total_s = __shfl_sync(0xffffffffu, my_s, 31);
-    }
-    int hd = __popc(there & ~win_heads);  // dense heads
-    for (int h0 = 32; h0 < kv.Hkv; h0 += 32) {
-      uint32_t t;
-      const uint32_t w = window_heads(kv, h0, lane, &t);
-      hd += __popc(t & ~w);
-    }
-    const uint32_t dense_work = hd * total_d, work = dense_work + (kv.Hkv - hd) * total_s;
-    // Equal ranges: boundary c lies at c each + min(c, more), CTA c has what lies between boundaries c
-    // and c + 1.  A boundary that would cut less than `snap` off an item's start or end moves there: a
-    // sixteenth of a range more or less against a cut's record and merge.
-    const uint32_t ctas = min(gridDim.x, (work + kMinWork - 1) / kMinWork);
-    const uint32_t each = ctas ? work / ctas : 0, more = work - each * ctas, c = blockIdx.x;
-    const uint32_t wide_end = more * (each + 1), snap = max(each / 16, 1u);
-    auto owner = [&](uint32_t at) {
-      return at < wide_end ? at / (each + 1) : more + (at - wide_end) / each;
     };
-    auto boundary = [&](uint32_t c) { return c * each + min(c, more); };
-    uint32_t x = boundary(c);
-    uint32_t x1 = c < ctas ? boundary(c + 1) : x;
-    if (c >= ctas) x = x1;
-    // Where cuts would not pay the line is the items, one place each: CTA c takes whole ones, c first and
-    // then one a round, back and forth, each request's query tiles from the last (the largest) down.
-    // That is so when the items are of a few tiles, and when they are many and end on small ones.
-    const uint32_t my_tiles = my_n > 0 ? (my_n + W - 1) / W : 0, my_end = warp_scan(my_tiles, lane);
-    const uint32_t items = __shfl_sync(0xffffffffu, my_end, 31) * kv.Hkv;
-    int biggest = __reduce_max_sync(0xffffffffu, my_n > 0 ? (my_base + my_n - 1) / 128 + 1 : 0);
-    int ends_on = __reduce_max_sync(0xffffffffu, my_n > 0 ? (my_base + min(my_n, W) - 1) / 128 + 1 : 0);
-    if (hd == 0) {  // a streaming item is its sink and window at most
-      const int most = min(a.sink, 1 << 20) / 128 + (min(a.local, 1 << 20) + W) / 128 + 3;
-      biggest = min(biggest, most);
-      ends_on = min(ends_on, most);
-    }
-    const bool whole_items = in_lanes && (biggest <= kWholeTiles || max(biggest, kWholeEnds * ends_on) <=
-                                                                        static_cast<int>(each / kWholeShare));
-    uint32_t round = 0;
-    if (whole_items) {
-      x = c;
-      x1 = items;
-    }
-    // a place on the line: head, request, query tile, key tile
-    struct At {
-      int win, d, h, b, i, k, base, n;
+    auto load_pieces = [&](uint32_t st, const CUtensorMap* map, int row, uint32_t bar) {
+      if (lane == 0) mbar_arrive_expect_tx(bar, kTileBytes);
+      __syncwarp();
+      if (loads)
+        tma_load_kv(smem_base + kOffRing + st * kTileBytes + my_half * kHalfBytes +
+                        ((my_seg * 128) << lseg),
+                    map, row, my_half, bar);
     };
-    At at = {};
-    auto place_item = [&]() {
-      const uint32_t tile = x / kv.Hkv;
-      at.b = __ffs(__ballot_sync(0xffffffffu, my_end > tile)) - 1;
-      at.h = static_cast<int>(x - tile * kv.Hkv);
-      at.i = static_cast<int>(__shfl_sync(0xffffffffu, my_end, at.b) - 1 - tile);
-      at.base = __shfl_sync(0xffffffffu, my_base, at.b);
-      at.n = __shfl_sync(0xffffffffu, my_n, at.b);
-      at.win = kv.streaming != nullptr && kv.streaming[at.h] != 0;
-    };
-    if (whole_items) {
-      if (x < x1) place_item();
-    } else if (x < x1) {
-      at.win = x >= dense_work;
-      const uint32_t per = at.win ? total_s : total_d, y = at.win ? x - dense_work : x;
-      at.d = y / per;
-      uint32_t r = y - at.d * per;
-      at.h = nth_head(kv, at.win, at.d, lane, win_heads, there);
+    if (warp == kLoadWarp) {
+      // ============================================================================= load warp
+      int my_base = 0, my_n = 0;  // of request `lane`
+      if (in_lanes && lane < kv.B) {
+        const int2 r = request_span(a, lane);
+        my_base = r.x;
+        my_n = r.y;
+      }
+      uint32_t there;
+      const uint32_t win_heads = window_heads(kv, 0, lane, &there);
+      uint32_t my_d = 0, my_s = 0;
       if (in_lanes) {
-        const uint32_t end = at.win ? my_s : my_d;
-        at.b = __ffs(__ballot_sync(0xffffffffu, end > r)) - 1;
-        const uint32_t before = __shfl_sync(0xffffffffu, end, max(at.b - 1, 0));
-        if (at.b > 0) r -= before;
+        const uint2 cost =
+            line_places(my_base, my_n, W, kv.streaming != nullptr, a.sink, a.local, lane);
+        bound = line_bound(cost);
+        my_d = warp_scan(cost.x, lane);
+        my_s = warp_scan(cost.y, lane);
+        total_d = __shfl_sync(0xffffffffu, my_d, 31);
+        total_s = __shfl_sync(0xffffffffu, my_s, 31);
+      }
+      int hd = __popc(there & ~win_heads);  // dense heads
+      for (int h0 = 32; h0 < kv.Hkv; h0 += 32) {
+        uint32_t t;
+        const uint32_t w = window_heads(kv, h0, lane, &t);
+        hd += __popc(t & ~w);
+      }
+      const bool fits = bound * kv.Hkv < 1ull << 31;
+      if (!fits && lane == 0) raise_status(kv.status, DSA_STATUS_OVERFLOW);
+      const uint32_t dense_work = hd * total_d;
+      const uint32_t work = fits ? dense_work + (kv.Hkv - hd) * total_s : 0;
+      // Equal ranges: boundary c lies at c each + min(c, more), CTA c has what lies between boundaries c
+      // and c + 1.  A boundary that would cut less than `snap` off an item's start or end moves there: a
+      // sixteenth of a range more or less against a cut's record and merge.
+      const uint32_t ctas = min(gridDim.x, (work + kMinWork - 1) / kMinWork);
+      const uint32_t each = ctas ? work / ctas : 0, more = work - each * ctas, c = blockIdx.x;
+      const uint32_t wide_end = more * (each + 1), snap = max(each / 16, 1u);
+      auto owner = [&](uint32_t at) {
+        return at < wide_end ? at / (each + 1) : more + (at - wide_end) / each;
+      };
+      auto boundary = [&](uint32_t c) { return c * each + min(c, more); };
+      uint32_t x = boundary(c);
+      uint32_t x1 = c < ctas ? boundary(c + 1) : x;
+      if (c >= ctas) x = x1;
+      // Whole items (the rule is kWholeTiles'): the line is the items, one place each, each request's
+      // query tiles from the last (the largest) down.  CTA c takes item c and then one a round, back
+      // and forth.
+      const uint32_t my_tiles = my_n > 0 ? (my_n + W - 1) / W : 0, my_end = warp_scan(my_tiles, lane);
+      const uint32_t items = __shfl_sync(0xffffffffu, my_end, 31) * kv.Hkv;
+      const int my_last = my_n > 0 ? (my_base + my_n - 1) / 128 + 1 : 0;
+      const int my_first = my_n > 0 ? (my_base + min(my_n, W) - 1) / 128 + 1 : 0;
+      int biggest = __reduce_max_sync(0xffffffffu, my_last);
+      int ends_on = __reduce_max_sync(0xffffffffu, my_first);
+      if (hd == 0) {  // a streaming item is its sink and window at most
+        const int most = min(a.sink, 1 << 20) / 128 + (min(a.local, 1 << 20) + W) / 128 + 3;
+        biggest = min(biggest, most);
+        ends_on = min(ends_on, most);
+      }
+      const int share = static_cast<int>(each / kWholeShare);
+      const bool whole_items = in_lanes && fits &&
+                               (biggest <= kWholeTiles || max(biggest, kWholeEnds * ends_on) <= share);
+      uint32_t round = 0;
+      if (whole_items) {
+        x = c;
+        x1 = items;
+      }
+      // a place on the line: head, request, query tile, key tile
+      struct At {
+        int win, d, h, b, i, k, base, n;
+      };
+      At at = {};
+      auto place_item = [&]() {
+        const uint32_t tile = x / kv.Hkv;
+        at.b = __ffs(__ballot_sync(0xffffffffu, my_end > tile)) - 1;
+        at.h = static_cast<int>(x - tile * kv.Hkv);
+        at.i = static_cast<int>(__shfl_sync(0xffffffffu, my_end, at.b) - 1 - tile);
         at.base = __shfl_sync(0xffffffffu, my_base, at.b);
         at.n = __shfl_sync(0xffffffffu, my_n, at.b);
-      } else {
-        const uint32_t* cum = at.win ? cum_s : cum_d;
-        int lo = 0, hi = kv.B - 1;
-        while (lo < hi) {
-          const int mid = (lo + hi) >> 1;
-          if (cum[mid] > r)
-            hi = mid;
-          else
-            lo = mid + 1;
-        }
-        at.b = lo;
-        if (lo > 0) r -= cum[lo - 1];
-        at.base = s_req[lo].x;
-        at.n = s_req[lo].y;
-      }
-      for (int i0 = 0; i0 * W < at.n; i0 += 32) {
-        int ns, w0;
-        uint32_t cost = 0;
-        if ((i0 + lane) * W < at.n)
-          cost = item_tiles(at.base, at.n, i0 + lane, W, at.win, a.sink, a.local, &ns, &w0) + kItemPad;
-        const uint32_t end = warp_scan(cost, lane);
-        const uint32_t above = __ballot_sync(0xffffffffu, end > r);
-        if (above) {
-          const int src = __ffs(above) - 1;
-          at.i = i0 + src;
-          const uint32_t k = r - __shfl_sync(0xffffffffu, end - cost, src);
-          const uint32_t whole = __shfl_sync(0xffffffffu, cost, src);
-          at.k = static_cast<int>(k);
-          if (k > 0 && k < snap) {
-            x -= k;
-            at.k = 0;
-          } else if (k > 0 && whole - k < snap) {
-            x += whole - k;  // nothing of it
-            at.k = static_cast<int>(whole);
-          }
-          break;
-        }
-        r -= __shfl_sync(0xffffffffu, end, 31);
-      }
-    }
-    __syncwarp();
-    fence_proxy_async_smem();  // the prefix sums are read; the ring takes their place
-
-    uint32_t tiles = 0;      // key tiles before this unit
-    Place pk = {0, 1};       // of the next K tile (a fresh barrier passes a wait for phase 1)
-    int u = 0;
-    bool ok = true;
-    while (x < x1 && ok) {
-      Unit un;
-      const int cnt = item_tiles(at.base, at.n, at.i, W, at.win, a.sink, a.local, &un.ns, &un.w0);
-      const uint32_t item0 = x - at.k, item1 = item0 + cnt + kItemPad;
-      int take = cnt;  // tiles of the item before the range's end
-      if (x1 < item1 && !whole_items) {
-        if (x1 - item0 < snap) break;  // (it begins too near the end: the next CTA's)
-        if (item1 - x1 >= snap) take = min(cnt, static_cast<int>(x1 - item0));
-      }
-      const int b = at.b, h = at.h, len = at.base + at.n;
-      if (at.k < take) {
-      un.kb = at.k;
-      un.ke = take;
-      const int nk = un.ke - un.kb;
-      int page = piece_page(piece_token(un.kb, un.ns, un.w0), b, len);
-      int page_next = nk > 1 ? piece_page(piece_token(un.kb + 1, un.ns, un.w0), b, len) : -2;
-      un.valid = 1;
-      un.b = b;
-      un.h = h;
-      un.win = at.win;
-      const int tok0 = a.start[b] + at.i * W;
-      un.ntok = min(W, at.n - at.i * W);
-      if (tok0 < 0 || tok0 > a.tokens - un.ntok) {  // outside the token axis: nothing is written there
-        un.ntok = tok0 < 0 ? 0 : max(a.tokens - tok0, 0);
-        if (lane == 0) raise_status(kv.status, DSA_STATUS_OVERFLOW);
-      }
-      un.pos0 = at.base + at.i * W;
-      un.len = len;
-      un.split = un.ntok <= TQ;
-      un.whole = un.kb == 0 && un.ke == cnt;
-      un.cta0 = un.cta1 = c;
-      if (!un.whole) {  // who has its first and its last tile
-        const uint32_t o0 = owner(item0), o1 = owner(item0 + cnt - 1);
-        un.cta0 = o0 + (boundary(o0 + 1) - item0 < snap);
-        un.cta1 = o1 - (item1 - boundary(o1) < snap);
-      }
-      un.tok0 = tok0;
-      // stream 0 of a pair ends at its own last token's tile
-      un.n0 = nk;
-      if (!un.split) {
-        const int last0 = (un.pos0 + TQ - 1) / 128;
-        const int list0 = last0 < un.w0 ? min(un.ns, last0 + 1) : un.ns + max(0, last0 - un.w0 + 1);
-        un.n0 = min(max((un.win ? list0 : last0 + 1) - un.kb, 0), nk);
-      }
-      const int us = u & 1;
-      if (u >= 2 && !warp_wait(smem_u32(&ctl->uempty[us]), ((u >> 1) - 1) & 1, abort, kv.status)) break;
-      auto publish = [&]() {
-        if (lane == 0) {
-          ctl->unit[us] = un;
-          mbar_arrive(smem_u32(&ctl->ufull[us]));
-        }
-        __syncwarp();
+        at.win = kv.streaming != nullptr && kv.streaming[at.h] != 0;
       };
-      if (u > 0) publish();  // (the first unit's loads go out before it: nothing is there to wait for)
-      if (u > 0 && !warp_wait(smem_u32(&ctl->qempty), (u - 1) & 1, abort, kv.status)) break;
-      if (lane == 0) {
-        const uint32_t bar = smem_u32(&ctl->qfull), bytes = static_cast<uint32_t>(G * TQ) * 128;
-        mbar_arrive_expect_tx(bar, (un.split ? 2 : 4) * bytes);
-        for (int t = 0; t < (un.split ? 1 : 2); ++t)
-          for (int half = 0; half < 2; ++half)
-            tma_load_q(smem_base + t * kTileBytes + half * kHalfBytes, &tmQ, h * G, un.tok0 + t * TQ, half,
-                       bar);
+      if (whole_items) {
+        if (x < x1) place_item();
+      } else if (x < x1) {
+        at.win = x >= dense_work;
+        const uint32_t per = at.win ? total_s : total_d, y = at.win ? x - dense_work : x;
+        at.d = y / per;
+        uint32_t r = y - at.d * per;
+        at.h = nth_head(kv, at.win, at.d, lane, win_heads, there);
+        if (in_lanes) {
+          const uint32_t end = at.win ? my_s : my_d;
+          at.b = __ffs(__ballot_sync(0xffffffffu, end > r)) - 1;
+          const uint32_t before = __shfl_sync(0xffffffffu, end, max(at.b - 1, 0));
+          if (at.b > 0) r -= before;
+          at.base = __shfl_sync(0xffffffffu, my_base, at.b);
+          at.n = __shfl_sync(0xffffffffu, my_n, at.b);
+        } else {
+          const uint32_t* cum = at.win ? cum_s : cum_d;
+          int lo = 0, hi = kv.B - 1;
+          while (lo < hi) {
+            const int mid = (lo + hi) >> 1;
+            if (cum[mid] > r)
+              hi = mid;
+            else
+              lo = mid + 1;
+          }
+          at.b = lo;
+          if (lo > 0) r -= cum[lo - 1];
+          at.base = s_req[lo].x;
+          at.n = s_req[lo].y;
+        }
+        for (int i0 = 0; i0 * W < at.n; i0 += 32) {
+          int ns, w0;
+          uint32_t cost = 0;
+          if ((i0 + lane) * W < at.n)
+            cost = item_tiles(at.base, at.n, i0 + lane, W, at.win, a.sink, a.local, &ns, &w0) + kItemPad;
+          const uint32_t end = warp_scan(cost, lane);
+          const uint32_t above = __ballot_sync(0xffffffffu, end > r);
+          if (above) {
+            const int src = __ffs(above) - 1;
+            at.i = i0 + src;
+            const uint32_t k = r - __shfl_sync(0xffffffffu, end - cost, src);
+            const uint32_t whole = __shfl_sync(0xffffffffu, cost, src);
+            at.k = static_cast<int>(k);
+            if (k > 0 && k < snap) {
+              x -= k;
+              at.k = 0;
+            } else if (k > 0 && whole - k < snap) {
+              x += whole - k;  // nothing of it
+              at.k = static_cast<int>(whole);
+            }
+            break;
+          }
+          r -= __shfl_sync(0xffffffffu, end, 31);
+        }
       }
       __syncwarp();
-      for (int kk = 0; kk < nk; ++kk) {
-        // page ids are read two tiles ahead of their use
-        const int page_after =
-            kk + 2 < nk ? piece_page(piece_token(un.kb + kk + 2, un.ns, un.w0), b, len) : -2;
-        const int row = piece_row(piece_token(un.kb + kk, un.ns, un.w0), page, h);
-        // the tile's valid 16-token groups, for the softmax
-        uint32_t good = 0xffu;
-        const uint32_t bad = __ballot_sync(0xffffffffu, page != -2 && row == oob) & ((1u << nseg) - 1u);
-        if (bad) {
-          for (int x = 0; x < nseg; ++x)
-            if (bad >> x & 1) good &= ~(((1u << (seg / 16)) - 1u) << (x * (seg / 16)));
-          if (lane == 0) raise_status(kv.status, DSA_STATUS_BAD_PAGE);
-        }
-        if (lane == 0) ctl->kmask[(tiles + kk) & 7] = good;
-        if (!(ok = warp_wait(smem_u32(&ctl->empty[pk.st]), pk.ph, abort, kv.status))) break;
-        load_pieces(pk.st, &tmK, row, smem_u32(&ctl->full[pk.st]));
-        if (u == 0 && kk == 0) publish();
-        pk.next2();
-        page = page_next;
-        page_next = page_after;
-      }
-      if (!ok) break;
-      tiles += nk;
-      ++u;
-      }  // (a range may begin in the pad behind an item's tiles)
-      if (whole_items) {
-        // back and forth: what a CTA gets more of in one round it gets less of in the next
-        x += ++round & 1 ? 2 * (gridDim.x - 1 - c) + 1 : 2 * c + 1;
-        if (x < x1) place_item();
-        continue;
-      }
-      // the next unit starts at the next item
-      x = item1;
-      at.k = 0;
-      if (x < x1 && ++at.i * W >= at.n) {
-        at.i = 0;
-        do {
-          if (++at.b >= kv.B) {
-            at.b = 0;
-            ++at.d;
-            if (!at.win && at.d >= hd) {
-              at.win = 1;
-              at.d = 0;
-            }
-            at.h = nth_head(kv, at.win, at.d, lane, win_heads, there);
-          }
-          if (in_lanes) {
-            at.base = __shfl_sync(0xffffffffu, my_base, at.b);
-            at.n = __shfl_sync(0xffffffffu, my_n, at.b);
-          } else {
-            const int L = request_len(kv, at.b);
-            at.n = min(max(a.count[at.b], 0), L);
-            at.base = L - at.n;
-          }
-        } while (at.n == 0);
-      }
-    }
-    if (!*abort) {
-      const int us = u & 1;
-      if (u < 2 || warp_wait(smem_u32(&ctl->uempty[us]), ((u >> 1) - 1) & 1, abort, kv.status)) {
-        if (lane == 0) {
-          ctl->unit[us].valid = 0;
-          mbar_arrive(smem_u32(&ctl->ufull[us]));
-        }
-      }
-    }
-    if (*abort) {  // loads in flight land before the CTA leaves
-      for (int t = 0; t < 64; ++t) __nanosleep(1000);
-    }
-  } else if (warp == kMmaWarp) {
-    // ============================================================================== issue warp
-    // One thread.  The tensor core takes about four products ahead of the one it works on, 256 cycles,
-    // so what lies between two groups of products has to stay below that: ring places are counted
-    // along instead of divided out, and descriptors are sums with constants.
-    if (elect_one()) {
-      auto wait = [&](const unsigned long long* bar, uint32_t parity) {
-        return mbar_wait(smem_u32(bar), parity, abort, kv.status);
-      };
-      Place pk = {0, 0}, pv = {1, 0};  // of the next K and V tile (positions alternate: K V K V ...)
-      const uint64_t dq = smem_desc(smem_base, 16), dk0 = smem_desc(smem_base + kOffRing, 16);
-      const uint64_t dv0 = smem_desc(smem_base + kOffRing, kHalfBytes);
-      constexpr uint32_t kTile16 = kTileBytes >> 4, kHalf16 = kHalfBytes >> 4;
-      uint32_t pph[2] = {0, 0};  // phases of P
+      fence_proxy_async_smem();  // the prefix sums are read; the ring takes their place
+
+      uint32_t tiles = 0;      // key tiles before this unit
+      Place pk = {0, 1};       // of the next K tile (a fresh barrier passes a wait for phase 1)
+      int u = 0;
       bool ok = true;
-      auto qk = [&](int t, uint32_t st, uint32_t q) {  // S_t = Q K^T
-        const uint64_t da = dq + q * kTile16, db = dk0 + st * kTile16;
-#pragma unroll
-        for (int ks = 0; ks < 8; ++ks) {
-          const uint32_t off = (ks >> 2) * kHalf16 + (ks & 3) * 2;
-          mma_ss(tmem + kS0 + 128 * t, da + off, db + off, ks > 0);
+      while (x < x1 && ok) {
+        Unit un;
+        const int cnt = item_tiles(at.base, at.n, at.i, W, at.win, a.sink, a.local, &un.ns, &un.w0);
+        const uint32_t item0 = x - at.k, item1 = item0 + cnt + kItemPad;
+        int take = cnt;  // tiles of the item before the range's end
+        if (x1 < item1 && !whole_items) {
+          if (x1 - item0 < snap) break;  // (it begins too near the end: the next CTA's)
+          if (item1 - x1 >= snap) take = min(cnt, static_cast<int>(x1 - item0));
         }
-        tc_commit(smem_u32(&ctl->sfull[t]));
-      };
-      auto product = [&](int t, uint32_t st, uint32_t acc) {  // O_t += P V, as P's halves arrive
-        const uint64_t db = dv0 + st * kTile16;
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          if (!wait(&ctl->pready[t][half], pph[t])) return false;
-          tc_fence_after();
-#pragma unroll
-          for (int ks = 4 * half; ks < 4 * half + 4; ++ks)
-            mma_ts(tmem + kO0 + 128 * t, tmem + kS0 + 128 * t + 8 * ks, db + ks * (2048 >> 4),
-                   ks > 0 ? 1 : acc);
-        }
-        pph[t] ^= 1;
-        tc_commit(smem_u32(&ctl->odone[t]));
-        return true;
-      };
-      for (int u = 0; ok; ++u) {
-        const int us = u & 1;
-        if (!wait(&ctl->ufull[us], (u >> 1) & 1)) break;
-        const Unit& un = ctl->unit[us];
-        const int nk = un.ke - un.kb, n0 = un.n0, split = un.split, valid = un.valid;
-        mbar_arrive(smem_u32(&ctl->uempty[us]));
-        if (!valid) break;
-        if (!wait(&ctl->qfull, u & 1)) break;
-        if (!(ok = wait(&ctl->full[pk.st], pk.ph))) break;
-        if (!split) {
-          if (n0 > 0) qk(0, pk.st, 0);
-          qk(1, pk.st, 1);
-          tc_commit(smem_u32(&ctl->empty[pk.st]));
-          if (nk == 1) tc_commit(smem_u32(&ctl->qempty));
-          pk.next2();
+        const int b = at.b, h = at.h, len = at.base + at.n;
+        if (at.k < take) {
+          un.kb = at.k;
+          un.ke = take;
+          const int nk = un.ke - un.kb;
+          int page = piece_page(piece_token(un.kb, un.ns, un.w0), b, len);
+          int page_next = nk > 1 ? piece_page(piece_token(un.kb + 1, un.ns, un.w0), b, len) : -2;
+          un.valid = 1;
+          un.b = b;
+          un.h = h;
+          un.win = at.win;
+          const int tok0 = a.start[b] + at.i * W;
+          un.ntok = min(W, at.n - at.i * W);
+          if (tok0 < 0 || tok0 > a.tokens - un.ntok) {  // outside the token axis: nothing is written there
+            un.ntok = tok0 < 0 ? 0 : max(a.tokens - tok0, 0);
+            if (lane == 0) raise_status(kv.status, DSA_STATUS_OVERFLOW);
+          }
+          un.pos0 = at.base + at.i * W;
+          un.len = len;
+          un.split = un.ntok <= TQ;
+          un.whole = un.kb == 0 && un.ke == cnt;
+          un.cta0 = un.cta1 = c;
+          if (!un.whole) {  // who has its first and its last tile
+            const uint32_t o0 = owner(item0), o1 = owner(item0 + cnt - 1);
+            un.cta0 = o0 + (boundary(o0 + 1) - item0 < snap);
+            un.cta1 = o1 - (item1 - boundary(o1) < snap);
+          }
+          un.tok0 = tok0;
+          // stream 0 of a pair ends at its own last token's tile
+          un.n0 = nk;
+          if (!un.split) {
+            const int last0 = (un.pos0 + TQ - 1) / 128;
+            const int list0 = last0 < un.w0 ? min(un.ns, last0 + 1) : un.ns + max(0, last0 - un.w0 + 1);
+            un.n0 = min(max((un.win ? list0 : last0 + 1) - un.kb, 0), nk);
+          }
+          const int us = u & 1;
+          if (u >= 2 && !warp_wait(smem_u32(&ctl->uempty[us]), ((u >> 1) - 1) & 1, abort, kv.status)) break;
+          auto publish = [&]() {
+            if (lane == 0) {
+              ctl->unit[us] = un;
+              mbar_arrive(smem_u32(&ctl->ufull[us]));
+            }
+            __syncwarp();
+          };
+          if (u > 0) publish();  // (the first unit's loads go out before it: nothing is there to wait for)
+          if (u > 0 && !warp_wait(smem_u32(&ctl->qempty), (u - 1) & 1, abort, kv.status)) break;
+          if (lane == 0) {
+            const uint32_t bar = smem_u32(&ctl->qfull), bytes = static_cast<uint32_t>(G * TQ) * 128;
+            mbar_arrive_expect_tx(bar, (un.split ? 2 : 4) * bytes);
+            for (int t = 0; t < (un.split ? 1 : 2); ++t)
+              for (int half = 0; half < 2; ++half)
+                tma_load_q(smem_base + t * kTileBytes + half * kHalfBytes, &tmQ, h * G, un.tok0 + t * TQ, half,
+                           bar);
+          }
+          __syncwarp();
           for (int kk = 0; kk < nk; ++kk) {
-            const bool more = kk + 1 < nk;
-            if (!(ok = wait(&ctl->full[pv.st], pv.ph))) break;
-            if (kk < n0 && !(ok = product(0, pv.st, kk > 0))) break;
-            if (more) {
-              if (!(ok = wait(&ctl->full[pk.st], pk.ph))) break;
-              if (kk + 1 < n0) qk(0, pk.st, 0);
+            // page ids are read two tiles ahead of their use
+            const int page_after =
+                kk + 2 < nk ? piece_page(piece_token(un.kb + kk + 2, un.ns, un.w0), b, len) : -2;
+            const int row = piece_row(piece_token(un.kb + kk, un.ns, un.w0), page, h);
+            // the tile's valid 16-token groups, for the softmax
+            uint32_t good = 0xffu;
+            const uint32_t bad = __ballot_sync(0xffffffffu, page != -2 && row == oob) & ((1u << nseg) - 1u);
+            if (bad) {
+              for (int x = 0; x < nseg; ++x)
+                if (bad >> x & 1) good &= ~(((1u << (seg / 16)) - 1u) << (x * (seg / 16)));
+              if (lane == 0) raise_status(kv.status, DSA_STATUS_BAD_PAGE);
             }
-            if (!(ok = product(1, pv.st, kk > 0))) break;
-            tc_commit(smem_u32(&ctl->empty[pv.st]));
-            pv.next2();
-            if (more) {
-              qk(1, pk.st, 1);
-              tc_commit(smem_u32(&ctl->empty[pk.st]));
-              if (kk + 2 == nk) tc_commit(smem_u32(&ctl->qempty));
-              pk.next2();
-            }
-          }
-        } else {
-          qk(0, pk.st, 0);
-          tc_commit(smem_u32(&ctl->empty[pk.st]));
-          pk.next2();
-          if (nk > 1) {
-            if (!(ok = wait(&ctl->full[pk.st], pk.ph))) break;
-            qk(1, pk.st, 0);
-            tc_commit(smem_u32(&ctl->empty[pk.st]));
+            if (lane == 0) ctl->kmask[(tiles + kk) & 7] = good;
+            if (!(ok = warp_wait(smem_u32(&ctl->empty[pk.st]), pk.ph, abort, kv.status))) break;
+            load_pieces(pk.st, &tmK, row, smem_u32(&ctl->full[pk.st]));
+            if (u == 0 && kk == 0) publish();
             pk.next2();
+            page = page_next;
+            page_next = page_after;
           }
-          if (nk <= 2) tc_commit(smem_u32(&ctl->qempty));
-          for (int kk = 0; kk < nk; kk += 2) {
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-              if (kk + t >= nk) break;
+          if (!ok) break;
+          tiles += nk;
+          ++u;
+        }  // (a range may begin in the pad behind an item's tiles)
+        if (whole_items) {
+          // back and forth: what a CTA gets more of in one round it gets less of in the next
+          x += ++round & 1 ? 2 * (gridDim.x - 1 - c) + 1 : 2 * c + 1;
+          if (x < x1) place_item();
+          continue;
+        }
+        // the next unit starts at the next item
+        x = item1;
+        at.k = 0;
+        if (x < x1 && ++at.i * W >= at.n) {
+          at.i = 0;
+          do {
+            if (++at.b >= kv.B) {
+              at.b = 0;
+              ++at.d;
+              if (!at.win && at.d >= hd) {
+                at.win = 1;
+                at.d = 0;
+              }
+              at.h = nth_head(kv, at.win, at.d, lane, win_heads, there);
+            }
+            if (in_lanes) {
+              at.base = __shfl_sync(0xffffffffu, my_base, at.b);
+              at.n = __shfl_sync(0xffffffffu, my_n, at.b);
+            } else {
+              const int2 r = request_span(a, at.b);
+              at.base = r.x;
+              at.n = r.y;
+            }
+          } while (at.n == 0);
+        }
+      }
+      if (!*abort) {
+        const int us = u & 1;
+        if (u < 2 || warp_wait(smem_u32(&ctl->uempty[us]), ((u >> 1) - 1) & 1, abort, kv.status)) {
+          if (lane == 0) {
+            ctl->unit[us].valid = 0;
+            mbar_arrive(smem_u32(&ctl->ufull[us]));
+          }
+        }
+      }
+      if (*abort) {  // loads in flight land before the CTA leaves
+        for (int t = 0; t < 64; ++t) __nanosleep(1000);
+      }
+    } else if (warp == kMmaWarp) {
+      // ============================================================================ issue warp
+      // One thread.  The tensor core takes about four products ahead of the one it works on, 256 cycles,
+      // so what lies between two groups of products has to stay below that: ring places are counted
+      // along instead of divided out, and descriptors are sums with constants.
+      if (elect_one()) {
+        auto wait = [&](const unsigned long long* bar, uint32_t parity) {
+          return mbar_wait(smem_u32(bar), parity, abort, kv.status);
+        };
+        Place pk = {0, 0}, pv = {1, 0};  // of the next K and V tile (positions alternate: K V K V ...)
+        const uint64_t dq = smem_desc(smem_base, 16), dk0 = smem_desc(smem_base + kOffRing, 16);
+        const uint64_t dv0 = smem_desc(smem_base + kOffRing, kHalfBytes);
+        constexpr uint32_t kTile16 = kTileBytes >> 4, kHalf16 = kHalfBytes >> 4;
+        uint32_t pph[2] = {0, 0};  // phases of P
+        bool ok = true;
+        auto qk = [&](int t, uint32_t st, uint32_t q) {  // S_t = Q K^T
+          const uint64_t da = dq + q * kTile16, db = dk0 + st * kTile16;
+  #pragma unroll
+          for (int ks = 0; ks < 8; ++ks) {
+            const uint32_t off = (ks >> 2) * kHalf16 + (ks & 3) * 2;
+            mma_ss(tmem + kS0 + 128 * t, da + off, db + off, ks > 0);
+          }
+          tc_commit(smem_u32(&ctl->sfull[t]));
+        };
+        auto product = [&](int t, uint32_t st, uint32_t acc) {  // O_t += P V, as P's halves arrive
+          const uint64_t db = dv0 + st * kTile16;
+  #pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            if (!wait(&ctl->pready[t][half], pph[t])) return false;
+            tc_fence_after();
+  #pragma unroll
+            for (int ks = 4 * half; ks < 4 * half + 4; ++ks)
+              mma_ts(tmem + kO0 + 128 * t, tmem + kS0 + 128 * t + 8 * ks, db + ks * (2048 >> 4),
+                     ks > 0 ? 1 : acc);
+          }
+          pph[t] ^= 1;
+          tc_commit(smem_u32(&ctl->odone[t]));
+          return true;
+        };
+        for (int u = 0; ok; ++u) {
+          const int us = u & 1;
+          if (!wait(&ctl->ufull[us], (u >> 1) & 1)) break;
+          const Unit& un = ctl->unit[us];
+          const int nk = un.ke - un.kb, n0 = un.n0, split = un.split, valid = un.valid;
+          mbar_arrive(smem_u32(&ctl->uempty[us]));
+          if (!valid) break;
+          if (!wait(&ctl->qfull, u & 1)) break;
+          if (!(ok = wait(&ctl->full[pk.st], pk.ph))) break;
+          if (!split) {
+            if (n0 > 0) qk(0, pk.st, 0);
+            qk(1, pk.st, 1);
+            tc_commit(smem_u32(&ctl->empty[pk.st]));
+            if (nk == 1) tc_commit(smem_u32(&ctl->qempty));
+            pk.next2();
+            for (int kk = 0; kk < nk; ++kk) {
+              const bool more = kk + 1 < nk;
               if (!(ok = wait(&ctl->full[pv.st], pv.ph))) break;
-              if (!(ok = product(t, pv.st, kk > 0))) break;
+              if (kk < n0 && !(ok = product(0, pv.st, kk > 0))) break;
+              if (more) {
+                if (!(ok = wait(&ctl->full[pk.st], pk.ph))) break;
+                if (kk + 1 < n0) qk(0, pk.st, 0);
+              }
+              if (!(ok = product(1, pv.st, kk > 0))) break;
               tc_commit(smem_u32(&ctl->empty[pv.st]));
               pv.next2();
-              if (kk + t + 2 < nk) {
-                if (!(ok = wait(&ctl->full[pk.st], pk.ph))) break;
-                qk(t, pk.st, 0);
+              if (more) {
+                qk(1, pk.st, 1);
                 tc_commit(smem_u32(&ctl->empty[pk.st]));
-                if (kk + t + 3 == nk) tc_commit(smem_u32(&ctl->qempty));
+                if (kk + 2 == nk) tc_commit(smem_u32(&ctl->qempty));
                 pk.next2();
               }
             }
-            if (!ok) break;
+          } else {
+            qk(0, pk.st, 0);
+            tc_commit(smem_u32(&ctl->empty[pk.st]));
+            pk.next2();
+            if (nk > 1) {
+              if (!(ok = wait(&ctl->full[pk.st], pk.ph))) break;
+              qk(1, pk.st, 0);
+              tc_commit(smem_u32(&ctl->empty[pk.st]));
+              pk.next2();
+            }
+            if (nk <= 2) tc_commit(smem_u32(&ctl->qempty));
+            for (int kk = 0; kk < nk; kk += 2) {
+  #pragma unroll
+              for (int t = 0; t < 2; ++t) {
+                if (kk + t >= nk) break;
+                if (!(ok = wait(&ctl->full[pv.st], pv.ph))) break;
+                if (!(ok = product(t, pv.st, kk > 0))) break;
+                tc_commit(smem_u32(&ctl->empty[pv.st]));
+                pv.next2();
+                if (kk + t + 2 < nk) {
+                  if (!(ok = wait(&ctl->full[pk.st], pk.ph))) break;
+                  qk(t, pk.st, 0);
+                  tc_commit(smem_u32(&ctl->empty[pk.st]));
+                  if (kk + t + 3 == nk) tc_commit(smem_u32(&ctl->qempty));
+                  pk.next2();
+                }
+              }
+              if (!ok) break;
+            }
           }
         }
+        if (*abort)  // products in flight end before TMEM is freed
+          for (int t = 0; t < 64; ++t) __nanosleep(1000);
       }
-      if (*abort)  // products in flight end before TMEM is freed
-        for (int t = 0; t < 64; ++t) __nanosleep(1000);
-    }
-    __syncwarp();
-  } else if (warp == kValueWarp) {
-    // ============================================================================== value warp
-    Place pv = {1, 1};
-    uint32_t tails = 0;  // tiles handed to the tail warp
-    bool ok = true;
-    for (int u = 0; ok; ++u) {
-      const int us = u & 1;
-      if (!warp_wait(smem_u32(&ctl->ufull[us]), (u >> 1) & 1, abort, kv.status)) break;
-      const Unit& in = ctl->unit[us];
-      const int valid = in.valid, b = in.b, h = in.h, len = in.len, kb = in.kb, ke = in.ke, ns = in.ns,
-                w0 = in.w0;
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&ctl->uempty[us]));
-      if (!valid) {
-        if (lane == 0) {
-          ctl->tail_stage[tails & 3] = -1;
-          mbar_arrive(smem_u32(&ctl->tail[tails & 3]));
-        }
-        break;
-      }
-      int page = piece_page(piece_token(kb, ns, w0), b, len);
-      int page_next = kb + 1 < ke ? piece_page(piece_token(kb + 1, ns, w0), b, len) : -2;
-      for (int k = kb; k < ke; ++k) {
-        const int page_after = k + 2 < ke ? piece_page(piece_token(k + 2, ns, w0), b, len) : -2;
-        const int s = piece_token(k, ns, w0), row = piece_row(s, page, h);
-        if (!(ok = warp_wait(smem_u32(&ctl->empty[pv.st]), pv.ph, abort, kv.status))) break;
-        // Rows behind the request's last token share its page: whatever they hold must not reach the
-        // product, where it would meet P = 0 (pieces wholly behind it are loaded as zeros).  Such a
-        // tile completes on a tail barrier, and the tail warp fills the stage's own barrier when
-        // they are cleared.
-        const int left = len - (s - (my_seg << lseg));
-        uint32_t bar = smem_u32(&ctl->full[pv.st]);
-        if (left < 128 && (left & (seg - 1)) != 0) {
-          bar = smem_u32(&ctl->tail[tails & 3]);
+    } else if (warp == kValueWarp) {
+      // ============================================================================ value warp
+      Place pv = {1, 1};
+      uint32_t tails = 0;  // tiles handed to the tail warp
+      bool ok = true;
+      for (int u = 0; ok; ++u) {
+        const int us = u & 1;
+        if (!warp_wait(smem_u32(&ctl->ufull[us]), (u >> 1) & 1, abort, kv.status)) break;
+        const Unit& in = ctl->unit[us];
+        const int valid = in.valid, b = in.b, h = in.h, len = in.len, kb = in.kb, ke = in.ke, ns = in.ns,
+                  w0 = in.w0;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&ctl->uempty[us]));
+        if (!valid) {
           if (lane == 0) {
-            ctl->tail_stage[tails & 3] = pv.st;
-            ctl->tail_row[tails & 3] = left;
+            ctl->tail_stage[tails & 3] = -1;
+            mbar_arrive(smem_u32(&ctl->tail[tails & 3]));
           }
-          ++tails;
+          break;
         }
-        load_pieces(pv.st, &tmV, row, bar);
-        pv.next2();
-        page = page_next;
-        page_next = page_after;
+        int page = piece_page(piece_token(kb, ns, w0), b, len);
+        int page_next = kb + 1 < ke ? piece_page(piece_token(kb + 1, ns, w0), b, len) : -2;
+        for (int k = kb; k < ke; ++k) {
+          const int page_after = k + 2 < ke ? piece_page(piece_token(k + 2, ns, w0), b, len) : -2;
+          const int s = piece_token(k, ns, w0), row = piece_row(s, page, h);
+          if (!(ok = warp_wait(smem_u32(&ctl->empty[pv.st]), pv.ph, abort, kv.status))) break;
+          // Rows behind the request's last token share its page: whatever they hold must not reach the
+          // product, where it would meet P = 0 (pieces wholly behind it are loaded as zeros).  Such a
+          // tile completes on a tail barrier, and the tail warp fills the stage's own barrier when
+          // they are cleared.
+          const int left = len - (s - (my_seg << lseg));
+          uint32_t bar = smem_u32(&ctl->full[pv.st]);
+          if (left < 128 && (left & (seg - 1)) != 0) {
+            bar = smem_u32(&ctl->tail[tails & 3]);
+            if (lane == 0) {
+              ctl->tail_stage[tails & 3] = pv.st;
+              ctl->tail_row[tails & 3] = left;
+            }
+            ++tails;
+          }
+          load_pieces(pv.st, &tmV, row, bar);
+          pv.next2();
+          page = page_next;
+          page_next = page_after;
+        }
+      }
+      if (*abort)  // loads in flight land before the CTA leaves
+        for (int t = 0; t < 64; ++t) __nanosleep(1000);
+    } else if (warp == kTailWarp) {
+      // ============================================================================= tail warp
+      for (uint32_t x = 0;; ++x) {
+        if (!warp_wait(smem_u32(&ctl->tail[x & 3]), (x >> 2) & 1, abort, kv.status)) break;
+        const int st = ctl->tail_stage[x & 3], r0 = ctl->tail_row[x & 3];
+        if (st < 0) break;
+        uint8_t* tile = smem + kOffRing + st * kTileBytes;
+        const int rows = seg - r0 % seg;
+        for (int e = lane; e < rows * 16; e += 32)
+          *reinterpret_cast<uint4*>(tile + ((e >> 3) & 1) * kHalfBytes + (r0 + (e >> 4)) * 128 +
+                                    (e & 7) * 16) = make_uint4(0, 0, 0, 0);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&ctl->full[st]));
       }
     }
-    if (*abort)  // loads in flight land before the CTA leaves
-      for (int t = 0; t < 64; ++t) __nanosleep(1000);
-  } else if (warp == kTailWarp) {
-    // =============================================================================== tail warp
-    for (uint32_t x = 0;; ++x) {
-      if (!warp_wait(smem_u32(&ctl->tail[x & 3]), (x >> 2) & 1, abort, kv.status)) break;
-      const int st = ctl->tail_stage[x & 3], r0 = ctl->tail_row[x & 3];
-      if (st < 0) break;
-      uint8_t* tile = smem + kOffRing + st * kTileBytes;
-      const int rows = seg - r0 % seg;
-      for (int e = lane; e < rows * 16; e += 32)
-        *reinterpret_cast<uint4*>(tile + ((e >> 3) & 1) * kHalfBytes + (r0 + (e >> 4)) * 128 +
-                                  (e & 7) * 16) = make_uint4(0, 0, 0, 0);
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&ctl->full[st]));
-    }
-  }
   } else {
     regs_inc<kSoftmaxRegs>();
     // ================================================================================= softmax
@@ -1263,7 +1289,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               uint32_t v[8];
 #pragma unroll
               for (int x = 0; x < 8; ++x)
-                v[x] = pack_bf16(__uint_as_float(r[e + 2 * x]) * inv, __uint_as_float(r[e + 2 * x + 1]) * inv);
+                v[x] = pack_bf16(__uint_as_float(r[e + 2 * x]) * inv,
+                                 __uint_as_float(r[e + 2 * x + 1]) * inv);
               store32(dst + e, v);
             }
           } else if (live) {
@@ -1303,7 +1330,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (last) {
             a.tickets[cta0] = 0;
             __threadfence();
-            ctl->merge[merges] = {un.tok0, un.h, static_cast<uint16_t>(un.ntok), static_cast<uint16_t>(parts), cta0};
+            ctl->merge[merges] = {un.tok0, un.h, static_cast<uint16_t>(un.ntok),
+                                  static_cast<uint16_t>(parts), cta0};
             ++merges;
           }
         }

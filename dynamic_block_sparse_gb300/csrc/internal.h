@@ -273,6 +273,7 @@ cudaError_t launch_append_chunk(const AppendArgs& a, int kind, cudaStream_t s);
 
 // Attention of a chunk over the paged cache (chunk_attn.cu).
 constexpr int kChunkMaxBatch = 8192;  // requests whose prefix sums one CTA keeps in shared memory
+constexpr int kChunkItemPad = 4;  // places of the line that an item takes besides its tiles
 constexpr int kChunkMaxGrid = 512;
 constexpr int kChunkMaxHeads = 65536;
 struct ChunkAttnArgs {

@@ -537,7 +537,9 @@ typedef struct dsa_chunk {
  *                of this step expect.  Table entries behind a shortened request keep their old ids.
  *   workspace  : dsa_plan_chunk_workspace_size(B) bytes, ZERO-FILLED before the first use (each
  *                completed call leaves it zero-filled).
- * batch <= 8192.
+ * The metadata of the page that now ends a shortened request still covers the dropped tokens (a
+ * looser bound, a mean with them) until tokens are appended to it.
+ * batch <= 8192; p * max_pages_per_seq <= 2^31 - 1024.
  */
 int dsa_plan_chunk(const dsa_paged_kv* kv, const int32_t* lens_in, const int32_t* delta,
                    int32_t* free_pages, int32_t free_capacity, const int32_t* free_in,
@@ -582,6 +584,7 @@ typedef struct dsa_rotary {
  *                  it twice; the KV write repeats harmlessly).
  * Nothing is written for tokens with row -1 and those behind start[B].  A token on a bad page
  * id is skipped (its query is still turned) and raises DSA_STATUS_BAD_PAGE.
+ * p * max_pages_per_seq <= 2^31 - 1024.
  */
 int dsa_append_chunk(const dsa_paged_kv* kv, const dsa_chunk* chunk, const void* k_new,
                      int64_t k_stride, const void* v_new, int64_t v_stride,
@@ -607,7 +610,8 @@ int dsa_append_chunk(const dsa_paged_kv* kv, const dsa_chunk* chunk, const void*
  * 0 .. L_b - 1 must be finite: queries are worked off in tiles against tiles of 128 keys, and a
  * non-finite value reaches the rows of a tile that do not see it, too (0 times infinity).  Keys need
  * not be finite, and what lies in a page behind the last token is never looked at.  A request whose
- * tokens leave the token axis raises DSA_STATUS_OVERFLOW; what lies outside is not written.
+ * tokens leave the token axis raises DSA_STATUS_OVERFLOW; what lies outside is not written, and nothing
+ * at all is where the counts together lie so far beyond it that the work no longer counts in 31 bits.
  * batch <= 8192; p * max_pages_per_seq <= 2^31 - 1024.
  */
 int dsa_chunk_attn(const dsa_paged_kv* kv, const dsa_chunk* chunk, const void* q,

@@ -407,6 +407,57 @@ def test_chunk_attn_tokens_outside_the_axis():
     c.check(big, m, l, SCALE, requests=[0])
 
 
+def test_chunk_attn_count_beyond_the_axis():
+    """A request with more tokens than the axis: a status, and the rows that are there are right."""
+    c = ChunkCase([(40, 90)], 16, 4, 2, seed=9)
+    kv = B.paged_kv(c.k, c.v, c.table, c.lens, 4, None, c.status)
+    T = 70
+    big = torch.full((c.tokens, 4, 128), 5.0, dtype=torch.bfloat16, device="cuda")
+    m, l = (torch.full((c.tokens, 4), 5.0, device="cuda") for _ in range(2))
+    ws = torch.zeros(B.dsa_chunk_attn_workspace_size(kv, T), dtype=torch.uint8, device="cuda")
+    B.dsa_chunk_attn(kv, B.chunk(c.start, c.count, tokens=T), c.q[:T], SCALE, big[:T], m[:T], l[:T], ws)
+    torch.cuda.synchronize()
+    assert int(c.status) == B.DSA_STATUS_OVERFLOW
+    assert (big[T:] == 5).all() and (m[T:] == 5).all()
+    c.spec[0] = (40, T)
+    c.check(big, m, l, SCALE)
+
+
+@pytest.mark.parametrize("batch", [16, 40])
+def test_chunk_attn_counts_far_beyond_the_axis(batch):
+    """Requests that each claim the whole axis, over tables of 2^30 positions: more key tiles than 32
+    bits count.  A status, and nothing is written."""
+    T, pages = 48000, 1 << 22
+    table = torch.full((batch, pages), -1, dtype=torch.int32, device="cuda")
+    pool = torch.zeros(4, 1, 256, 128, dtype=torch.bfloat16, device="cuda")
+    lens = torch.full((batch,), 1 << 30, dtype=torch.int32, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    kv = B.paged_kv(pool, pool, table, lens, 1, None, status)
+    start = torch.zeros(batch + 1, dtype=torch.int32, device="cuda")
+    count = torch.full((batch,), T, dtype=torch.int32, device="cuda")
+    q = torch.zeros(T, 1, 128, dtype=torch.bfloat16, device="cuda")
+    out, m, l = torch.full_like(q, 5), *(torch.full((T, 1), 5.0, device="cuda") for _ in range(2))
+    ws = torch.zeros(B.dsa_chunk_attn_workspace_size(kv, T), dtype=torch.uint8, device="cuda")
+    B.dsa_chunk_attn(kv, B.chunk(start, count, tokens=T), q, SCALE, out, m, l, ws)
+    torch.cuda.synchronize()
+    assert int(status) == B.DSA_STATUS_OVERFLOW
+    assert (out == 5).all() and (m == 5).all() and (l == 5).all() and not ws.any()
+
+
+def test_chunk_attn_many_whole_items():
+    """One prompt of many heads of their own: several whole items a CTA, of 2 to 22 key tiles."""
+    n, heads = 2700, 64
+    c = ChunkCase([(0, n)], 64, heads, heads, seed=10)
+    out, m, l = _attend(c, SCALE)
+    torch.cuda.synchronize()
+    from chunk_support import attend_reference, check_rows, visible
+    ok = visible(np.arange(n), n, None)
+    for h in (0, 17, 63):
+        ref = attend_reference(c.q[:, h].double().cpu().numpy(), c.rows(c.k, 0, h),
+                               c.rows(c.v, 0, h), ok, SCALE)
+        check_rows((out[:, h], m[:, h], l[:, h]), ref, f"head {h}")
+
+
 def test_chunk_attn_large_logits():
     """Logits of several hundred, growing along the sequence (the running maximum moves at every tile)
     and falling (it never moves)."""

@@ -84,6 +84,7 @@ def test_plan_chunk_refusals(lib):
     assert call(kv=_kv(batch=8193)) == -3 and b"8193" in lib.dsa_last_error()
     assert call(kv=_kv(batch=8192, max_pages_per_seq=1 << 19)) == -3
     assert call(kv=_kv(page_size=256, max_pages_per_seq=1 << 23, batch=1)) == -3
+    assert call(kv=_kv(page_size=256, max_pages_per_seq=(1 << 23) - 1, batch=1)) == -3
     assert call(ws=None) == -5
     assert call(ws_bytes=8) == -5
     assert call(ws=8200) == -2
