@@ -44,7 +44,8 @@ constexpr uint32_t kTileBytes = 2 * kHalfBytes;
 // and no CTA takes less than kMinWork of it: a cut costs a record, a ticket and a share of a merge,
 // about as much as four tiles.
 constexpr int kItemPad = kChunkItemPad, kMinWork = 6;
-constexpr int kWholeTiles = 20, kWholeShare = 3, kWholeEnds = 4;
+constexpr int kWholeTiles = 20, kWholeRounds = 12, kWholeShare = 3, kWholeEnds = 4;
+constexpr int kWholeBatch = 1024;
 constexpr float kLazyLog2 = 8.f;  // P stays below 2^8 times its weight at the true maximum
 
 // Registers per thread of the softmax and of the other warps.  The launch has 168 x 384 = 64512, and
@@ -572,23 +573,36 @@ __global__ void __launch_bounds__(kThreads, 1)
   grid_dependency_wait();
 
   // ---- the line of work: prefix sums over the requests of an item row's tiles, dense and streaming
-  // (the host bounds the line by 2^31 places).  Up to 32 requests the load warp keeps them in its lanes;
-  // otherwise the whole CTA makes them in shared memory.
+  // (the host bounds the line by 2^31 places), by the whole CTA in shared memory, and per 32 requests
+  // their query tiles and the key tiles of their largest and of their smallest items
   uint32_t* cum_d = reinterpret_cast<uint32_t*>(smem + kOffRing);  // [B]
   uint32_t* cum_s = cum_d + kv.B;
   uint32_t* s_warp = cum_s + kv.B;  // [2][kThreads / 32]
-  unsigned long long* s_bound = reinterpret_cast<unsigned long long*>(ctl->xm);  // [kThreads / 32]
   int2* s_req = reinterpret_cast<int2*>(smem);  // [B]: tokens before the chunk, new tokens
-  const bool in_lanes = kv.B <= 32;
+  unsigned long long* s_bound = reinterpret_cast<unsigned long long*>(ctl->xm);  // [kThreads / 32]
+  int* s_tiles = reinterpret_cast<int*>(s_bound + kThreads / 32);                // [3][32]
+  const bool few = kv.B <= kWholeBatch;
+  // (read beside the lengths: the kinds of heads 0 .. 31)
+  const int my_kind = kv.streaming != nullptr && lane < kv.Hkv ? kv.streaming[lane] : 0;
   uint32_t total_d = 0, total_s = 0;
   unsigned long long bound = 0;
-  for (int b0 = 0; b0 < kv.B && !in_lanes; b0 += kThreads) {
+  for (int b0 = 0; b0 < kv.B; b0 += kThreads) {
     const int b = b0 + tid;
     int2 r = make_int2(0, 0);
     if (b < kv.B) s_req[b] = r = request_span(a, b);
     const uint2 cost = line_places(r.x, r.y, W, kv.streaming != nullptr, a.sink, a.local, lane);
     const uint32_t cd = warp_scan(cost.x, lane), cs = warp_scan(cost.y, lane);
     const unsigned long long most = line_bound(cost);
+    if (few) {
+      const int q_tiles = __reduce_add_sync(0xffffffffu, (r.y + W - 1) / W);
+      const int last = __reduce_max_sync(0xffffffffu, r.y > 0 ? (r.x + r.y - 1) / 128 + 1 : 0);
+      const int first = __reduce_max_sync(0xffffffffu, r.y > 0 ? (r.x + min(r.y, W) - 1) / 128 + 1 : 0);
+      if (lane == 0 && b < kv.B) {
+        s_tiles[b / 32] = q_tiles;
+        s_tiles[32 + b / 32] = last;
+        s_tiles[64 + b / 32] = first;
+      }
+    }
     if (lane == 31) {
       s_bound[warp] = most;
       s_warp[warp] = cd;
@@ -596,7 +610,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncthreads();
     uint32_t bd = total_d, bs = total_s;
-    for (int w = 0; w < kThreads / 32; ++w) {
+    const int warps = min((kv.B - b0 + 31) / 32, kThreads / 32);  // with requests
+    for (int w = 0; w < warps; ++w) {
       if (w < warp) {
         bd += s_warp[w];
         bs += s_warp[kThreads / 32 + w];
@@ -662,24 +677,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     if (warp == kLoadWarp) {
       // ============================================================================= load warp
-      int my_base = 0, my_n = 0;  // of request `lane`
-      if (in_lanes && lane < kv.B) {
-        const int2 r = request_span(a, lane);
-        my_base = r.x;
-        my_n = r.y;
-      }
-      uint32_t there;
-      const uint32_t win_heads = window_heads(kv, 0, lane, &there);
-      uint32_t my_d = 0, my_s = 0;
-      if (in_lanes) {
-        const uint2 cost =
-            line_places(my_base, my_n, W, kv.streaming != nullptr, a.sink, a.local, lane);
-        bound = line_bound(cost);
-        my_d = warp_scan(cost.x, lane);
-        my_s = warp_scan(cost.y, lane);
-        total_d = __shfl_sync(0xffffffffu, my_d, 31);
-        total_s = __shfl_sync(0xffffffffu, my_s, 31);
-      }
+      const uint32_t there = __ballot_sync(0xffffffffu, lane < kv.Hkv);
+      const uint32_t win_heads = __ballot_sync(0xffffffffu, my_kind != 0);
       int hd = __popc(there & ~win_heads);  // dense heads
       for (int h0 = 32; h0 < kv.Hkv; h0 += 32) {
         uint32_t t;
@@ -695,7 +694,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // sixteenth of a range more or less against a cut's record and merge.
       const uint32_t ctas = min(gridDim.x, (work + kMinWork - 1) / kMinWork);
       const uint32_t each = ctas ? work / ctas : 0, more = work - each * ctas, c = blockIdx.x;
-      const uint32_t wide_end = more * (each + 1), snap = max(each / 16, 1u);
+      const uint32_t wide_end = more * (each + 1), snap = max(min(each / 16, 4u), 1u);
       auto owner = [&](uint32_t at) {
         return at < wide_end ? at / (each + 1) : more + (at - wide_end) / each;
       };
@@ -706,20 +705,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       // Whole items (the rule is kWholeTiles'): the line is the items, one place each, each request's
       // query tiles from the last (the largest) down.  CTA c takes item c and then one a round, back
       // and forth.
-      const uint32_t my_tiles = my_n > 0 ? (my_n + W - 1) / W : 0, my_end = warp_scan(my_tiles, lane);
-      const uint32_t items = __shfl_sync(0xffffffffu, my_end, 31) * kv.Hkv;
-      const int my_last = my_n > 0 ? (my_base + my_n - 1) / 128 + 1 : 0;
-      const int my_first = my_n > 0 ? (my_base + min(my_n, W) - 1) / 128 + 1 : 0;
-      int biggest = __reduce_max_sync(0xffffffffu, my_last);
-      int ends_on = __reduce_max_sync(0xffffffffu, my_first);
+      const bool group = few && lane * 32 < kv.B;  // a lane knows 32 requests
+      const uint32_t group_end = warp_scan(group ? s_tiles[lane] : 0, lane);
+      const uint32_t items = __shfl_sync(0xffffffffu, group_end, 31) * kv.Hkv;
+      int biggest = __reduce_max_sync(0xffffffffu, group ? s_tiles[32 + lane] : 0);
+      int ends_on = __reduce_max_sync(0xffffffffu, group ? s_tiles[64 + lane] : 0);
       if (hd == 0) {  // a streaming item is its sink and window at most
         const int most = min(a.sink, 1 << 20) / 128 + (min(a.local, 1 << 20) + W) / 128 + 3;
         biggest = min(biggest, most);
         ends_on = min(ends_on, most);
       }
       const int share = static_cast<int>(each / kWholeShare);
-      const bool whole_items = in_lanes && fits &&
-                               (biggest <= kWholeTiles || max(biggest, kWholeEnds * ends_on) <= share);
+      const int small = items <= gridDim.x ? kWholeTiles : kWholeRounds;
+      const bool whole_items =
+          few && fits && (biggest <= small || max(biggest, kWholeEnds * ends_on) <= share);
       uint32_t round = 0;
       if (whole_items) {
         x = c;
@@ -730,13 +729,26 @@ __global__ void __launch_bounds__(kThreads, 1)
         int win, d, h, b, i, k, base, n;
       };
       At at = {};
+      int here = -1, my_base = 0, my_n = 0;  // the 32 requests at hand, one a lane
+      uint32_t my_end = 0;
       auto place_item = [&]() {
         const uint32_t tile = x / kv.Hkv;
-        at.b = __ffs(__ballot_sync(0xffffffffu, my_end > tile)) - 1;
+        const int g = __ffs(__ballot_sync(0xffffffffu, group_end > tile)) - 1, b = g * 32 + lane;
+        if (g != here) {
+          int2 r = make_int2(0, 0);
+          if (b < kv.B) r = here < 0 ? s_req[b] : request_span(a, b);
+          my_base = r.x;
+          my_n = r.y;
+          my_end = warp_scan((my_n + W - 1) / W, lane);
+          if (g > 0) my_end += __shfl_sync(0xffffffffu, group_end, max(g - 1, 0));
+          here = g;
+        }
+        const int src = __ffs(__ballot_sync(0xffffffffu, my_end > tile)) - 1;
+        at.b = g * 32 + src;
         at.h = static_cast<int>(x - tile * kv.Hkv);
-        at.i = static_cast<int>(__shfl_sync(0xffffffffu, my_end, at.b) - 1 - tile);
-        at.base = __shfl_sync(0xffffffffu, my_base, at.b);
-        at.n = __shfl_sync(0xffffffffu, my_n, at.b);
+        at.i = static_cast<int>(__shfl_sync(0xffffffffu, my_end, src) - 1 - tile);
+        at.base = __shfl_sync(0xffffffffu, my_base, src);
+        at.n = __shfl_sync(0xffffffffu, my_n, src);
         at.win = kv.streaming != nullptr && kv.streaming[at.h] != 0;
       };
       if (whole_items) {
@@ -747,28 +759,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         at.d = y / per;
         uint32_t r = y - at.d * per;
         at.h = nth_head(kv, at.win, at.d, lane, win_heads, there);
-        if (in_lanes) {
-          const uint32_t end = at.win ? my_s : my_d;
-          at.b = __ffs(__ballot_sync(0xffffffffu, end > r)) - 1;
-          const uint32_t before = __shfl_sync(0xffffffffu, end, max(at.b - 1, 0));
-          if (at.b > 0) r -= before;
-          at.base = __shfl_sync(0xffffffffu, my_base, at.b);
-          at.n = __shfl_sync(0xffffffffu, my_n, at.b);
-        } else {
-          const uint32_t* cum = at.win ? cum_s : cum_d;
-          int lo = 0, hi = kv.B - 1;
-          while (lo < hi) {
-            const int mid = (lo + hi) >> 1;
-            if (cum[mid] > r)
-              hi = mid;
-            else
-              lo = mid + 1;
-          }
-          at.b = lo;
-          if (lo > 0) r -= cum[lo - 1];
-          at.base = s_req[lo].x;
-          at.n = s_req[lo].y;
+        const uint32_t* cum = at.win ? cum_s : cum_d;
+        int lo = 0;
+        for (int n = kv.B; n > 1;) {  // the first above r lies in lo .. lo + n - 1; 32 probes at once
+          const int step = (n + 31) / 32;
+          const uint32_t end = cum[lo + min((lane + 1) * step, n) - 1];
+          const int src = __ffs(__ballot_sync(0xffffffffu, end > r)) - 1;
+          lo += src * step;
+          n = min(step, n - src * step);
         }
+        at.b = lo;
+        if (lo > 0) r -= cum[lo - 1];
+        at.base = s_req[lo].x;
+        at.n = s_req[lo].y;
         for (int i0 = 0; i0 * W < at.n; i0 += 32) {
           int ns, w0;
           uint32_t cost = 0;
@@ -911,14 +914,9 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
               at.h = nth_head(kv, at.win, at.d, lane, win_heads, there);
             }
-            if (in_lanes) {
-              at.base = __shfl_sync(0xffffffffu, my_base, at.b);
-              at.n = __shfl_sync(0xffffffffu, my_n, at.b);
-            } else {
-              const int2 r = request_span(a, at.b);
-              at.base = r.x;
-              at.n = r.y;
-            }
+            const int2 r = request_span(a, at.b);
+            at.base = r.x;
+            at.n = r.y;
           } while (at.n == 0);
         }
       }

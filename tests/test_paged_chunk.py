@@ -285,6 +285,8 @@ DENSE = [
     ([(1500, 200)], 64, 6, 1),
     ([(i * 13, 1 + i % 3) for i in range(40)], 16, 4, 2),
     ([(i % 70, (i % 5) * (i % 3)) for i in range(600)], 16, 2, 1),
+    ([(i % 90, (i % 4) * (i % 3)) for i in range(1100)], 16, 2, 2),
+    ([(5000 - 100 * i, 1 + 70 * (i % 5 == 2)) for i in range(45)], 64, 4, 1),
     ([(200, 40)], 32, 80, 40),
     ([(70000, 16)], 64, 16, 1),    # 78 parts of a 256-row item
     ([(100000, 1), (3, 1)], 64, 8, 1),
