@@ -14,11 +14,11 @@
 // most 128 / G tokens (decode, short chunks, tails) they share the query tile and take alternate key
 // tiles, and their results are joined in TMEM at the end.
 //
-// Work partition (stream-K): the key tiles of all (KV head, request, query tile) items form one line,
-// cut into equal ranges, one per CTA.  Every CTA works out the line's length from the requests'
-// lengths by itself (no planning launch).  An item inside one CTA is finished there; a cut item leaves
-// one partial record per CTA, and the CTA that takes the item's last ticket merges them in CTA order.
-// No CTA waits for another.
+// Work partition: the key tiles of all (KV head, request, query tile) items form one line, cut into
+// equal ranges, one per CTA.  Every CTA works out the line's length from the requests' lengths by itself
+// (no planning launch).  An item inside one CTA is finished there; a cut item leaves one partial record
+// per CTA, and the CTA that takes the item's last ticket merges them in CTA order.  Where cuts cost more
+// than they even out (kWholeTiles), CTAs take whole items instead.  No CTA waits for another.
 //
 // Inside a CTA: warps 0-3 and 4-7 are the streams' softmax warpgroups (a thread owns a row: S from
 // TMEM, P back to TMEM over S as bf16, at a unit's end O from TMEM to the output or to a record), warps 8
@@ -27,6 +27,16 @@
 // a V tile in more time than the products take), one thread of warp 9 issues the tcgen05 products (S =
 // Q K^T from shared memory, O += P V with P from TMEM), and warp 10 clears the rows behind a request's
 // last token in the V tile that holds it.
+//
+// What bounds it.  Prompts: a tile of 256 x 128 is 32 products of 64 cycles, 2048 cycles; it takes about
+// 2400, because a stream's next S waits for its P, and its P for the maximum over all of S.  Decode: the
+// cache's bytes, behind ~8 us in which the CTA starts, plans and gets its first tile.  In between, where
+// a CTA has some tens of tiles, the records and merges of cut items (each 10 to 15 us at the end).
+// Measured on a GB300, launches replayed in a graph: one prompt of 8191 tokens, 32 heads of their own,
+// 357 us, 1.54 PFLOP/s, 0.81 of a measured bf16 product; 2048 tokens after 30K, 32 heads on 8, 675 us,
+// 1.55 PFLOP/s (the power cap holds it there); one token of 4 requests of 32K, 100 us, 5.3 TB/s, 0.79 of
+// a measured copy; one token of 8 requests on 8 streaming heads (64 + 256 tokens), 15 us; two prompts of
+// about 5000 tokens, 32 heads on 8, window 1000, 184 us, 0.93 PFLOP/s of visible pairs.
 #include "common.cuh"
 #include "internal.h"
 
@@ -40,13 +50,25 @@ constexpr int kLoadWarp = 8, kMmaWarp = 9, kTailWarp = 10, kValueWarp = 11;
 constexpr int kRing = 5;
 constexpr uint32_t kHalfBytes = 128 * 128;  // 64 dims of 128 rows, 128-byte swizzled lines
 constexpr uint32_t kTileBytes = 2 * kHalfBytes;
-// The line of work counts an item's tiles and kItemPad more, what starting and ending a unit costs;
-// and no CTA takes less than kMinWork of it: a cut costs a record, a ticket and a share of a merge,
-// about as much as four tiles.
+// The line of work counts an item's tiles and kItemPad more, what starting and ending a unit costs
+// (2 to 6 lie within 1 %), and no CTA takes less than kMinWork of it: a cut costs a record, a ticket and
+// a share of a merge, as much as some tiles (one token of 8 heads over 8000: 24.2 us, 25.4 when ranges
+// go down to one place; over 4096 of one head: 20.6 and 25.2).
 constexpr int kItemPad = kChunkItemPad, kMinWork = 6;
+// When whole items beat cuts (times in us, cut / whole).  (1) Items of few tiles: a cut's record and
+// merge cost as much as 10 to 15 tiles, whole items an uneven end of at most one item.  With an item or
+// less per CTA that is so up to some kWholeTiles (600 new tokens, 28 heads on 4: 34 / 17.5; 8 decode
+// requests with windows: 20 / 15), with several up to kWholeRounds (64 short decode requests: 64 / 55;
+// but 512 of up to 16 tiles: 77 / 88).  (2) Many items per CTA, of which the last ones taken are small:
+// the largest item at most 1 / kWholeShare of a CTA's share, and kWholeEnds of the ones taken last too
+// (the prompt of 8191 tokens, 33 items of 2 to 64 tiles on each of 32 heads: 397 / 357).  The chunk of
+// 2048 tokens after 30K, where all items are long, stays cut.  Up to kWholeBatch requests, because a lane
+// of the load warp knows 32 of them.
 constexpr int kWholeTiles = 20, kWholeRounds = 12, kWholeShare = 3, kWholeEnds = 4;
 constexpr int kWholeBatch = 1024;
-constexpr float kLazyLog2 = 8.f;  // P stays below 2^8 times its weight at the true maximum
+// P stays below 2^8 times its weight at the true maximum: exact in bf16's exponent and far from fp32's
+// limits in l and O.  With 0 (a rescale at every rise) the prompt of 8191 tokens takes 423 us, not 357.
+constexpr float kLazyLog2 = 8.f;
 
 // Registers per thread of the softmax and of the other warps.  The launch has 168 x 384 = 64512, and
 // 208 x 256 + 88 x 128 is exactly that.
@@ -690,8 +712,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t dense_work = hd * total_d;
       const uint32_t work = fits ? dense_work + (kv.Hkv - hd) * total_s : 0;
       // Equal ranges: boundary c lies at c each + min(c, more), CTA c has what lies between boundaries c
-      // and c + 1.  A boundary that would cut less than `snap` off an item's start or end moves there: a
-      // sixteenth of a range more or less against a cut's record and merge.
+      // and c + 1.  A boundary that would cut less than `snap` off an item's start or end moves there:
+      // up to four tiles more or less, a sixteenth of a range, against a cut's record and merge (seven
+      // requests of 60 to 700 or one new tokens: 91 us, 95 without; a sixteenth whatever its length
+      // costs the chunk of 2048 tokens 2 %).
       const uint32_t ctas = min(gridDim.x, (work + kMinWork - 1) / kMinWork);
       const uint32_t each = ctas ? work / ctas : 0, more = work - each * ctas, c = blockIdx.x;
       const uint32_t wide_end = more * (each + 1), snap = max(min(each / 16, 4u), 1u);
