@@ -605,6 +605,10 @@ def dsa_append_chunk(kv: PagedKV, chunk: Chunk, k_new, v_new, rotary: Rotary | N
         raise ValueError(f"the chunk holds {chunk.batch} requests, the cache {kv.batch}")
     if rotary is not None and rotary.tokens is not None and rotary.tokens != n:
         raise ValueError(f"positions of {rotary.tokens} tokens for a chunk of {n}")
+    if meta is not None and logical_page > 0:
+        need = kv.num_phys_pages * kv.num_kv_heads * (kv.page_size // logical_page) * 512
+        if not meta.is_contiguous() or meta.nbytes < need:
+            raise ValueError(f"meta must be contiguous and hold {need} bytes, got {meta.nbytes}")
     qs = 0
     if q is not None:
         qs = _token_rows(q, n, kv.num_q_heads, "q")

@@ -579,6 +579,46 @@ def test_two_workspaces_on_two_streams_at_once():
 
 # -------------------------------------------------------------------------------------- the pipeline
 
+def test_step_in_a_pool_beyond_32_bit_offsets():
+    """Pages whose elements lie behind 2^31 of the pool (4.3 GB each for keys and values)."""
+    from chunk_support import attend_reference, check_rows, visible
+    P = 65600
+    k, v = (torch.zeros(P, 1, 256, 128, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    table = torch.tensor([[65590, 3, 65599], [65598, 65597, 2]], dtype=torch.int32, device="cuda")
+    spec = [(0, 600), (256, 44)]
+    T = 644
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+    row = [b for b, (o, n) in enumerate(spec) for _ in range(n)]
+    pos = [o + i for o, n in spec for i in range(n)]
+    chunk = B.chunk(i32([0, 600, T]), i32([600, 44]), i32(row), i32(pos))
+    lens, status = i32([600, 300]), i32([0])
+    g = torch.Generator().manual_seed(11)
+    kn, vn, q = (torch.randn(T, h, 128, generator=g).bfloat16().cuda() for h in (1, 1, 2))
+    kv = B.paged_kv(k, v, table, lens, 2, None, status)
+    meta = torch.zeros(P, 1, 1, 128, 2, dtype=torch.bfloat16, device="cuda")
+    B.dsa_append_chunk(kv, chunk, kn, vn, meta_kind=B.DSA_META_MINMAX, logical_page=256, meta=meta)
+    out = torch.empty_like(q)
+    m, l = (torch.empty(T, 2, device="cuda") for _ in range(2))
+    ws = torch.zeros(B.dsa_chunk_attn_workspace_size(kv, T), dtype=torch.uint8, device="cuda")
+    B.dsa_chunk_attn(kv, chunk, q, SCALE, out, m, l, ws)
+    torch.cuda.synchronize()
+    assert int(status) == 0
+    for b, (o, n) in enumerate(spec):
+        t0, L = (0, 600)[b], o + n
+        K, V = (x[table[b].long(), 0].reshape(-1, 128)[:L] for x in (k, v))
+        assert torch.equal(K[o:], kn[t0:t0 + n, 0]) and torch.equal(V[o:], vn[t0:t0 + n, 0])
+        for j in range(o // 256, ceil_div(L, 256)):
+            rows = K[256 * j:min(L, 256 * j + 256)]
+            rec = meta[int(table[b, j]), 0, 0]
+            assert torch.equal(rec[:, 0], rows.amax(0)) and torch.equal(rec[:, 1], rows.amin(0))
+        ok = visible(np.arange(o, L), L, None)
+        for h in range(2):
+            ref = attend_reference(q[t0:t0 + n, h].double().cpu().numpy(), K.double().cpu().numpy(),
+                                   V.double().cpu().numpy(), ok, SCALE)
+            check_rows((out[t0:t0 + n, h], m[t0:t0 + n, h], l[t0:t0 + n, h]), ref,
+                       f"request {b} head {h}")
+
+
 def test_prefill_then_decode_through_the_decoders():
     """Prompts in two chunks through a decoder's prefill, then decode steps: metadata equals a fresh
     build bit for bit, and a decode step over all pages equals the attention of the chunk call."""

@@ -169,6 +169,17 @@ def test_binding_refuses_wrong_tensors(lib):
     with pytest.raises(ValueError, match="bf16"):
         B._token_rows(torch.zeros(4, 2, 128), 4, 2, "k_new")
     assert B._token_rows(torch.zeros(4, 10, 128, dtype=torch.bfloat16)[:, 2:4], 4, 2, "k") == 1280
+    kv, c = B.PagedKV(), B.Chunk()
+    kv.batch, kv.num_phys_pages, kv.num_kv_heads, kv.page_size = 2, 3, 2, 32
+    c.batch, c.tokens = 2, 4
+    new = torch.zeros(4, 2, 128, dtype=torch.bfloat16)
+    for short in (torch.zeros(3 * 2 * 2 * 256 - 1, dtype=torch.bfloat16),
+                  torch.zeros(3 * 2 * 2 * 256, 2, dtype=torch.bfloat16)[:, 0]):
+        with pytest.raises(ValueError, match="meta"):
+            B.dsa_append_chunk(kv, c, new, new, logical_page=16, meta=short)
+    with pytest.raises(ValueError, match="CUDA"):
+        B.dsa_append_chunk(kv, c, new, new, logical_page=16,
+                           meta=torch.zeros(3 * 2 * 2 * 256, dtype=torch.bfloat16))
 
 
 def test_rotary_phases_are_exact_fractions_of_a_turn():
