@@ -40,8 +40,6 @@
 #include "common.cuh"
 #include "internal.h"
 
-#include <type_traits>
-
 namespace dsa {
 namespace {
 
@@ -51,7 +49,7 @@ constexpr int kRing = 5;
 constexpr uint32_t kHalfBytes = 128 * 128;  // 64 dims of 128 rows, 128-byte swizzled lines
 constexpr uint32_t kTileBytes = 2 * kHalfBytes;
 // The line of work counts an item's tiles and kItemPad more, what starting and ending a unit costs
-// (2 to 6 lie within 1 %), and no CTA takes less than kMinWork of it: a cut costs a record, a ticket and
+// (2 to 6 lie within 2 %), and no CTA takes less than kMinWork of it: a cut costs a record, a ticket and
 // a share of a merge, as much as some tiles (one token of 8 heads over 8000: 24.2 us, 25.4 when ranges
 // go down to one place; over 4096 of one head: 20.6 and 25.2).
 constexpr int kItemPad = kChunkItemPad, kMinWork = 6;
@@ -66,8 +64,9 @@ constexpr int kItemPad = kChunkItemPad, kMinWork = 6;
 // of the load warp knows 32 of them.
 constexpr int kWholeTiles = 20, kWholeRounds = 12, kWholeShare = 3, kWholeEnds = 4;
 constexpr int kWholeBatch = 1024;
-// P stays below 2^8 times its weight at the true maximum: exact in bf16's exponent and far from fp32's
-// limits in l and O.  With 0 (a rescale at every rise) the prompt of 8191 tokens takes 423 us, not 357.
+// P stays below 2^8 times its weight at the true maximum: the same relative rounding to bf16, and far from
+// fp32's limits in l and O.  With 0 (a rescale at every rise) the prompt of 8191 tokens takes 423 us, not
+// 357.
 constexpr float kLazyLog2 = 8.f;
 
 // Registers per thread of the softmax and of the other warps.  The launch has 168 x 384 = 64512, and
@@ -109,7 +108,7 @@ struct Ctl {
   unsigned long long qfull, qempty, sfull[2], pready[2][2], odone[2], ufull[2], uempty[2],
       both, help, tail[4], rows_in[8];
   uint32_t tmem;
-  int abort, last, pad;
+  int abort;
   Unit unit[2];
   Merge merge[2];  // cut items to merge at the CTA's end, where the softmax warps lend a hand
   int merges;
