@@ -573,7 +573,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(smem_u32(&ctl->uempty[t]), 10);  // softmax warps, issue warp, value warp
     }
     mbar_init(smem_u32(&ctl->both), 8);          // the softmax warps
-    mbar_init(smem_u32(&ctl->help), 1);
+    mbar_init(smem_u32(&ctl->help), 8);          // the softmax warps, when their last unit is out
     for (int w = 0; w < 8; ++w) mbar_init(smem_u32(&ctl->rows_in[w]), 1);
     for (int s = 0; s < 4; ++s) mbar_init(smem_u32(&ctl->tail[s]), 1);
     ctl->abort = 0;
@@ -1145,7 +1145,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     for (int u = 0; ok; ++u) {
       const int us = u & 1;
-      if (!warp_wait(smem_u32(&ctl->ufull[us]), (u >> 1) & 1, abort, kv.status)) break;
+      if (!(ok = warp_wait(smem_u32(&ctl->ufull[us]), (u >> 1) & 1, abort, kv.status))) break;
       // (read from shared memory where it is used: the loop below needs the registers for the row)
       const volatile Unit& un = ctl->unit[us];
       if (!un.valid) break;
@@ -1360,8 +1360,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&ctl->uempty[us]));
     }
-    if (ok && tid == 0) {
-      ctl->merges = merges;
+    // Merges overlay the query tiles and the ring, so they wait for the last products of both streams:
+    // stream 0 may be done with a unit some thousand cycles before stream 1.
+    if (ok && lane == 0) {
+      if (tid == 0) ctl->merges = merges;
       mbar_arrive(smem_u32(&ctl->help));
     }
     __syncwarp();

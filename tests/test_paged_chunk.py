@@ -577,6 +577,35 @@ def test_two_workspaces_on_two_streams_at_once():
             assert torch.equal(x, y)
 
 
+@pytest.mark.parametrize("spec", [
+    [(12306, 1), (4948, 1), (0, 347), (0, 1), (4896, 1)],
+    [(0, 389), (0, 312), (0, 320), (3231, 1)],
+])
+def test_chunk_attn_merges_wait_for_both_streams(spec):
+    """32 heads of their own over requests whose cut leaves CTAs with a part of a long item and then a
+    whole item of 129 to 256 tokens, in which the first 128 tokens see a key tile less than the others:
+    the merge at the CTA's end may not begin before the later of the two is done.  The same bits on
+    every call, alone and beside a call on another stream that delays some of the CTAs."""
+    c = ChunkCase(spec, 64, 32, 32, seed=12)
+    other = ChunkCase([(3000, 1), (0, 200)], 64, 8, 8, seed=13)
+    ws = torch.zeros(B.dsa_chunk_attn_workspace_size(
+        B.paged_kv(c.k, c.v, c.table, c.lens, 32), c.tokens), dtype=torch.uint8, device="cuda")
+    first = _attend(c, ws=ws)
+    torch.cuda.synchronize()
+    assert int(c.status) == 0
+    c.check(*first, SCALE)
+    s = torch.cuda.Stream()
+    for rep in range(40):
+        if rep % 2:
+            with torch.cuda.stream(s):
+                _attend(other)
+        got = _attend(c, ws=ws)
+        for x, y in zip(got, first):
+            assert torch.equal(x, y)
+    torch.cuda.synchronize()
+    assert int(c.status) == 0 and int(other.status) == 0
+
+
 # -------------------------------------------------------------------------------------- the pipeline
 
 def test_step_in_a_pool_beyond_32_bit_offsets():
