@@ -1372,8 +1372,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp < kLoadWarp && warp_wait(smem_u32(&ctl->help), 0, abort, kv.status)) {
     const int merges = *const_cast<volatile int*>(&ctl->merges);
     uint32_t phase[2] = {met, 0};
-    for (int x = 0; x < merges; ++x)
-      if (!merge_records(a, ctl->merge[x], smem, ctl, phase)) break;
+    bool ok = true;
+    for (int x = 0; x < merges && ok; ++x) ok = merge_records(a, ctl->merge[x], smem, ctl, phase);
+    if (!ok)  // rows in flight land before the CTA leaves
+      for (int t = 0; t < 64; ++t) __nanosleep(1000);
   }
   __syncthreads();
   if (warp == kMmaWarp)
