@@ -196,13 +196,17 @@ class TopKDecoder:
 
     def prefill(self, chunk: Chunk, q, k_new, v_new, rotary=None, stream=None):
         """Appends a planned chunk (prompts, or pieces of them), keeping this decoder's metadata
-        current, and attends it over the whole cache: (out bf16, m, l)."""
+        current, and attends it over the whole cache: (out bf16, m, l).  Not once the decoder attends
+        KV8 or KV4 pages: they hold what the pools held when they were quantised."""
+        if getattr(self, "kv8", None) is not None or getattr(self, "kv4", None) is not None:
+            raise ValueError("this decoder attends KV8 / KV4 pages quantised before: prefill first, "
+                             "then use_kv8 / use_kv4")
         q_t = chunk.append(k_new, v_new, [(self.kind, self.lp, self.meta)], rotary, q, stream)
         return chunk.attend(q_t, self.scale, stream=stream)
 
     def use_kv8(self, stream=None):
-        """Attends over KV8 pages from now on (the pools are quantised once, here); selection is
-        unchanged (it reads the metadata)."""
+        """Attends over KV8 pages from now on (the pools are quantised once, here, and prefill is
+        refused from then on); selection is unchanged (it reads the metadata)."""
         c = self.cache
         self.kv8 = c.kv8(stream)
         ws = B.dsa_sparse_decode_attn_kv8_workspace_size(c.kv, self.idx.shape[-1])
@@ -211,7 +215,8 @@ class TopKDecoder:
         return self
 
     def use_kv4(self, stream=None):
-        """Attends over KV4 pages from now on (the pools are quantised once, here)."""
+        """Attends over KV4 pages from now on (the pools are quantised once, here, and prefill is
+        refused from then on)."""
         c = self.cache
         self.kv4 = c.kv4(stream)
         ws = B.dsa_sparse_decode_attn_kv4_workspace_size(c.kv, self.idx.shape[-1])

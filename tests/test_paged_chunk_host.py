@@ -224,3 +224,15 @@ def test_plan_reference_keeps_every_page_once(seed):
                 assert pos == slot == -1
         seen.add(got["refused"])
     assert seen  # both outcomes occur over the seeds; each is asserted page by page above
+
+
+def test_prefill_is_refused_on_quantised_pages():
+    """KV8 and KV4 pages are a copy of the pools: a prompt that entered the pools only would be missing
+    from every later step."""
+    from dynamic_block_sparse_gb300.pipeline import TopKDecoder
+    for which in ("kv8", "kv4"):
+        dec = object.__new__(TopKDecoder)
+        dec.kv8 = dec.kv4 = None
+        setattr(dec, which, torch.zeros(1, dtype=torch.uint8))
+        with pytest.raises(ValueError, match="quantised"):
+            dec.prefill(None, None, None, None)
