@@ -140,7 +140,9 @@ class Chunk:
     def plan(self, delta, stream=None):
         """Starts a step: ``delta[b]`` new tokens for request b (or -n: its last n tokens dropped),
         with pages from the stack.  Advances the cache's lengths and page table and fills the chunk; a
-        request that does not fit gets ``count[b] = 0`` and raises DSA_STATUS_NO_PAGES."""
+        request that does not fit gets ``count[b] = 0`` and raises DSA_STATUS_NO_PAGES.  What a decoder
+        keeps from its steps about the pages (a reused selection) is renewed by its ``prefill``; a
+        caller that appends without it selects anew before the next step."""
         c = self.cache
         if self.free_pages is None:
             raise ValueError("this chunk has no stack of free pages to plan with")
@@ -271,6 +273,7 @@ class HierDecoder:
         self.out, self.m, self.l, self.result = c.result_views()
         ws = B.dsa_sparse_decode_attn_workspace_size(c.kv, self.idx.shape[-1])
         self.workspace = torch.zeros(max(16, ws), dtype=torch.uint8, device=c.device)
+        self.prefilled = False  # since the last selection
 
     def build_meta(self, stream=None):
         B.dsa_build_page_meta(self.cache.kv, B.DSA_META_MINMAX, self.lp, self.meta, stream)
@@ -282,7 +285,9 @@ class HierDecoder:
     def prefill(self, chunk: Chunk, q, k_new, v_new, rotary=None, stream=None):
         """Appends a planned chunk (prompts, or pieces of them), keeping this decoder's metadata
         current, and attends it over the whole cache (streaming heads over their sink + local
-        tokens): (out bf16, m, l)."""
+        tokens): (out bf16, m, l).  The next ``step`` selects whatever its number, since the selection
+        kept from before knows neither the new pages nor a request that took over another's row."""
+        self.prefilled = True
         q_t = chunk.append(k_new, v_new, [(B.DSA_META_MINMAX, self.lp, self.meta)], rotary, q,
                            stream)
         return chunk.attend(q_t, self.scale, self.sink, self.local, stream=stream)
@@ -291,12 +296,14 @@ class HierDecoder:
         c = self.cache
         B.dsa_score_pages(c.kv, q, self.meta, B.DSA_META_MINMAX, self.lp, self.scores, stream)
         B.dsa_select_hier(self.scores, self.stride, self.g, self.k, self.idx, self.count, stream)
+        self.prefilled = False
 
     def step(self, q, t: int, stream=None):
-        """Decode step t: selection runs when t is a multiple of the reuse interval (LServe §4.3),
-        otherwise the previous selection is reused with this step's query."""
-        c = self.cache
-        if t % self.reuse == 0:
+        """Decode step t: selection runs when t is a multiple of the reuse interval (LServe §4.3) or
+        a prefill came before, otherwise the previous selection is reused with this step's query.  (A
+        captured graph keeps what was decided at its capture: after a prefill, replay one that
+        selects.)"""
+        if self.prefilled or t % self.reuse == 0:
             self.select(q, stream)
         self.attend(q, stream)
         return self.out, self.m, self.l

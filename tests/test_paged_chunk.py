@@ -685,3 +685,35 @@ def test_prefill_then_decode_through_the_decoders():
                 assert ((out[:2].float() - o2).abs() <= 2.0 ** -8 * o2.abs() + 2.0 ** -7 * 4.5).all()
                 assert (m[:2] - m2).abs().max() <= 1e-4
             assert n >= 1
+
+
+def test_hier_step_after_a_request_took_over_a_row():
+    """A long request is released and a prompt takes its row between two selections: the step that would
+    reuse the old selection attends the new request's pages, as a decoder without a past does."""
+    from dynamic_block_sparse_gb300.pipeline import Cache, Chunk, HierDecoder
+    torch.manual_seed(5)
+    hq, hkv, p = 8, 2, 16
+    k = torch.zeros(200, hkv, p, 128, dtype=torch.bfloat16, device="cuda")
+    cache = Cache(k, k.clone(), torch.full((2, 80), -1, dtype=I32, device="cuda"),
+                  torch.zeros(2, dtype=I32, device="cuda"), hq, _t([0, 1], torch.uint8))
+    make = lambda: HierDecoder(cache, k_phys=4, logical_page=16, sink=8, local=40)
+    dec = make()
+    chunk = Chunk(cache, 1000, free_pages=torch.arange(200, dtype=I32, device="cuda"))
+    new = lambda: [torch.randn(1000, h, 128, device="cuda").bfloat16() for h in (hq, hkv, hkv)]
+    q = torch.randn(2, hq, 128, device="cuda").bfloat16()
+    chunk.plan(_t([900, 60]))
+    dec.prefill(chunk, *new())
+    dec.step(q, 0)
+    dec.idx[0].copy_(torch.tensor([40, 41, 42, 43], dtype=I32))  # the old request's far pages
+    chunk.plan(_t([-900, 0]))
+    chunk.plan(_t([200, 1]))
+    dec.prefill(chunk, *new())
+    got = [x.clone() for x in dec.step(q, 1)]
+    fresh = make()
+    fresh.build_meta()
+    want = fresh.step(q, 0)
+    torch.cuda.synchronize()
+    assert int(cache.status) == 0
+    for x, y in zip(got, want):
+        assert torch.equal(x, y)
+    assert (got[2][0] > 0).all()

@@ -236,3 +236,32 @@ def test_prefill_is_refused_on_quantised_pages():
         setattr(dec, which, torch.zeros(1, dtype=torch.uint8))
         with pytest.raises(ValueError, match="quantised"):
             dec.prefill(None, None, None, None)
+
+
+def test_a_reused_selection_ends_with_a_prefill():
+    """HierDecoder keeps its selection for ``reuse`` steps, but not across a prefill."""
+    from dynamic_block_sparse_gb300.pipeline import HierDecoder
+
+    class Chunk:
+        def append(self, *a):
+            return None
+
+        def attend(self, *a, **kw):
+            return None
+
+    dec = object.__new__(HierDecoder)
+    dec.reuse, dec.prefilled, dec.lp, dec.sink, dec.local, dec.scale = 4, False, 16, 1, 1, 1.0
+    dec.cache = dec.meta = dec.out = dec.m = dec.l = None
+    selected = []
+    dec.attend = lambda q, stream=None: None
+
+    def select(q, stream=None):
+        selected.append(q)
+        dec.prefilled = False
+
+    dec.select = select
+    for t in range(8):
+        if t in (2, 4, 7):
+            dec.prefill(Chunk(), None, None, None)
+        dec.step(t, t)
+    assert selected == [0, 2, 4, 7]
