@@ -467,10 +467,28 @@ class PRRDecoder:
 
     def prefill(self, chunk: Chunk, q, k_new, v_new, rotary=None, stream=None):
         """Appends a planned chunk (prompts, or pieces of them), keeping this decoder's metadata
-        current, and attends it over the whole cache: (out bf16, m, l)."""
+        current, and attends it over the whole cache: (out bf16, m, l).  The predictor starts anew on
+        the pages that hold the chunk's tokens alone: what it knew of their positions belongs to tokens
+        dropped since, or to a request whose row this one took over."""
         q_t = chunk.append(k_new, v_new, [(B.DSA_META_MINMAX, self.cache.page_size, self.meta)], rotary, q,
                            stream)
+        self._forget(chunk, stream)
         return chunk.attend(q_t, self.scale, stream=stream)
+
+    def _forget(self, chunk: Chunk, stream=None):
+        """Resets level and trend of the pages that a prefilled request's older tokens do not reach,
+        and takes these pages out of the predicted set (the end of its ascending list)."""
+        c = self.cache
+        with torch.cuda.stream(stream):  # (None: the current one)
+            older = c.seq_lens - chunk.count  # tokens before the chunk
+            kept = torch.where(chunk.count > 0, (older + (c.page_size - 1)) // c.page_size, self.stride)
+            page = torch.arange(self.stride, dtype=torch.int32, device=c.device)
+            gone = (page >= kept[:, None])[:, None]
+            self.ell.masked_fill_(gone, -math.inf)
+            self.trend.masked_fill_(gone, 0.0)
+            slot = torch.arange(self.k_pred, dtype=torch.int32, device=c.device)
+            stays = (slot < self.spec_count[..., None]) & (self.spec_idx < kept[:, None, None])
+            self.spec_count.copy_(stays.sum(-1))
 
     # ---- stages (one or two library calls each), exposed so a caller can time them one by one
     def stage_score(self, q, stream=None):

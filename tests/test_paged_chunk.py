@@ -717,3 +717,46 @@ def test_hier_step_after_a_request_took_over_a_row():
     for x, y in zip(got, want):
         assert torch.equal(x, y)
     assert (got[2][0] > 0).all()
+
+
+@pytest.mark.parametrize("fused", [True, False])
+def test_prr_step_after_a_request_took_over_a_row(fused):
+    """A request is released and a prompt takes its row between two PRR steps: the next step starts the
+    predictor anew there and, in superset mode, attends the selected pages alone, while the other request
+    (one more token, in a page that it had) carries its state on."""
+    from dynamic_block_sparse_gb300.pipeline import Cache, Chunk, PRRDecoder, TopKDecoder
+    torch.manual_seed(6)
+    hq, hkv, p, k = 8, 2, 16, 4
+    pool = torch.zeros(200, hkv, p, 128, dtype=torch.bfloat16, device="cuda")
+    cache = Cache(pool, pool.clone(), torch.full((2, 80), -1, dtype=I32, device="cuda"),
+                  torch.zeros(2, dtype=I32, device="cuda"), hq)
+    dec = PRRDecoder(cache, k, 6, 0.3, 0.2, 0.5, superset=True, fused=fused)
+    chunk = Chunk(cache, 1000, free_pages=torch.arange(200, dtype=I32, device="cuda"))
+    new = lambda: [torch.randn(1000, h, 128, device="cuda").bfloat16() for h in (hq, hkv, hkv)]
+    query = lambda: torch.randn(2, hq, 128, device="cuda").bfloat16()
+    chunk.plan(_t([900, 500]))
+    dec.prefill(chunk, *new())
+    for _ in range(3):
+        dec.step(query())
+    chunk.plan(_t([-900, 0]))
+    chunk.plan(_t([300, 1]))
+    ell = dec.ell.clone()
+    dec.prefill(chunk, *new())
+    assert torch.equal(dec.ell[1, :, :32], ell[1, :, :32])
+    assert dec.spec_count.tolist() == [[0] * hkv, [6] * hkv]
+    q = query()
+    dec.step(q)
+    one = TopKDecoder(cache, k)
+    one.build_meta()
+    want = one.step(q)
+    torch.cuda.synchronize()
+    assert int(cache.status) == 0
+    assert torch.equal(dec.ell[0, :, :19], dec.scores[0, :, :19]) and (dec.trend[0] == 0).all()
+    assert (dec.ell[0, :, 19:] == -math.inf).all()
+    assert not torch.equal(dec.ell[1, :, :32], dec.scores[1, :, :32])
+    assert torch.equal(dec.idx[0], one.idx[0])
+    # the same pages, merged in another order: fp32 sums of some tens of tokens, and probabilities
+    # rounded to bf16 against another maximum (2^-8 of themselves in both; |v| averages below 4.5)
+    for x, y in zip((dec.out, dec.m, dec.l), want):
+        assert (x[0] - y[0]).abs().max() <= 2.0 ** -7 * 4.5
+    assert ((dec.l[0] - want[2][0]).abs() <= 2.0 ** -18 * want[2][0] * 64).all()

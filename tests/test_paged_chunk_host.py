@@ -265,3 +265,27 @@ def test_a_reused_selection_ends_with_a_prefill():
             dec.prefill(Chunk(), None, None, None)
         dec.step(t, t)
     assert selected == [0, 2, 4, 7]
+
+
+def test_the_predictor_forgets_pages_a_prefill_filled():
+    """PRRDecoder: requests that grow, grow after a rollback, take over a row, or take no part."""
+    import types
+
+    from dynamic_block_sparse_gb300.pipeline import PRRDecoder
+    dec = object.__new__(PRRDecoder)
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32)
+    dec.cache = types.SimpleNamespace(seq_lens=i32([70, 48, 30, 0, 90]), page_size=16, device="cpu")
+    dec.k_pred, dec.stride, dec.t = 4, 7, 3
+    dec.ell = torch.arange(5 * 2 * 7).reshape(5, 2, 7).float()
+    dec.trend = dec.ell + 1
+    P = i32([[0, 2, 4, 5], [1, 3, 6, -1], [0, 1, 2, 3], [0, 3, -1, -1], [2, 3, 5, 6]])
+    dec.spec_bufs = [None, P[:, None].expand(5, 2, 4).contiguous()]
+    dec.spec_counts = [None, i32([[4] * 2, [3] * 2, [4] * 2, [2] * 2, [4] * 2])]
+    ell, trend = dec.ell.clone(), dec.trend.clone()
+    # tokens before the chunk: 65 (5 pages), 32 (2), 0, a refused request's 0, a request at rest
+    dec._forget(types.SimpleNamespace(count=i32([5, 16, 30, 0, 0])))
+    for b, kept in enumerate([5, 2, 0, 7, 7]):
+        assert torch.equal(dec.ell[b, :, :kept], ell[b, :, :kept])
+        assert torch.equal(dec.trend[b, :, :kept], trend[b, :, :kept])
+        assert (dec.ell[b, :, kept:] == -math.inf).all() and (dec.trend[b, :, kept:] == 0).all()
+    assert dec.spec_count.tolist() == [[3] * 2, [1] * 2, [0] * 2, [2] * 2, [4] * 2]
