@@ -169,6 +169,12 @@ class Chunk:
                          local, stream)
         return self.out, self.m, self.l
 
+    def attend_all(self, q, scale: float, stream=None):
+        """``attend`` with every KV head over the whole cache, those marked streaming too (a sink as
+        long as the cache), for decoders that know no window."""
+        c = self.cache
+        return self.attend(q, scale, sink=c.max_pages * c.page_size, stream=stream)
+
 
 class TopKDecoder:
     def __init__(self, cache: Cache, k: int, logical_page: int | None = None,
@@ -198,13 +204,14 @@ class TopKDecoder:
 
     def prefill(self, chunk: Chunk, q, k_new, v_new, rotary=None, stream=None):
         """Appends a planned chunk (prompts, or pieces of them), keeping this decoder's metadata
-        current, and attends it over the whole cache: (out bf16, m, l).  Not once the decoder attends
-        KV8 or KV4 pages: they hold what the pools held when they were quantised."""
+        current, and attends it over the whole cache (every head): (out bf16, m, l).  Not once
+        the decoder attends KV8 or KV4 pages: they hold what the pools held when they were
+        quantised."""
         if getattr(self, "kv8", None) is not None or getattr(self, "kv4", None) is not None:
             raise ValueError("this decoder attends KV8 / KV4 pages quantised before: prefill first, "
                              "then use_kv8 / use_kv4")
         q_t = chunk.append(k_new, v_new, [(self.kind, self.lp, self.meta)], rotary, q, stream)
-        return chunk.attend(q_t, self.scale, stream=stream)
+        return chunk.attend_all(q_t, self.scale, stream)
 
     def use_kv8(self, stream=None):
         """Attends over KV8 pages from now on (the pools are quantised once, here, and prefill is
@@ -347,10 +354,10 @@ class ThresholdDecoder:
 
     def prefill(self, chunk: Chunk, q, k_new, v_new, rotary=None, stream=None):
         """Appends a planned chunk (prompts, or pieces of them), keeping this decoder's metadata
-        current, and attends it over the whole cache: (out bf16, m, l)."""
+        current, and attends it over the whole cache (every head): (out bf16, m, l)."""
         q_t = chunk.append(k_new, v_new, [(B.DSA_META_MEAN, self.cache.page_size, self.meta)], rotary, q,
                            stream)
-        return chunk.attend(q_t, self.scale, stream=stream)
+        return chunk.attend_all(q_t, self.scale, stream)
 
     def step(self, q, stream=None):
         c = self.cache
@@ -467,13 +474,13 @@ class PRRDecoder:
 
     def prefill(self, chunk: Chunk, q, k_new, v_new, rotary=None, stream=None):
         """Appends a planned chunk (prompts, or pieces of them), keeping this decoder's metadata
-        current, and attends it over the whole cache: (out bf16, m, l).  The predictor starts anew on
-        the pages that hold the chunk's tokens alone: what it knew of their positions belongs to tokens
-        dropped since, or to a request whose row this one took over."""
+        current, and attends it over the whole cache (every head): (out bf16, m, l).  The
+        predictor starts anew on the pages that hold the chunk's tokens alone: what it knew of their
+        positions belongs to tokens dropped since, or to a request whose row this one took over."""
         q_t = chunk.append(k_new, v_new, [(B.DSA_META_MINMAX, self.cache.page_size, self.meta)], rotary, q,
                            stream)
         self._forget(chunk, stream)
-        return chunk.attend(q_t, self.scale, stream=stream)
+        return chunk.attend_all(q_t, self.scale, stream)
 
     def _forget(self, chunk: Chunk, stream=None):
         """Resets level and trend of the pages that a prefilled request's older tokens do not reach,

@@ -760,3 +760,31 @@ def test_prr_step_after_a_request_took_over_a_row(fused):
     for x, y in zip((dec.out, dec.m, dec.l), want):
         assert (x[0] - y[0]).abs().max() <= 2.0 ** -7 * 4.5
     assert ((dec.l[0] - want[2][0]).abs() <= 2.0 ** -18 * want[2][0] * 64).all()
+
+
+@pytest.mark.parametrize("name", ["topk", "threshold", "prr"])
+def test_prefill_without_windows_attends_every_head(name):
+    """Decoders that know no window prefill streaming heads over the whole cache as well: the rows of a
+    cache without the marks, bit for bit."""
+    from dynamic_block_sparse_gb300.pipeline import (Cache, Chunk, PRRDecoder, ThresholdDecoder,
+                                                     TopKDecoder)
+    make = {"topk": lambda c: TopKDecoder(c, 4), "threshold": lambda c: ThresholdDecoder(c, 0.9, 8),
+            "prr": lambda c: PRRDecoder(c, 4, 6, 0.3, 0.2, 0.5)}[name]
+    hq, hkv, p, T = 8, 2, 32, 300
+    g = torch.Generator().manual_seed(7)
+    new = [torch.randn(T, h, 128, generator=g).bfloat16().cuda() for h in (hq, hkv, hkv)]
+    got = []
+    for marks in (None, [0, 1], [0, 0], [1, 1]):
+        k = torch.zeros(20, hkv, p, 128, dtype=torch.bfloat16, device="cuda")
+        cache = Cache(k, k.clone(), torch.full((2, 9), -1, dtype=I32, device="cuda"),
+                      torch.zeros(2, dtype=I32, device="cuda"), hq,
+                      None if marks is None else _t(marks, torch.uint8))
+        chunk = Chunk(cache, T, free_pages=torch.arange(20, dtype=I32, device="cuda"))
+        chunk.plan(_t([200, 100]))
+        got.append(make(cache).prefill(chunk, *new))
+        torch.cuda.synchronize()
+        assert int(cache.status) == 0
+    assert (got[0][2] >= 1 - 2.0 ** -18).all()  # (the largest logit adds 1)
+    for x in got[1:]:
+        for a, b in zip(x, got[0]):
+            assert torch.equal(a, b)

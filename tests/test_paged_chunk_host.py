@@ -289,3 +289,33 @@ def test_the_predictor_forgets_pages_a_prefill_filled():
         assert torch.equal(dec.trend[b, :, :kept], trend[b, :, :kept])
         assert (dec.ell[b, :, kept:] == -math.inf).all() and (dec.trend[b, :, kept:] == 0).all()
     assert dec.spec_count.tolist() == [[3] * 2, [1] * 2, [0] * 2, [2] * 2, [4] * 2]
+
+
+@pytest.mark.parametrize("name", ["TopKDecoder", "ThresholdDecoder", "PRRDecoder"])
+def test_prefill_without_a_window_covers_the_cache(name):
+    """These decoders have no sink and window to give: their prefill lets streaming heads see the whole
+    cache, as its documentation says, instead of nothing."""
+    import types
+
+    from dynamic_block_sparse_gb300 import pipeline
+    seen = {}
+
+    class Chunk(pipeline.Chunk):
+        def __init__(self, cache):
+            self.cache = cache
+
+        def append(self, *a):
+            return "q"
+
+        def attend(self, q, scale, sink=0, local=0, stream=None):
+            seen.update(q=q, sink=sink, local=local)
+            return "answer"
+
+    cls = getattr(pipeline, name)
+    dec = object.__new__(cls)
+    dec.cache = types.SimpleNamespace(page_size=16, max_pages=9)
+    dec.kind = dec.lp = dec.meta = None
+    dec.scale = 1.0
+    dec._forget = lambda *a: None
+    assert dec.prefill(Chunk(dec.cache), None, None, None) == "answer"
+    assert seen == dict(q="q", sink=144, local=0)
