@@ -246,10 +246,12 @@ DSA_DEV Pair pair_add(float ch, float cl, const Pair& p) {  // |ch| >= |p|
 DSA_DEV float2 cos_sin_turn(unsigned long long turn) {
   const unsigned q = static_cast<unsigned>((turn + (1ull << 61)) >> 62);  // nearest quarter
   const long long r = static_cast<long long>(turn - (static_cast<unsigned long long>(q) << 62));
-  // r as the exact sum of 24 + 32 bits (what is dropped is below 2^-56 of a turn)
+  // r from its 24, 24 and 16 bits, each exact in a float; the second sum matters where the first one
+  // cancels (a small negative r has -2^40 there), and its error is below 2^-47 of r
   const float rh = static_cast<float>(static_cast<int>(r >> 40)) * 1099511627776.f;
-  const float rl = static_cast<float>(static_cast<unsigned>(r >> 8)) * 256.f;
-  const Pair t = pair_sum(rh, rl);
+  const float rm = static_cast<float>(static_cast<unsigned>(r >> 16) & 0xffffffu) * 65536.f;
+  Pair t = pair_sum(rh, rm);
+  t = pair_sum(t.h, __fadd_rn(t.l, static_cast<float>(static_cast<unsigned>(r) & 0xffffu)));
   // theta = r * 2 pi / 2^64
   constexpr float kTurnH = 3.4061217e-19f, kTurnL = -9.4783964e-27f;
   float th = __fmul_rn(t.h, kTurnH);

@@ -251,6 +251,36 @@ def test_append_chunk_in_place_and_bad_pages():
             assert torch.equal(c.k[ph].view(torch.int16), k0[ph].view(torch.int16))
 
 
+@pytest.mark.parametrize("sign", [1, -1])
+def test_append_turns_small_angles_to_the_last_bit(sign):
+    """Angles of 2^-36 to 2^-22 of a turn on both sides of zero, where the sine alone decides the value:
+    one half of every pair is zero, so the other half's place gets y sin.  The sine is off by 2^-24 of
+    itself at most and the product by as much, so the stored value is the rounding of the exact one, or
+    of what lies 2^-22 of it away."""
+    n, p = 40, 16
+    phase = [int(2 ** (28 + i * 14 / 64) / n) | 1 for i in range(64)]
+    k, v = (torch.zeros(3, 1, p, 128, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    new = torch.randn(n, 1, 128, generator=torch.Generator().manual_seed(1)).bfloat16().cuda()
+    new[..., :64] = 0
+    status = torch.zeros(1, dtype=I32, device="cuda")
+    table, lens = _t([[0, 1, 2]]), _t([n])
+    kv = B.paged_kv(k, v, table, lens, 1, None, status)
+    rot = B.rotary(torch.tensor(phase, dtype=torch.int64, device="cuda"), 128,
+                   positions=_t([[sign * (i + 1) for i in range(n)]]))
+    chunk = B.chunk(_t([0, n]), _t([n]), _t([0] * n), _t(list(range(n))))
+    B.dsa_append_chunk(kv, chunk, new, new, rot)
+    torch.cuda.synchronize()
+    assert int(status) == 0
+    got = k.reshape(-1, 128)[:n].cpu()
+    pos = np.array([sign * (i + 1) for i in range(n)], dtype=np.float64)[:, None]
+    exact = -new[:, 0, 64:].double().cpu().numpy() * np.sin(
+        pos * np.array(phase, dtype=np.float64) * (2 * np.pi / 2.0 ** 64))
+    near = [torch.tensor(exact * (1 + e)).bfloat16() for e in (-2.0 ** -22, 2.0 ** -22)]
+    assert ((got[:, :64] == near[0]) | (got[:, :64] == near[1])).all()
+    # (the cosine is 1 there to far below 2^-24)
+    assert torch.equal(got[:, 64:], new[:, 0, 64:].cpu())
+
+
 # ----------------------------------------------------------------------------------------- attention
 
 def _attend(c, scale=SCALE, sink=0, local=0, ws=None, stream=None):
@@ -731,11 +761,12 @@ def test_prr_step_after_a_request_took_over_a_row(fused):
     cache = Cache(pool, pool.clone(), torch.full((2, 80), -1, dtype=I32, device="cuda"),
                   torch.zeros(2, dtype=I32, device="cuda"), hq)
     dec = PRRDecoder(cache, k, 6, 0.3, 0.2, 0.5, superset=True, fused=fused)
-    chunk = Chunk(cache, 1000, free_pages=torch.arange(200, dtype=I32, device="cuda"))
-    new = lambda: [torch.randn(1000, h, 128, device="cuda").bfloat16() for h in (hq, hkv, hkv)]
+    chunk = Chunk(cache, 1400, free_pages=torch.arange(200, dtype=I32, device="cuda"))
+    new = lambda: [torch.randn(1400, h, 128, device="cuda").bfloat16() for h in (hq, hkv, hkv)]
     query = lambda: torch.randn(2, hq, 128, device="cuda").bfloat16()
     chunk.plan(_t([900, 500]))
     dec.prefill(chunk, *new())
+    assert chunk.count.tolist() == [900, 500]
     for _ in range(3):
         dec.step(query())
     chunk.plan(_t([-900, 0]))
