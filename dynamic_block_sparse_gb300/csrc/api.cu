@@ -147,6 +147,31 @@ int query_map(const void* q, const KvView& v, int tokens, CUtensorMap* map) {
   return encode_map(map, q, 4, dims, strides, box);
 }
 
+// A span of memory that a call reads or writes.
+struct Span {
+  const char* what;
+  const void* at;
+  unsigned long long bytes;
+};
+
+// Fails where one of the `nw` written spans meets another written one or a read one (the CTAs of a
+// launch read and write in any order).
+int check_apart(const Span* written, int nw, const Span* read, int nr) {
+  auto meet = [](const Span& a, const Span& b) {
+    const auto x = reinterpret_cast<uintptr_t>(a.at), y = reinterpret_cast<uintptr_t>(b.at);
+    return a.at && b.at && x < y + b.bytes && y < x + a.bytes && a.bytes > 0 && b.bytes > 0;
+  };
+  for (int i = 0; i < nw; ++i) {
+    for (int j = i + 1; j < nw; ++j)
+      if (meet(written[i], written[j]))
+        return fail(DSA_ERR_INVALID_ARG, "%s and %s overlap", written[i].what, written[j].what);
+    for (int j = 0; j < nr; ++j)
+      if (meet(written[i], read[j]))
+        return fail(DSA_ERR_INVALID_ARG, "%s and %s overlap", written[i].what, read[j].what);
+  }
+  return DSA_OK;
+}
+
 // Positions of a request, and a tile more, count in 32 bits in the kernels of a chunk.
 int check_positions(const KvView& v) {
   if (static_cast<long long>(v.p) * v.max_pages > (1LL << 31) - 1024)
@@ -1028,6 +1053,22 @@ int dsa_plan_chunk(const dsa_paged_kv* kv, const int32_t* lens_in, const int32_t
   if (!workspace || workspace_bytes < dsa_plan_chunk_workspace_size(v.B))
     return fail(DSA_ERR_WORKSPACE, "dsa_plan_chunk: workspace too small");
   if (!aligned(workspace, 16)) return fail(DSA_ERR_ALIGNMENT, "workspace must be 16-byte aligned");
+  const unsigned long long word = sizeof(int32_t), batch = v.B * word, axis = chunk->tokens * word;
+  const Span written[] = {{"page_table", kv->page_table, batch * v.max_pages},
+                          {"seq_lens", kv->seq_lens, batch},
+                          {"free_pages", free_pages, free_capacity * word},
+                          {"free_out", free_out, word},
+                          {"start", chunk->start, batch + word},
+                          {"count", chunk->count, batch},
+                          {"row", chunk->row, axis},
+                          {"pos", chunk->pos, axis},
+                          {"slot", chunk->slot, axis},
+                          {"workspace", workspace, dsa_plan_chunk_workspace_size(v.B)}};
+  // lengths and stack height may be updated in place
+  const Span read[] = {{"delta", delta, batch},
+                       {"lens_in", lens_in == kv->seq_lens ? nullptr : lens_in, batch},
+                       {"free_in", free_in == free_out ? nullptr : free_in, word}};
+  if ((rc = check_apart(written, 10, read, 3))) return rc;
   PlanArgs a;
   a.B = v.B;
   a.p = v.p;
@@ -1102,6 +1143,14 @@ int dsa_append_chunk(const dsa_paged_kv* kv, const dsa_chunk* chunk, const void*
                   v.p);
     if (!aligned(meta, 16)) return fail(DSA_ERR_ALIGNMENT, "meta must be 16-byte aligned");
   }
+  if (q) {
+    const int64_t q_row = static_cast<int64_t>(v.Hq) * kHeadDim, last = chunk->tokens - 1;
+    const Span written[] = {{"q_out", q_out, (last * q_row + q_row) * 2ull}};
+    const Span read[] = {{"q", q == q_out ? nullptr : q, (last * q_stride + q_row) * 2ull},
+                         {"k_new", k_new, (last * k_stride + kv_row) * 2ull},
+                         {"v_new", v_new, (last * v_stride + kv_row) * 2ull}};
+    if ((rc = check_apart(written, 1, read, 3))) return rc;
+  }
   AppendArgs a = {};
   a.kv = v;
   a.k_pages = static_cast<__nv_bfloat16*>(const_cast<void*>(kv->k_pages));
@@ -1172,6 +1221,13 @@ int dsa_chunk_attn(const dsa_paged_kv* kv, const dsa_chunk* chunk, const void* q
   if (!workspace || workspace_bytes < w.total)
     return fail(DSA_ERR_WORKSPACE, "dsa_chunk_attn: workspace too small");
   if (!aligned(workspace, 16)) return fail(DSA_ERR_ALIGNMENT, "workspace must be 16-byte aligned");
+  const unsigned long long heads = static_cast<unsigned long long>(chunk->tokens) * v.Hq;
+  const Span written[] = {{"out", out, heads * kHeadDim * 2},
+                          {"m", m, heads * sizeof(float)},
+                          {"l", l, heads * sizeof(float)},
+                          {"workspace", workspace, w.total}};
+  const Span read[] = {{"q", q, heads * kHeadDim * 2}};
+  if ((rc = check_apart(written, 4, read, 1))) return rc;
   CUtensorMap tq, tk, tv;
   const int piece = v.p % 128 == 0 ? 128 : v.p % 64 == 0 ? 64 : v.p % 32 == 0 ? 32 : 16;
   if ((rc = query_map(q, v, chunk->tokens, &tq)) || (rc = piece_map(kv->k_pages, v, piece, &tk)) ||

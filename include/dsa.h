@@ -539,6 +539,7 @@ typedef struct dsa_chunk {
  *                completed call leaves it zero-filled).
  * The metadata of the page that now ends a shortened request still covers the dropped tokens (a
  * looser bound, a mean with them) until tokens are appended to it.
+ * What is written may overlap neither each other nor what is read, but for the two pairs above.
  * batch <= 8192; p * max_pages_per_seq <= 2^31 - 1024.
  */
 int dsa_plan_chunk(const dsa_paged_kv* kv, const int32_t* lens_in, const int32_t* delta,
@@ -578,7 +579,8 @@ typedef struct dsa_rotary {
  *                  Hkv * D and a multiple of 8 (slices of one fused projection); 16-byte aligned.
  *   rotary       : NULL: q and k are taken as they are.
  *   q, q_out     : NULL, or the queries (same form, Hq heads) and bf16 [tokens][Hq][D] for the turned
- *                  ones (may be q itself when that is contiguous).
+ *                  ones (may be q itself when that is contiguous; otherwise it may overlap none of q,
+ *                  k_new and v_new).
  *   meta         : as for dsa_append_kv, or NULL.  A caller keeping several metadata buffers calls
  *                  once per buffer, with q NULL after the first (turning q in place twice would turn
  *                  it twice; the KV write repeats harmlessly).
@@ -599,9 +601,10 @@ int dsa_append_chunk(const dsa_paged_kv* kv, const dsa_chunk* chunk, const void*
  * kv->seq_lens counts the chunk and its keys and values are in their pages; the queries of request b
  * are its last count[b] positions.
  *   q   : bf16 [tokens][Hq][D], 16-byte aligned.  scale must be positive and finite.
- *   out : bf16 [tokens][Hq][D], 16-byte aligned; may not overlap q.  m, l: fp32 [tokens][Hq] or NULL
- *         (m the maximal logit, l the sum of exp(s - m)).  A query that sees no token gets O = 0,
- *         m = -inf, l = 0.  Rows of tokens that take no part are left as they are.
+ *   out : bf16 [tokens][Hq][D], 16-byte aligned.  m, l: fp32 [tokens][Hq] or NULL (m the maximal
+ *         logit, l the sum of exp(s - m)).  A query that sees no token gets O = 0, m = -inf, l = 0.
+ *         Rows of tokens that take no part are left as they are.  out, m, l and the workspace may
+ *         overlap neither each other nor q.
  *   workspace : dsa_chunk_attn_workspace_size(kv, tokens) bytes, 16-byte aligned, ZERO-FILLED before
  *               the first use (each completed call leaves the words it counts with at zero; zero-fill
  *               it again after DSA_STATUS_TIMEOUT).  Calls that share a workspace must be ordered

@@ -319,3 +319,42 @@ def test_prefill_without_a_window_covers_the_cache(name):
     dec._forget = lambda *a: None
     assert dec.prefill(Chunk(dec.cache), None, None, None) == "answer"
     assert seen == dict(q="q", sink=144, local=0)
+
+
+def test_overlapping_arguments_are_refused(lib):
+    """An output that shares memory with an input or another output: the CTAs of a launch would read
+    what others have written."""
+    from dynamic_block_sparse_gb300 import binding as B
+    at = lambda i: (1 << 32) + (i << 24)  # 16 MB apart
+    kv = _kv(k_pages=at(30), v_pages=at(31), page_table=at(0), seq_lens=at(1))
+
+    def refused(rc):
+        return rc == -1 and b"overlap" in lib.dsa_last_error()
+
+    def plan(**kw):
+        a = dict(lens=at(2), delta=at(3), free=at(4), fin=at(5), fout=at(6), start=at(7), count=at(8),
+                 row=at(9), pos=at(10), slot=at(11), ws=at(12))
+        a.update(kw)
+        c = _chunk(16, **{k: a[k] for k in ("start", "count", "row", "pos", "slot")})
+        return lib.dsa_plan_chunk(ctypes.byref(kv), a["lens"], a["delta"], a["free"], 16, a["fin"],
+                                  a["fout"], ctypes.byref(c), a["ws"], 16, None)
+    for bad in (dict(delta=at(8)), dict(delta=at(8) + 4), dict(delta=at(1)), dict(lens=at(8)),
+                dict(lens=at(1) + 4), dict(lens=at(9) + 60), dict(fin=at(4)), dict(pos=at(9)),
+                dict(slot=at(9) + 32), dict(row=at(7) + 8), dict(free=at(0)), dict(fout=at(1)),
+                dict(delta=at(12)), dict(count=at(7) - 4)):
+        assert refused(plan(**bad)), bad
+
+    def append(tokens=16, k=at(2), v=at(3), q=at(4), qs=1024, qo=at(5), ks=256):
+        return lib.dsa_append_chunk(ctypes.byref(kv), ctypes.byref(_chunk(tokens)), k, ks, v, 256, None,
+                                    q, qs, qo, 0, 16, None, None)
+    assert refused(append(qo=at(4) + 16)) and refused(append(qo=at(2))) and refused(append(qo=at(3)))
+    assert refused(append(qo=at(4) + 16 * 2048 - 16)) and refused(append(qo=at(2) - 16 * 2048 + 16))
+    # slices of one projection of 13 heads, q_out over the last token's k
+    assert refused(append(q=at(4), qs=1664, k=at(4) + 2048, ks=1664, qo=at(4) + 15 * 3328 + 2544))
+
+    def attend(q=at(2), out=at(3), m=at(4), l=at(5), ws=at(6)):
+        return lib.dsa_chunk_attn(ctypes.byref(kv), ctypes.byref(_chunk(16)), q, 0, 0, 0.1, out, m, l,
+                                  ws, 1 << 30, None)
+    for bad in (dict(out=at(2) + 16), dict(out=at(2) - 16), dict(m=at(2)), dict(l=at(3) + 32764),
+                dict(m=at(5)), dict(ws=at(2) - 4096), dict(l=at(6)), dict(l=at(4) + 508)):
+        assert refused(attend(**bad)), bad
