@@ -164,11 +164,15 @@ def _io_ptr(t) -> int:
     raise ValueError("tensor must live on a CUDA device or in page-locked host memory")
 
 
+# The current device and its stream's handle alone: building the torch.cuda.Stream object takes as long
+# as the library call itself.  Where a torch lacks these two, its public calls serve.
+_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda device: torch.cuda.current_stream(device).cuda_stream)
+
+
 def _stream(stream) -> int | None:
-    if stream is None:
-        # the handle alone: building the Stream object takes as long as the library call itself
-        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
-    return stream.cuda_stream
+    return _raw_stream(_device()) if stream is None else stream.cuda_stream
 
 
 def _check(name: str, rc: int) -> None:
@@ -576,9 +580,8 @@ def dsa_plan_chunk(kv: PagedKV, lens_in, delta, free_pages, free_in, free_out, c
 
 def _here(t, what: str) -> None:
     """Kernels run on the current device: a tensor of another one is refused."""
-    if t.is_cuda and t.get_device() != torch._C._cuda_getDevice():
-        raise ValueError(f"{what} is on {t.device}, the current device is "
-                         f"cuda:{torch._C._cuda_getDevice()}")
+    if t.is_cuda and t.get_device() != _device():
+        raise ValueError(f"{what} is on {t.device}, the current device is cuda:{_device()}")
 
 
 def _token_rows(t, tokens: int, heads: int, what: str) -> int:

@@ -358,3 +358,19 @@ def test_overlapping_arguments_are_refused(lib):
     for bad in (dict(out=at(2) + 16), dict(out=at(2) - 16), dict(m=at(2)), dict(l=at(3) + 32764),
                 dict(m=at(5)), dict(ws=at(2) - 4096), dict(l=at(6)), dict(l=at(4) + 508)):
         assert refused(attend(**bad)), bad
+
+
+def test_current_stream_without_the_short_cuts():
+    """The stream's handle comes from torch's public calls where torch has no shorter ones."""
+    import sys
+    code = """
+import types, torch
+for name in ("_cuda_getDevice", "_cuda_getCurrentRawStream"):
+    if hasattr(torch._C, name):
+        delattr(torch._C, name)
+torch.cuda.current_device = lambda: 3
+torch.cuda.current_stream = lambda device=None: types.SimpleNamespace(cuda_stream=100 + (device or 0))
+from dynamic_block_sparse_gb300 import binding as B
+assert B._stream(None) in (100, 103) and B._stream(types.SimpleNamespace(cuda_stream=7)) == 7
+"""
+    subprocess.run([sys.executable, "-c", code], check=True, cwd=ROOT)
