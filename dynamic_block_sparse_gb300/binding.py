@@ -156,6 +156,37 @@ def _ptr(t) -> int | None:
     return t.data_ptr()
 
 
+def _current() -> int:
+    """The current CUDA device; -2, the device of no tensor, before CUDA is in use."""
+    return _device() if torch.cuda.is_initialized() else -2
+
+
+def _on(t, here: int) -> int | None:
+    """``_ptr`` of a tensor on the current device, where the kernel will run."""
+    if t is None:
+        return None
+    if t.get_device() != here:
+        raise ValueError(f"tensor must live on the current CUDA device ({here}), got {t.device}")
+    return t.data_ptr()
+
+
+def _where(*tensors) -> int:
+    """The device of a descriptor's tensors (None left out)."""
+    devices = {t.get_device() for t in tensors if t is not None}
+    if len(devices) > 1:
+        raise ValueError(f"a descriptor's tensors must be on one device, got {sorted(devices)}")
+    return devices.pop()
+
+
+def _desc(d, here: int):
+    """A descriptor by reference, its tensors on the current device."""
+    if d is None:
+        return None
+    if getattr(d, "where", here) != here:
+        raise ValueError(f"{type(d).__name__} is on device {d.where}, the current CUDA device is {here}")
+    return ctypes.byref(d)
+
+
 def _io_ptr(t) -> int:
     """A CUDA tensor, or a page-locked host tensor the device reads or writes over the host link
     (the fused PRR step's query and result)."""
@@ -208,6 +239,7 @@ def paged_kv(k_pages, v_pages, page_table, seq_lens, num_q_heads: int,
     kv.page_size = page
     kv.max_pages_per_seq = page_table.shape[1]
     kv.num_phys_pages = P
+    kv.where = _where(k_pages, v_pages, page_table, seq_lens, head_is_streaming, status)
     return kv
 
 
@@ -482,14 +514,15 @@ def dsa_prr_step(kv: PagedKV, q, meta, scores, ell, trend, alpha: float, beta: f
 
 # ------------------------------------------------------------------------------ chunks of tokens
 
-def _i32(t, shape, what: str, optional: bool = False):
-    """A contiguous int32 CUDA tensor of the given shape (or None), else a ValueError."""
+def _i32(t, shape, what: str, optional: bool = False, here: int | None = None):
+    """A contiguous int32 CUDA tensor of the given shape (or None), on device ``here`` if that is
+    given, else a ValueError."""
     if t is None and optional:
         return None
     if t.dtype is not torch.int32 or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{what} must be a contiguous int32 tensor of shape {shape}, got "
                          f"{t.dtype} {tuple(t.shape)}")
-    return _ptr(t)
+    return _ptr(t) if here is None else _on(t, here)
 
 
 def page_tables(page_table, seq_lens, page_size: int, num_phys_pages: int, status=None) -> PagedKV:
@@ -503,6 +536,7 @@ def page_tables(page_table, seq_lens, page_size: int, num_phys_pages: int, statu
     kv.num_q_heads = kv.num_kv_heads = 1
     kv.head_dim, kv.page_size, kv.num_phys_pages = 128, page_size, num_phys_pages
     kv.tensors = (page_table, seq_lens, status)  # kept alive with the descriptor
+    kv.where = _where(*kv.tensors)
     return kv
 
 
@@ -521,6 +555,7 @@ def chunk(start, count, row=None, pos=None, slot=None, tokens: int | None = None
     c.tokens = n
     c.batch = batch
     c.tensors = (start, count, row, pos, slot)  # kept alive with the descriptor
+    c.where = _where(*c.tensors)
     return c
 
 
@@ -547,6 +582,7 @@ def rotary(phase, rot_dim: int, axis=None, positions=None, interleaved: bool = F
     r = Rotary()
     r.phase, r.axis = _ptr(phase), _ptr(axis)
     r.tensors = (phase, axis, positions)  # kept alive with the descriptor
+    r.where = _where(*r.tensors)
     r.num_axes = 1
     r.tokens = None
     if positions is not None:
@@ -569,19 +605,13 @@ def dsa_plan_chunk(kv: PagedKV, lens_in, delta, free_pages, free_in, free_out, c
     rows = (kv.batch,)
     if chunk.batch != kv.batch:
         raise ValueError(f"the chunk holds {chunk.batch} requests, the tables {kv.batch}")
-    n = free_pages.numel()
-    _here(delta, "delta")
+    n, here = free_pages.numel(), _current()
+    i32 = lambda t, shape, what: _i32(t, shape, what, False, here)
     _check("dsa_plan_chunk", load().dsa_plan_chunk(
-        ctypes.byref(kv), _i32(lens_in, rows, "lens_in"), _i32(delta, rows, "delta"),
-        _i32(free_pages, (n,), "free_pages"), n, _i32(free_in, (1,), "free_in"),
-        _i32(free_out, (1,), "free_out"), ctypes.byref(chunk), _ptr(workspace), workspace.nbytes,
+        _desc(kv, here), i32(lens_in, rows, "lens_in"), i32(delta, rows, "delta"),
+        i32(free_pages, (n,), "free_pages"), n, i32(free_in, (1,), "free_in"),
+        i32(free_out, (1,), "free_out"), _desc(chunk, here), _on(workspace, here), workspace.nbytes,
         _stream(stream)))
-
-
-def _here(t, what: str) -> None:
-    """Kernels run on the current device: a tensor of another one is refused."""
-    if t.is_cuda and t.get_device() != _device():
-        raise ValueError(f"{what} is on {t.device}, the current device is cuda:{_device()}")
 
 
 def _token_rows(t, tokens: int, heads: int, what: str) -> int:
@@ -602,8 +632,7 @@ def dsa_append_chunk(kv: PagedKV, chunk: Chunk, k_new, v_new, rotary: Rotary | N
     """Turns the chunk's keys (and queries, into ``q_out``), writes keys and values into their pages
     and renews the metadata of every touched page in ``meta`` (if given).  ``k_new``, ``v_new`` and
     ``q`` are bf16 ``[tokens][heads][128]`` and may be slices of one projection."""
-    n = chunk.tokens
-    _here(k_new, "k_new")
+    n, here = chunk.tokens, _current()
     if chunk.batch != kv.batch:
         raise ValueError(f"the chunk holds {chunk.batch} requests, the cache {kv.batch}")
     if rotary is not None and rotary.tokens is not None and rotary.tokens != n:
@@ -618,11 +647,10 @@ def dsa_append_chunk(kv: PagedKV, chunk: Chunk, k_new, v_new, rotary: Rotary | N
         if _token_rows(q_out, n, kv.num_q_heads, "q_out") != kv.num_q_heads * 128:
             raise ValueError("q_out must be contiguous")
     _check("dsa_append_chunk", load().dsa_append_chunk(
-        ctypes.byref(kv), ctypes.byref(chunk), _ptr(k_new),
-        _token_rows(k_new, n, kv.num_kv_heads, "k_new"), _ptr(v_new),
-        _token_rows(v_new, n, kv.num_kv_heads, "v_new"),
-        None if rotary is None else ctypes.byref(rotary), _ptr(q), qs, _ptr(q_out), meta_kind,
-        logical_page, _ptr(meta), _stream(stream)))
+        _desc(kv, here), _desc(chunk, here), _on(k_new, here),
+        _token_rows(k_new, n, kv.num_kv_heads, "k_new"), _on(v_new, here),
+        _token_rows(v_new, n, kv.num_kv_heads, "v_new"), _desc(rotary, here), _on(q, here), qs,
+        _on(q_out, here), meta_kind, logical_page, _on(meta, here), _stream(stream)))
 
 
 def dsa_chunk_attn_workspace_size(kv: PagedKV, tokens: int) -> int:
@@ -634,8 +662,7 @@ def dsa_chunk_attn(kv: PagedKV, chunk: Chunk, q, scale: float, out, m=None, l=No
     """Attention of a chunk over the paged cache: causal on dense KV heads, sink + local window on
     those marked streaming.  ``q`` and ``out`` bf16 ``[tokens][Hq][128]``, ``m`` and ``l`` fp32
     ``[tokens][Hq]`` or None."""
-    n, hq = chunk.tokens, kv.num_q_heads
-    _here(q, "q")
+    n, hq, here = chunk.tokens, kv.num_q_heads, _current()
     if chunk.batch != kv.batch:
         raise ValueError(f"the chunk holds {chunk.batch} requests, the cache {kv.batch}")
     for t, what in ((q, "q"), (out, "out")):
@@ -646,6 +673,6 @@ def dsa_chunk_attn(kv: PagedKV, chunk: Chunk, q, scale: float, out, m=None, l=No
                               or not t.is_contiguous()):
             raise ValueError(f"{what} must be contiguous fp32 [{n}][{hq}]")
     _check("dsa_chunk_attn", load().dsa_chunk_attn(
-        ctypes.byref(kv), ctypes.byref(chunk), _ptr(q), sink, local, scale, _ptr(out), _ptr(m),
-        _ptr(l), _ptr(workspace),
+        _desc(kv, here), _desc(chunk, here), _on(q, here), sink, local, scale, _on(out, here),
+        _on(m, here), _on(l, here), _on(workspace, here),
         0 if workspace is None else workspace.nbytes, _stream(stream)))

@@ -374,3 +374,77 @@ from dynamic_block_sparse_gb300 import binding as B
 assert B._stream(None) in (100, 103) and B._stream(types.SimpleNamespace(cuda_stream=7)) == 7
 """
     subprocess.run([sys.executable, "-c", code], check=True, cwd=ROOT)
+
+
+class _OnDevice:
+    """A tensor's look on a CUDA device that is not there."""
+
+    def __init__(self, t, device: int):
+        self.t, self.dtype, self.shape, self.nbytes = t, t.dtype, t.shape, t.nbytes
+        self.device, self.is_cuda = torch.device("cuda", device), True
+
+    def get_device(self):
+        return self.device.index
+
+    def data_ptr(self):
+        return 1 << 32
+
+    def is_contiguous(self):
+        return True
+
+    def contiguous(self):
+        return self
+
+    def numel(self):
+        return self.t.numel()
+
+
+def test_tensors_of_another_device_are_refused(lib, monkeypatch):
+    """Every tensor of the three calls, those of the descriptors among them, has to be on the current
+    device: a kernel there could not read it."""
+    import types
+
+    from dynamic_block_sparse_gb300 import binding as B
+    monkeypatch.setattr(torch.cuda, "is_initialized", lambda: True)
+    monkeypatch.setattr(B, "_device", lambda: 0)
+    calls = []
+    ran = types.SimpleNamespace(**{n: lambda *a, n=n: calls.append(n) or 0 for n in (
+        "dsa_plan_chunk", "dsa_append_chunk", "dsa_chunk_attn")})
+    monkeypatch.setattr(B, "load", lambda: ran)
+    T, bf = 6, torch.bfloat16
+    i32 = lambda *s: torch.zeros(s, dtype=torch.int32)
+    rows = lambda h: torch.zeros(T, h, 128, dtype=bf)
+    stream = types.SimpleNamespace(cuda_stream=1)
+
+    def run(call, other=()):
+        d = lambda name, t: _OnDevice(t, 1 if name in other else 0)
+        pool = lambda n: d("kv", torch.zeros(4, 2, 16, 128, dtype=bf))
+        chunk = B.chunk(*(d("chunk", x) for x in (i32(3), i32(2), i32(T), i32(T))))
+        kv = B.paged_kv(pool(0), pool(1), d("kv", i32(2, 3)), d("kv", i32(2)), 4)
+        if call == "plan":
+            kv = B.page_tables(d("kv", i32(2, 3)), d("kv", i32(2)), 16, 4)
+            B.dsa_plan_chunk(kv, d("lens_in", i32(2)), d("delta", i32(2)), d("free_pages", i32(4)),
+                             d("free_in", i32(1)), d("free_out", i32(1)), chunk,
+                             d("workspace", i32(4)), stream)
+        elif call == "append":
+            rot = B.rotary(d("rotary", torch.zeros(64, dtype=torch.int64)), 128)
+            B.dsa_append_chunk(kv, chunk, d("k_new", rows(2)), d("v_new", rows(2)), rot,
+                               d("q", rows(4)), d("q_out", rows(4)), 0, 16,
+                               d("meta", torch.zeros(4 * 2 * 256, dtype=bf)), stream)
+        else:
+            f32 = torch.zeros(T, 4)
+            B.dsa_chunk_attn(kv, chunk, d("q", rows(4)), 0.1, d("out", rows(4)), d("m", f32),
+                             d("l", f32), d("workspace", i32(4)), 0, 0, stream)
+
+    names = {"plan": "kv chunk lens_in delta free_pages free_in free_out workspace",
+             "append": "kv chunk k_new v_new rotary q q_out meta", "attend": "kv chunk q out m l workspace"}
+    for call, args in names.items():
+        run(call)
+        assert len(calls) == 1
+        for name in args.split():
+            with pytest.raises(ValueError, match="current CUDA device"):
+                run(call, (name,))
+        assert len(calls) == 1, call
+        calls.clear()
+    with pytest.raises(ValueError, match="one device"):
+        B.chunk(_OnDevice(i32(3), 0), _OnDevice(i32(2), 1), tokens=4)
