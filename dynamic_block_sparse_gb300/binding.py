@@ -578,7 +578,7 @@ def rotary(phase, rot_dim: int, axis=None, positions=None, interleaved: bool = F
                          f"{tuple(phase.shape)}")
     if axis is not None and (axis.dtype != torch.uint8 or tuple(axis.shape) != (rot_dim // 2,)):
         raise ValueError(f"axis must be uint8 [{rot_dim // 2}]")
-    phase = phase.contiguous()
+    phase, axis = phase.contiguous(), None if axis is None else axis.contiguous()
     r = Rotary()
     r.phase, r.axis = _ptr(phase), _ptr(axis)
     r.tensors = (phase, axis, positions)  # kept alive with the descriptor

@@ -448,3 +448,14 @@ def test_tensors_of_another_device_are_refused(lib, monkeypatch):
         calls.clear()
     with pytest.raises(ValueError, match="one device"):
         B.chunk(_OnDevice(i32(3), 0), _OnDevice(i32(2), 1), tokens=4)
+
+
+def test_rotary_takes_strided_axes(monkeypatch):
+    """The axes of pairs may be a view: what the descriptor points to is their dense copy."""
+    from dynamic_block_sparse_gb300 import binding as B
+    monkeypatch.setattr(B, "_ptr", lambda t: None if t is None else t.data_ptr())
+    axis = (torch.arange(128, dtype=torch.uint8) % 3)[::2]
+    r = B.rotary(torch.arange(128, dtype=torch.int64)[::2], 128, axis,
+                 torch.zeros(3, 5, dtype=torch.int32))
+    assert (ctypes.c_uint8 * 64).from_address(r.axis)[:] == axis.tolist()
+    assert (ctypes.c_int64 * 64).from_address(r.phase)[:] == list(range(0, 128, 2))
