@@ -179,12 +179,23 @@ def _where(*tensors) -> int:
 
 
 def _desc(d, here: int):
-    """A descriptor by reference, its tensors on the current device."""
+    """A descriptor by reference, its tensors on the current device and as the library reads them."""
     if d is None:
         return None
+    if getattr(d, "fault", None):
+        raise ValueError(d.fault)
     if getattr(d, "where", here) != here:
         raise ValueError(f"{type(d).__name__} is on device {d.where}, the current CUDA device is {here}")
     return ctypes.byref(d)
+
+
+def _scratch(t, here: int) -> tuple[int | None, int]:
+    """Pointer and bytes of a workspace."""
+    if t is None:
+        return None, 0
+    if not t.is_contiguous():
+        raise ValueError("the workspace must be contiguous")
+    return _on(t, here), t.nbytes
 
 
 def _io_ptr(t) -> int:
@@ -240,6 +251,22 @@ def paged_kv(k_pages, v_pages, page_table, seq_lens, num_q_heads: int,
     kv.max_pages_per_seq = page_table.shape[1]
     kv.num_phys_pages = P
     kv.where = _where(k_pages, v_pages, page_table, seq_lens, head_is_streaming, status)
+    kv.fault = None  # why the calls that write the cache refuse it
+    named = dict(k_pages=k_pages, v_pages=v_pages, page_table=page_table, seq_lens=seq_lens,
+                 head_is_streaming=head_is_streaming, status=status)
+    for what, t in named.items():
+        if t is not None and not t.is_contiguous():
+            kv.fault = f"{what} must be contiguous"
+    if v_pages.dtype != torch.bfloat16:
+        kv.fault = f"v_pages must be bf16, got {v_pages.dtype}"
+    if tuple(seq_lens.shape) != (kv.batch,):
+        kv.fault = f"seq_lens must hold {kv.batch} lengths, got {tuple(seq_lens.shape)}"
+    mask = head_is_streaming
+    if mask is not None and (mask.dtype not in (torch.uint8, torch.int8, torch.bool)
+                             or tuple(mask.shape) != (Hkv,)):
+        kv.fault = f"head_is_streaming must hold {Hkv} bytes, got {mask.dtype} {tuple(mask.shape)}"
+    if status is not None and status.dtype != torch.int32:
+        kv.fault = f"status must be int32, got {status.dtype}"
     return kv
 
 
@@ -610,7 +637,7 @@ def dsa_plan_chunk(kv: PagedKV, lens_in, delta, free_pages, free_in, free_out, c
     _check("dsa_plan_chunk", load().dsa_plan_chunk(
         _desc(kv, here), i32(lens_in, rows, "lens_in"), i32(delta, rows, "delta"),
         i32(free_pages, (n,), "free_pages"), n, i32(free_in, (1,), "free_in"),
-        i32(free_out, (1,), "free_out"), _desc(chunk, here), _on(workspace, here), workspace.nbytes,
+        i32(free_out, (1,), "free_out"), _desc(chunk, here), *_scratch(workspace, here),
         _stream(stream)))
 
 
@@ -674,5 +701,4 @@ def dsa_chunk_attn(kv: PagedKV, chunk: Chunk, q, scale: float, out, m=None, l=No
             raise ValueError(f"{what} must be contiguous fp32 [{n}][{hq}]")
     _check("dsa_chunk_attn", load().dsa_chunk_attn(
         _desc(kv, here), _desc(chunk, here), _on(q, here), sink, local, scale, _on(out, here),
-        _on(m, here), _on(l, here), _on(workspace, here),
-        0 if workspace is None else workspace.nbytes, _stream(stream)))
+        _on(m, here), _on(l, here), *_scratch(workspace, here), _stream(stream)))

@@ -459,3 +459,49 @@ def test_rotary_takes_strided_axes(monkeypatch):
                  torch.zeros(3, 5, dtype=torch.int32))
     assert (ctypes.c_uint8 * 64).from_address(r.axis)[:] == axis.tolist()
     assert (ctypes.c_int64 * 64).from_address(r.phase)[:] == list(range(0, 128, 2))
+
+
+def test_a_cache_of_strided_or_other_tensors_is_refused(lib, monkeypatch):
+    """The library reads the cache's tensors as dense arrays of its types: a slice of a wider page table
+    would give each request another's pages."""
+    import types
+
+    from dynamic_block_sparse_gb300 import binding as B
+    monkeypatch.setattr(B, "_ptr", lambda t: None if t is None else t.data_ptr())
+    monkeypatch.setattr(B, "_on", lambda t, here: None if t is None else t.data_ptr())
+    monkeypatch.setattr(B, "_current", lambda: -1)
+    ran = []
+    monkeypatch.setattr(B, "load", lambda: types.SimpleNamespace(**{n: lambda *a: ran.append(a) or 0 for n in (
+        "dsa_append_chunk", "dsa_chunk_attn", "dsa_plan_chunk")}))
+    z = lambda *s, t=torch.int32: torch.zeros(s, dtype=t)
+    bf, u8, stream = torch.bfloat16, torch.uint8, types.SimpleNamespace(cuda_stream=1)
+    pool = lambda: z(4, 2, 16, 128, t=bf)
+    good = dict(k_pages=pool(), v_pages=pool(), page_table=z(2, 3), seq_lens=z(2), num_q_heads=4,
+                head_is_streaming=z(2, t=u8), status=z(1))
+    chunk = B.chunk(z(3), z(2), z(6), z(6))
+
+    def calls(kv):
+        yield lambda: B.dsa_plan_chunk(kv, z(2), z(2), z(4), z(1), z(1), chunk, z(4), stream)
+        yield lambda: B.dsa_append_chunk(kv, chunk, z(6, 2, 128, t=bf), z(6, 2, 128, t=bf), stream=stream)
+        yield lambda: B.dsa_chunk_attn(kv, chunk, z(6, 4, 128, t=bf), 0.1, z(6, 4, 128, t=bf),
+                                       workspace=z(4), stream=stream)
+
+    for call in calls(B.paged_kv(**good)):
+        call()
+    assert len(ran) == 3
+    for name, t in (("page_table", z(2, 6)[:, :3]), ("page_table", z(3, 2).t()), ("seq_lens", z(4)[::2]),
+                    ("seq_lens", z(1)), ("k_pages", z(4, 4, 16, 128, t=bf)[:, ::2]),
+                    ("v_pages", z(4, 2, 16, 256, t=bf)[..., ::2]),
+                    ("v_pages", z(4, 2, 16, 128, t=torch.float16)), ("head_is_streaming", z(2)),
+                    ("head_is_streaming", z(1, t=u8)), ("head_is_streaming", z(4, t=u8)[::2]),
+                    ("status", z(1, t=torch.int64))):
+        for call in calls(B.paged_kv(**{**good, name: t})):
+            with pytest.raises(ValueError, match=name):
+                call()
+    kv, ws = B.paged_kv(**good), z(1).expand(1 << 20)  # (many bytes by its shape, four in memory)
+    with pytest.raises(ValueError, match="workspace"):
+        B.dsa_plan_chunk(kv, z(2), z(2), z(4), z(1), z(1), chunk, ws, stream)
+    with pytest.raises(ValueError, match="workspace"):
+        B.dsa_chunk_attn(kv, chunk, z(6, 4, 128, t=bf), 0.1, z(6, 4, 128, t=bf), workspace=ws,
+                         stream=stream)
+    assert len(ran) == 3
