@@ -711,10 +711,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t dense_work = hd * total_d;
       const uint32_t work = fits ? dense_work + (kv.Hkv - hd) * total_s : 0;
       // Equal ranges: boundary c lies at c each + min(c, more), CTA c has what lies between boundaries c
-      // and c + 1.  A boundary that would cut less than `snap` off an item's start or end moves there:
-      // up to four tiles more or less, a sixteenth of a range, against a cut's record and merge (seven
-      // requests of 60 to 700 or one new tokens: 91 us, 95 without; a sixteenth whatever its length
-      // costs the chunk of 2048 tokens 2 %).
+      // and c + 1.  A boundary less than `snap` behind an item's start moves there: up to four tiles
+      // more or less, a sixteenth of a range, against a cut's record and merge (seven requests of 60 to
+      // 700 or one new tokens: 91 us, 95 without; a sixteenth whatever its length costs the chunk of
+      // 2048 tokens 2 %).  One near an item's end stays: in the pad it cuts nothing off, before it the
+      // item's last one to four tiles.
       const uint32_t ctas = min(gridDim.x, (work + kMinWork - 1) / kMinWork);
       const uint32_t each = ctas ? work / ctas : 0, more = work - each * ctas, c = blockIdx.x;
       const uint32_t wide_end = more * (each + 1), snap = max(min(each / 16, 4u), 1u);
@@ -806,14 +807,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int src = __ffs(above) - 1;
             at.i = i0 + src;
             const uint32_t k = r - __shfl_sync(0xffffffffu, end - cost, src);
-            const uint32_t whole = __shfl_sync(0xffffffffu, cost, src);
             at.k = static_cast<int>(k);
-            if (k > 0 && k < snap) {
+            if (k < snap) {
               x -= k;
               at.k = 0;
-            } else if (k > 0 && whole - k < snap) {
-              x += whole - k;  // nothing of it
-              at.k = static_cast<int>(whole);
             }
             break;
           }
@@ -834,7 +831,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         int take = cnt;  // tiles of the item before the range's end
         if (x1 < item1 && !whole_items) {
           if (x1 - item0 < snap) break;  // (it begins too near the end: the next CTA's)
-          if (item1 - x1 >= snap) take = min(cnt, static_cast<int>(x1 - item0));
+          take = min(cnt, static_cast<int>(x1 - item0));
         }
         const int b = at.b, h = at.h, len = at.base + at.n;
         if (at.k < take) {
@@ -861,7 +858,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!un.whole) {  // who has its first and its last tile
             const uint32_t o0 = owner(item0), o1 = owner(item0 + cnt - 1);
             un.cta0 = o0 + (boundary(o0 + 1) - item0 < snap);
-            un.cta1 = o1 - (item1 - boundary(o1) < snap);
+            un.cta1 = o1;
           }
           un.tok0 = tok0;
           // stream 0 of a pair ends at its own last token's tile
