@@ -157,8 +157,11 @@ def _ptr(t) -> int | None:
 
 
 def _current() -> int:
-    """The current CUDA device; -2, the device of no tensor, before CUDA is in use."""
-    return _device() if torch.cuda.is_initialized() else -2
+    """The current CUDA device; -2, the device of no tensor, where there is none."""
+    try:
+        return _device()
+    except RuntimeError:
+        return -2
 
 
 def _on(t, here: int) -> int | None:
@@ -215,6 +218,10 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
 
 def _stream(stream) -> int | None:
     return _raw_stream(_device()) if stream is None else stream.cuda_stream
+
+
+def _stream_on(stream, here: int) -> int | None:
+    return _raw_stream(here) if stream is None else stream.cuda_stream
 
 
 def _check(name: str, rc: int) -> None:
@@ -633,12 +640,12 @@ def dsa_plan_chunk(kv: PagedKV, lens_in, delta, free_pages, free_in, free_out, c
     if chunk.batch != kv.batch:
         raise ValueError(f"the chunk holds {chunk.batch} requests, the tables {kv.batch}")
     n, here = free_pages.numel(), _current()
-    i32 = lambda t, shape, what: _i32(t, shape, what, False, here)
     _check("dsa_plan_chunk", load().dsa_plan_chunk(
-        _desc(kv, here), i32(lens_in, rows, "lens_in"), i32(delta, rows, "delta"),
-        i32(free_pages, (n,), "free_pages"), n, i32(free_in, (1,), "free_in"),
-        i32(free_out, (1,), "free_out"), _desc(chunk, here), *_scratch(workspace, here),
-        _stream(stream)))
+        _desc(kv, here), _i32(lens_in, rows, "lens_in", False, here),
+        _i32(delta, rows, "delta", False, here), _i32(free_pages, (n,), "free_pages", False, here), n,
+        _i32(free_in, (1,), "free_in", False, here), _i32(free_out, (1,), "free_out", False, here),
+        _desc(chunk, here), *_scratch(workspace, here),
+        _stream_on(stream, here)))
 
 
 def _token_rows(t, tokens: int, heads: int, what: str) -> int:
@@ -677,7 +684,7 @@ def dsa_append_chunk(kv: PagedKV, chunk: Chunk, k_new, v_new, rotary: Rotary | N
         _desc(kv, here), _desc(chunk, here), _on(k_new, here),
         _token_rows(k_new, n, kv.num_kv_heads, "k_new"), _on(v_new, here),
         _token_rows(v_new, n, kv.num_kv_heads, "v_new"), _desc(rotary, here), _on(q, here), qs,
-        _on(q_out, here), meta_kind, logical_page, _on(meta, here), _stream(stream)))
+        _on(q_out, here), meta_kind, logical_page, _on(meta, here), _stream_on(stream, here)))
 
 
 def dsa_chunk_attn_workspace_size(kv: PagedKV, tokens: int) -> int:
@@ -701,4 +708,4 @@ def dsa_chunk_attn(kv: PagedKV, chunk: Chunk, q, scale: float, out, m=None, l=No
             raise ValueError(f"{what} must be contiguous fp32 [{n}][{hq}]")
     _check("dsa_chunk_attn", load().dsa_chunk_attn(
         _desc(kv, here), _desc(chunk, here), _on(q, here), sink, local, scale, _on(out, here),
-        _on(m, here), _on(l, here), *_scratch(workspace, here), _stream(stream)))
+        _on(m, here), _on(l, here), *_scratch(workspace, here), _stream_on(stream, here)))

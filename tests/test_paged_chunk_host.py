@@ -405,7 +405,6 @@ def test_tensors_of_another_device_are_refused(lib, monkeypatch):
     import types
 
     from dynamic_block_sparse_gb300 import binding as B
-    monkeypatch.setattr(torch.cuda, "is_initialized", lambda: True)
     monkeypatch.setattr(B, "_device", lambda: 0)
     calls = []
     ran = types.SimpleNamespace(**{n: lambda *a, n=n: calls.append(n) or 0 for n in (
