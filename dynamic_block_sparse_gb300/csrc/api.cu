@@ -1047,6 +1047,10 @@ int dsa_plan_chunk(const dsa_paged_kv* kv, const int32_t* lens_in, const int32_t
     return fail(DSA_ERR_INVALID_ARG, "dsa_plan_chunk: NULL pointer");
   if (v.B > kPlanMaxBatch)
     return fail(DSA_ERR_UNSUPPORTED, "batch %d > %d", v.B, kPlanMaxBatch);
+  // (the kernel steps over both in 32 bits)
+  if (chunk->tokens > kPlanMaxAxis || free_capacity > kPlanMaxAxis)
+    return fail(DSA_ERR_UNSUPPORTED, "%d tokens or %d free pages > %d", chunk->tokens, free_capacity,
+                kPlanMaxAxis);
   if ((rc = check_positions(v))) return rc;
   if (static_cast<long long>(v.B) * v.max_pages >= (1LL << 31))
     return fail(DSA_ERR_UNSUPPORTED, "page table of %d x %d entries is too large", v.B, v.max_pages);

@@ -20,6 +20,8 @@ namespace {
 // 3.7 us, 256 requests with 10183 tokens 6.8 us, 2048 requests with 88325 tokens 11.1 us.
 constexpr int kPlanThreads = 512;
 constexpr int kPlanWarps = kPlanThreads / 32;
+constexpr int kPlanCtas = 152;
+static_assert(2 * kPlanThreads * kPlanCtas <= 0x7fffffff - kPlanMaxAxis, "indexes count in 32 bits");
 
 DSA_DEV int clamp_i32(long long v) {
   return static_cast<int>(v < 0x7fffffffLL ? v : 0x7fffffffLL);
@@ -520,7 +522,7 @@ cudaError_t launch_plan_chunk(const PlanArgs& a, cudaStream_t s) {
   cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(plan_chunk_kernel), bytes);
   if (e != cudaSuccess) return e;
   int grid = (a.tokens + kPlanThreads - 1) / kPlanThreads;  // a token a thread, up to a CTA per SM
-  grid = grid < 1 ? 1 : grid > 152 ? 152 : grid;
+  grid = grid < 1 ? 1 : grid > kPlanCtas ? kPlanCtas : grid;
   return launch_pdl(plan_chunk_kernel, grid, kPlanThreads, bytes, s, a);
 }
 

@@ -224,6 +224,7 @@ cudaError_t launch_calib(const float* traj, int T, int rows, int n, int stride, 
 
 // Page plan of a chunk of new tokens (chunk.cu).
 constexpr int kPlanMaxBatch = 8192;  // requests whose prefix sums one CTA keeps in shared memory
+constexpr int kPlanMaxAxis = 0x7fffffff - (1 << 20);  // tokens, free pages: a grid's step fits behind
 struct PlanArgs {
   int B, p, max_pages, num_phys;
   int32_t* page_table;

@@ -540,7 +540,8 @@ typedef struct dsa_chunk {
  * The metadata of the page that now ends a shortened request still covers the dropped tokens (a
  * looser bound, a mean with them) until tokens are appended to it.
  * What is written may overlap neither each other nor what is read, but for the two pairs above.
- * batch <= 8192; p * max_pages_per_seq <= 2^31 - 1024.
+ * batch <= 8192; p * max_pages_per_seq <= 2^31 - 1024; chunk->tokens and free_capacity below
+ * 2^31 - 2^20.
  */
 int dsa_plan_chunk(const dsa_paged_kv* kv, const int32_t* lens_in, const int32_t* delta,
                    int32_t* free_pages, int32_t free_capacity, const int32_t* free_in,

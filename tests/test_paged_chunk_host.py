@@ -504,3 +504,14 @@ def test_a_cache_of_strided_or_other_tensors_is_refused(lib, monkeypatch):
         B.dsa_chunk_attn(kv, chunk, z(6, 4, 128, t=bf), 0.1, z(6, 4, 128, t=bf), workspace=ws,
                          stream=stream)
     assert len(ran) == 3
+
+
+def test_plan_refuses_axes_beyond_its_indexes(lib):
+    """The plan's indexes run a grid's step past the token axis and the stack: both stay below 2^31 by
+    that."""
+    def call(tokens, cap):
+        return lib.dsa_plan_chunk(ctypes.byref(_kv()), 4096, 4096, 4096, cap, 4096, 4096,
+                                  ctypes.byref(_chunk(tokens)), 8192, 0, None)
+    most = (1 << 31) - 1 - (1 << 20)
+    assert call(most + 1, 16) == -3 and call(16, most + 1) == -3 and call((1 << 31) - 1, 16) == -3
+    assert call(most, most) == -5  # (these pass on to the workspace's check)
