@@ -819,3 +819,107 @@ def test_prefill_without_windows_attends_every_head(name):
     for x in got[1:]:
         for a, b in zip(x, got[0]):
             assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("name", ["threshold", "prr"])
+def test_prefill_then_decode_through_the_other_decoders(name):
+    """Prompts in two chunks, a rollback and single tokens through the prefill of the PSA and PRR
+    decoders, each followed by a decode step whose budget covers every page: metadata equals a fresh
+    build bit for bit, and the step the rows that the chunk call gave the last tokens."""
+    from dynamic_block_sparse_gb300.pipeline import Cache, Chunk, PRRDecoder, ThresholdDecoder
+    torch.manual_seed(4)
+    hq, hkv, p = 8, 2, 64
+    k = torch.zeros(40, hkv, p, 128, dtype=torch.bfloat16, device="cuda")
+    cache = Cache(k, k.clone(), torch.full((2, 12), -1, dtype=I32, device="cuda"),
+                  torch.zeros(2, dtype=I32, device="cuda"), hq)
+    if name == "threshold":
+        dec, kind = ThresholdDecoder(cache, tau=1.0, cap=12), B.DSA_META_MEAN
+    else:
+        dec, kind = PRRDecoder(cache, 12, 12, 0.3, 0.2, 0.5), B.DSA_META_MINMAX
+    chunk = Chunk(cache, 500, free_pages=torch.randperm(40, device="cuda").to(I32))
+    rot = B.rotary(B.rotary_phases([10000.0 ** (-i / 64) for i in range(64)]), 128)
+    lens = [0, 0]
+    for delta in ([300, 200], [77, 1], [-100, -200], [1, 60], [1, 1]):
+        chunk.plan(_t(delta))
+        lens = [max(0, a + d) for a, d in zip(lens, delta)]
+        if min(delta) < 0:
+            continue
+        qkv = torch.randn(500, hq + 2 * hkv, 128, device="cuda").bfloat16()
+        out, m, l = dec.prefill(chunk, qkv[:, :hq], qkv[:, hq:hq + hkv], qkv[:, hq + hkv:], rotary=rot)
+        torch.cuda.synchronize()
+        assert int(cache.status) == 0 and cache.seq_lens.tolist() == lens
+        fresh = torch.zeros_like(dec.meta)
+        B.dsa_build_page_meta(cache.kv, kind, p, fresh)
+        for b in range(2):
+            for j in range(ceil_div(lens[b], p)):
+                ph = int(cache.page_table[b, j])
+                assert torch.equal(dec.meta[ph].view(torch.uint8), fresh[ph].view(torch.uint8))
+        last = [delta[0] - 1, sum(delta) - 1]
+        o2, m2, l2 = dec.step(chunk.q[last].contiguous())
+        torch.cuda.synchronize()
+        assert int(cache.status) == 0
+        # both round every probability and this one the result (2^-8 of itself each); values of a few
+        # standard deviations bound the weighted sum of |v| by 4.5
+        assert ((out[last].float() - o2).abs() <= 2.0 ** -8 * o2.abs() + 2.0 ** -7 * 4.5).all()
+        assert (m[last] - m2).abs().max() <= 1e-4
+
+
+def test_captured_append_keeps_metadata():
+    """Plan and append with both kinds of metadata captured once and replayed for other lengths: the
+    records of every page that holds a token equal a fresh build's bit for bit."""
+    from dynamic_block_sparse_gb300.pipeline import Cache, Chunk
+    torch.manual_seed(1)
+    hkv, p, T = 2, 32, 120
+    k = torch.zeros(40, hkv, p, 128, dtype=torch.bfloat16, device="cuda")
+    cache = Cache(k, k.clone(), torch.full((3, 10), -1, dtype=I32, device="cuda"),
+                  torch.zeros(3, dtype=I32, device="cuda"), 4)
+    chunk = Chunk(cache, T, free_pages=torch.arange(40, dtype=I32, device="cuda"))
+    metas = [(kind, lp, cache.meta_buffer(kind, lp)) for kind, lp in (
+        (B.DSA_META_MINMAX, 16), (B.DSA_META_MEAN, 32))]
+    kn, vn = (torch.zeros(T, hkv, 128, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    delta = torch.zeros(3, dtype=I32, device="cuda")
+    s = torch.cuda.Stream()
+
+    def step():
+        chunk.plan(delta)
+        chunk.append(kn, vn, metas)
+
+    with torch.cuda.stream(s):
+        step()  # attributes are set outside the capture
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        step()
+    for d in ([40, 0, 50], [1, 1, 1], [30, 66, 0], [-20, 1, 1], [1, -100, 90], [5, 33, 2]):
+        delta.copy_(_t(d))
+        for x in (kn, vn):
+            x.copy_(torch.randn(x.shape, device="cuda").bfloat16())
+        graph.replay()
+        torch.cuda.synchronize()
+        assert int(cache.status) == 0
+        for kind, lp, meta in metas:
+            fresh = torch.zeros_like(meta)
+            B.dsa_build_page_meta(cache.kv, kind, lp, fresh)
+            for b in range(3):
+                # (a page that a rollback shortened keeps its records until it gets a token)
+                if d[b] > 0:
+                    for j in range(ceil_div(int(cache.seq_lens[b]), p)):
+                        ph = int(cache.page_table[b, j])
+                        assert torch.equal(meta[ph].view(torch.uint8), fresh[ph].view(torch.uint8))
+
+
+def test_rotary_with_a_strided_axis_list():
+    """Axes given as a view turn as their dense copy does."""
+    c = ChunkCase([(0, 40)], 16, 2, 1, seed=14)
+    axis = (torch.arange(128, device="cuda") % 3).to(torch.uint8)[::2]
+    pos = torch.randint(0, 1000, (3, 40), device="cuda").to(I32)
+    phase = B.rotary_phases([10000.0 ** (-i / 64) for i in range(64)])
+    got = []
+    for a in (axis, axis.contiguous()):
+        kv = B.paged_kv(c.k, c.v, c.table, c.lens, 2, None, c.status)
+        chunk = B.chunk(c.start, c.count, _t([0] * 40), _t(list(range(40))))
+        out = torch.empty_like(c.q)
+        B.dsa_append_chunk(kv, chunk, c.q[:, :1], c.q[:, 1:], B.rotary(phase, 128, a, pos), c.q, out)
+        got.append(out)
+    torch.cuda.synchronize()
+    assert int(c.status) == 0 and torch.equal(*got)

@@ -515,3 +515,19 @@ def test_plan_refuses_axes_beyond_its_indexes(lib):
     most = (1 << 31) - 1 - (1 << 20)
     assert call(most + 1, 16) == -3 and call(16, most + 1) == -3 and call((1 << 31) - 1, 16) == -3
     assert call(most, most) == -5  # (these pass on to the workspace's check)
+
+
+def test_plan_reference_takes_and_refuses():
+    """The random steps above reach both outcomes."""
+    seen = set()
+    for seed in range(20):
+        r = random.Random(seed)
+        p, B, width, phys = 16, r.randint(1, 9), r.randint(2, 12), r.randint(6, 60)
+        table = np.full((B, width), -7, dtype=np.int64)
+        lens, free = [0] * B, list(range(phys))
+        for _ in range(30):
+            delta = [r.choice([0, 1, r.randint(1, p * 3), -r.randint(1, 40)]) for _ in range(B)]
+            got = plan_reference(table, lens, delta, free, p, tokens=200)
+            table, lens, free = got["table"], got["lens"], got["stack"]
+            seen.add(got["refused"])
+    assert seen == {True, False}
