@@ -211,14 +211,16 @@ __global__ void __launch_bounds__(kPlanThreads) plan_chunk_kernel(const PlanArgs
 // bytes, and the first rows are on their way while the sines are worked out.
 // What bounds it is DRAM behind a chain (row, position, page, sines, rows, metadata) some 4 us long that
 // the CTAs of an SM overlap.  Measured on a GB300, launches replayed in a graph: one token for each of 4
-// requests, 32 + 8 heads, 4.3 us; 8398 tokens of 32 + 8 heads, three axes, min/max metadata, 39 us, 5.3
-// TB/s, 0.80 of a measured copy; 3967 tokens of 32 + 32 heads, mean metadata, 40 us, 5.0 TB/s, 0.74.
+// requests, 32 + 8 heads, 4.3 us; 8398 tokens of 32 + 8 heads, three axes, min/max metadata, 39.5 us, 5.3
+// TB/s, 0.79 of a measured copy; 3967 tokens of 32 + 32 heads, mean metadata, 40.5 us, 4.9 TB/s, 0.74.
 constexpr int kAppThreads = 256;
 constexpr int kAppTokens = 16;
 constexpr int kAppRows = 4;
 // Heads share a CTA (keys) or a warp (queries) and with it the sines, but a short chunk needs the CTAs:
 // below kAppCtas of them heads are split (4 decode tokens 4.3 us, 7.5 with all heads together), and
-// below kAppWarps query warps query heads (one token of 64 heads: 3.8 and 6.4 us).
+// below kAppWarps query warps query heads (one token of 64 heads: 3.8 and 6.4 us).  Four CTAs run on an
+// SM, at 64 registers with three words spilled; three, with none, take 43.9 and 41.6 us for the two long
+// cases above.
 constexpr int kAppCtas = 3 * 152, kAppWarps = 32 * 152;
 
 // ---- cosine and sine of a fraction of a turn (64-bit fixed point), to the last bit of fp32 but for

@@ -4,7 +4,10 @@
 // Mathematics: one pass over the key tiles of a query tile with the running reference maximum and sum
 // of the softmax per row (logits in log2 units).  The reference only moves when a row's maximum has
 // grown by more than 2^8 (kLazyLog2), so the accumulator is rarely rescaled; the true maximum is kept
-// beside it for the m output.
+// beside it for the m output.  Everything is fp32 but P, which is rounded to bf16: both operands of a
+// tcgen05 product have one type, and V is bf16.  The outputs' relative error against 64 bits is 2.3e-3
+// with it (root mean square), 1.7e-3 from the rounding of the output alone; a second product with the low
+// half of P would win that back for half as many products again.
 //
 // Query tiles: a KV head's G query heads share its keys, so a tile's 128 rows are (token, head) pairs
 // of 128 / G tokens, and a CTA works on two streams of 128 rows at once, each with its own softmax
@@ -33,10 +36,11 @@
 // cache's bytes, behind ~8 us in which the CTA starts, plans and gets its first tile.  In between, where
 // a CTA has some tens of tiles, the records and merges of cut items (each 10 to 15 us at the end).
 // Measured on a GB300, launches replayed in a graph: one prompt of 8191 tokens, 32 heads of their own,
-// 357 us, 1.54 PFLOP/s, 0.81 of a measured bf16 product; 2048 tokens after 30K, 32 heads on 8, 675 us,
-// 1.55 PFLOP/s (the power cap holds it there); one token of 4 requests of 32K, 100 us, 5.3 TB/s, 0.79 of
-// a measured copy; one token of 8 requests on 8 streaming heads (64 + 256 tokens), 15 us; two prompts of
-// about 5000 tokens, 32 heads on 8, window 1000, 184 us, 0.93 PFLOP/s of visible pairs.
+// 353 us, 1.56 PFLOP/s, 0.82 of a measured bf16 product; 2048 tokens after 30K, 32 heads on 8, 652 us,
+// 1.61 PFLOP/s (the power cap takes it to 701 us in calls back to back for a second); one token of 4
+// requests of 32K, 99 us, 5.3 TB/s, 0.80 of a measured copy; one token of 8 requests on 8 streaming heads
+// (64 + 256 tokens), 15 us; two prompts of about 5000 tokens, 32 heads on 8, window 1000, 185 us, 0.93
+// PFLOP/s of visible pairs.
 #include "common.cuh"
 #include "internal.h"
 
