@@ -257,13 +257,15 @@ def paged_kv(k_pages, v_pages, page_table, seq_lens, num_q_heads: int,
     kv.page_size = page
     kv.max_pages_per_seq = page_table.shape[1]
     kv.num_phys_pages = P
-    kv.where = _where(k_pages, v_pages, page_table, seq_lens, head_is_streaming, status)
-    kv.fault = None  # why the calls that write the cache refuse it
+    kv.where = k_pages.get_device()
+    kv.fault = None  # why the chunk calls refuse it
     named = dict(k_pages=k_pages, v_pages=v_pages, page_table=page_table, seq_lens=seq_lens,
                  head_is_streaming=head_is_streaming, status=status)
     for what, t in named.items():
         if t is not None and not t.is_contiguous():
             kv.fault = f"{what} must be contiguous"
+        if t is not None and t.get_device() != kv.where:
+            kv.fault = f"{what} must be on the current CUDA device, beside k_pages"
     if v_pages.dtype != torch.bfloat16:
         kv.fault = f"v_pages must be bf16, got {v_pages.dtype}"
     if tuple(seq_lens.shape) != (kv.batch,):

@@ -141,8 +141,8 @@ class Chunk:
         """Starts a step: ``delta[b]`` new tokens for request b (or -n: its last n tokens dropped),
         with pages from the stack.  Advances the cache's lengths and page table and fills the chunk; a
         request that does not fit gets ``count[b] = 0`` and raises DSA_STATUS_NO_PAGES.  What a decoder
-        keeps from its steps about the pages (a reused selection) is renewed by its ``prefill``; a
-        caller that appends without it selects anew before the next step."""
+        keeps from its steps about the pages (a reused selection, a predictor's state) is renewed by its
+        ``prefill``; a caller that appends without it has to see to that before the next step."""
         c = self.cache
         if self.free_pages is None:
             raise ValueError("this chunk has no stack of free pages to plan with")

@@ -445,6 +445,12 @@ def test_tensors_of_another_device_are_refused(lib, monkeypatch):
                 run(call, (name,))
         assert len(calls) == 1, call
         calls.clear()
+    for at in range(4):  # the cache's tensors are on one device, or it is refused
+        ts = [_OnDevice(x, 1 if i == at else 0) for i, x in enumerate((
+            torch.zeros(4, 2, 16, 128, dtype=bf), torch.zeros(4, 2, 16, 128, dtype=bf), i32(2, 3), i32(2)))]
+        with pytest.raises(ValueError, match="current CUDA device"):
+            B.dsa_chunk_attn(B.paged_kv(*ts, 4), B.chunk(_OnDevice(i32(3), 0), _OnDevice(i32(2), 0), tokens=T),
+                             _OnDevice(rows(4), 0), 0.1, _OnDevice(rows(4), 0), stream=stream)
     with pytest.raises(ValueError, match="one device"):
         B.chunk(_OnDevice(i32(3), 0), _OnDevice(i32(2), 1), tokens=4)
 
