@@ -37,7 +37,7 @@
 // a CTA has some tens of tiles, the records and merges of cut items (each 10 to 15 us at the end).
 // Measured on a GB300, launches replayed in a graph: one prompt of 8191 tokens, 32 heads of their own,
 // 353 us, 1.56 PFLOP/s, 0.82 of a measured bf16 product; 2048 tokens after 30K, 32 heads on 8, 652 us,
-// 1.61 PFLOP/s (the power cap takes it to 701 us in calls back to back for a second); one token of 4
+// 1.61 PFLOP/s (the power cap takes it to 701 to 735 us in calls back to back); one token of 4
 // requests of 32K, 99 us, 5.3 TB/s, 0.80 of a measured copy; one token of 8 requests on 8 streaming heads
 // (64 + 256 tokens), 15 us; two prompts of about 5000 tokens, 32 heads on 8, window 1000, 185 us, 0.93
 // PFLOP/s of visible pairs.
